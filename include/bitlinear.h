@@ -510,6 +510,176 @@ int bitlinear_backward_dw(const int8_t *Xq, int64_t ldq, const float *beta, int6
  */
 const char *bitlinear_backward_kernel(int64_t M, int64_t N, int64_t K, int which);
 
+/*
+ * ---- Around the BitLinears of a decoder layer -------------------------------
+ * RMS norm with the residual's addition and int8 output, a key / value cache in
+ * int8, and the attention that reads it.  Activations are 8-bit (LIT-380
+ * record, Key takeaways, bullet 1); here the norm that feeds a BitLinear writes
+ * them, and the cache keeps keys and values in the same per-row absmax form.
+ */
+
+/*
+ * Residual addition, RMS norm and per-token int8 quantisation, in binary32:
+ *   h_mk    = x_mk + r_mk             (r absent: h = x),
+ *   rho_m   = 1 / sqrt(mean_k h_mk^2 + eps)  (sum in binary64, rounded once;
+ *             0 where mean + eps = 0),
+ *   y_mk    = (h_mk * rho_m) * w_k    (w absent: 1),
+ *   beta_m, q_mk = the activation quantiser of y (bitlinear_quantize_act).
+ * The norm takes the binary32 h; H is h rounded once to h_dtype.
+ *   X      [M x K], x_dtype F32 or BF16, row stride ldx >= K.
+ *   R      residual [M x K] of h_dtype, row stride ldr >= K, or NULL.
+ *   w      fp32 [K], or NULL.
+ *   eps    >= 0, finite.
+ *   H      [M x K], h_dtype F32 or BF16, row stride ldh >= K, or NULL (h is not
+ *          kept).  May be R itself, or X itself (same address, type and
+ *          stride): the residual stream updated in place.
+ *   Xq     q_dtype BITLINEAR_I8: int8 rows, stride ldq >= K, ldq % 16 == 0;
+ *          bytes K .. ldq-1 are written with 0.  q_dtype BITLINEAR_I8_TILED:
+ *          bitlinear_act_tiled_bytes(M, K, layout) bytes in the tiled
+ *          activation layout of 'layout' (ldq ignored; K <= 65536, else
+ *          UNSUPPORTED).  16-byte aligned.  Both feed bitlinear_forward.
+ *   beta   fp32 [M].
+ * X, R, H and w need only the alignment of their elements.  Nothing else may
+ * overlap.  'layout' is ignored for BITLINEAR_I8.
+ */
+int bitlinear_norm_quantize(const void *X, int x_dtype, int64_t M, int64_t K, int64_t ldx, const void *R, int64_t ldr,
+                            const float *w, float eps, void *H, int h_dtype, int64_t ldh, void *Xq, int q_dtype,
+                            int64_t ldq, int layout, float *beta, void *stream);
+
+/*
+ * The values int8 rows stand for: V_mk = q_mk * (beta_m / 127), both operations
+ * in binary32, rounded once to v_dtype (the Xhat of the backward pass).
+ *   Xq   int8 rows [M x K], stride ldq >= K; beta fp32 [M].
+ *   V    [M x K], v_dtype F32 or BF16, row stride ldv >= K.
+ */
+int bitlinear_dequantize_act(const int8_t *Xq, int64_t ldq, const float *beta, int64_t M, int64_t K, void *V,
+                             int v_dtype, int64_t ldv, void *stream);
+
+/* Workspace bytes bitlinear_norm_backward needs (-1 if invalid): fp32 partial
+ * sums of dW, one row of K per workgroup; 0 for dw = 0 (no dW). */
+int64_t bitlinear_norm_backward_workspace_bytes(int64_t M, int64_t K, int dw);
+
+/*
+ * Gradient of the norm under the straight-through estimator (the quantiser's
+ * derivative is 1).  With h the values held in H, rho_m as above (from H) and
+ * g = w * dY:
+ *   dX_mk = rho_m g_mk - h_mk (rho_m^3 / K) sum_j g_mj h_mj + dH_mk,
+ *   dW_k  = sum_m dY_mk h_mk rho_m,
+ * in binary32 (the sum of squares and sum_j in binary64).  dX is the gradient
+ * of both x and r.
+ *   dY   fp32 [M x K], row stride lddy >= K (bitlinear_backward_dx's output).
+ *   H    [M x K], h_dtype F32 or BF16, row stride ldh >= K.
+ *   w    fp32 [K] or NULL (ones).
+ *   dH   gradient arriving through the residual stream, [M x K] of h_dtype, row
+ *        stride lddh >= K, or NULL.
+ *   dX   [M x K] of h_dtype, row stride lddx >= K; may be dH itself.
+ *   dW   fp32 [K] (written, not accumulated), or NULL.
+ *   ws   >= bitlinear_norm_backward_workspace_bytes(M, K, dW != NULL) bytes,
+ *        16-byte aligned.
+ * Deterministic: the partial sums of dW are added in a fixed order.
+ */
+int bitlinear_norm_backward(const float *dY, int64_t lddy, const void *H, int h_dtype, int64_t ldh, const float *w,
+                            float eps, const void *dH, int64_t lddh, int64_t M, int64_t K, void *dX, int64_t lddx,
+                            float *dW, void *ws, int64_t ws_bytes, void *stream);
+
+/*
+ * A paged cache of keys and values in int8, with one binary32 scale per token
+ * and head: a value is byte * scale, with scale = max|x| / 127 over the token's
+ * head_dim values and byte = rint(x * (127 / max|x|)) as in the activation
+ * quantiser.  A page holds page_tokens tokens (a multiple of 64) of every head;
+ * slot = page * page_tokens + t names a place.  With Dp = head_dim rounded up to
+ * 16:
+ *   K        int8: byte ((page * heads + head) * page_tokens + t) * Dp + d.
+ *   V        int8, transposed in blocks of 64 tokens: byte
+ *            ((page * heads + head) * page_tokens + 64 * (t / 64)) * Dp + 64 * d
+ *            + 16 * ((t % 16) / 4) + 8 * ((t % 64) / 32) + 4 * ((t % 32) / 16)
+ *            + t % 4, so that 16 bytes are one lane's keys of two matrix-core
+ *            operands.
+ *   K_scale, V_scale  fp32: element (page * heads + head) * page_tokens + t.
+ * K and V are bitlinear_cache_bytes bytes each, 16-byte aligned; the scales
+ * have pages * heads * page_tokens elements each.  Bytes d >= head_dim are
+ * written with 0 along with a token.  A fresh cache needs no initial contents.
+ */
+typedef struct {
+    int8_t *K;
+    float *K_scale;
+    int8_t *V;
+    float *V_scale;
+    int64_t pages, page_tokens, heads, head_dim;
+} bitlinear_cache_t;
+
+#define BITLINEAR_MAX_HEAD_DIM 256
+
+/* Bytes of K (and of V): pages * heads * page_tokens * Dp, or -1 for sizes
+ * outside: pages, heads >= 1, page_tokens a multiple of 64 up to 2^20,
+ * head_dim in [1, 256], heads <= 4096, pages * page_tokens <= 2^36. */
+int64_t bitlinear_cache_bytes(int64_t pages, int64_t page_tokens, int64_t heads, int64_t head_dim);
+
+/*
+ * Quantise the keys and values of new tokens into their slots.
+ *   K, V   [tokens x heads x head_dim], dtype F32 or BF16, a head's values
+ *          contiguous; ld*_token and ld*_head are strides in elements (>= 0).
+ *   slots  int64 [tokens] (device).  A slot outside [0, pages * page_tokens) is
+ *          skipped.  Two tokens with the same slot race.
+ * tokens in [0, 2^24]; 0 does nothing.
+ */
+int bitlinear_cache_write(const bitlinear_cache_t *cache, const void *K, int64_t ldk_token, int64_t ldk_head,
+                          const void *V, int64_t ldv_token, int64_t ldv_head, int dtype, int64_t tokens,
+                          const int64_t *slots, void *stream);
+
+/*
+ * Read slots back: K, V [tokens x heads x head_dim] of dtype F32 or BF16 (the
+ * binary32 product byte * scale, rounded once).  A slot outside the cache gives
+ * zeros.  The strides keep (token, head) rows apart: one of them must be at
+ * least the other's whole extent.
+ */
+int bitlinear_cache_read(const bitlinear_cache_t *cache, const int64_t *slots, int64_t tokens, void *K,
+                         int64_t ldk_token, int64_t ldk_head, void *V, int64_t ldv_token, int64_t ldv_head, int dtype,
+                         void *stream);
+
+/*
+ * Attention of a batch of sequences that share a prefix, over the int8 cache.
+ * Query token i (0-based) of sequence b, with n_b query tokens, sees the
+ * prefix_len keys of the shared prefix and the sequence's own keys
+ * 0 .. own_len[b] - n_b + i: its own keys are in the cache already (one query
+ * token: the whole own length).  Per query head j (kv head j / (heads /
+ * cache->heads)):
+ *   s = scale * <q, key>,  p = softmax(s),  o = sum p * value.
+ * Scores and outputs are accumulated in binary32, softmax statistics are
+ * binary32.  The prefix's keys are read once for all sequences.  A query that
+ * sees no key gives o = 0 and lse = -inf.
+ *   Q       [tokens x heads x head_dim], dtype F32 or BF16, head rows
+ *           contiguous, strides in elements (>= 0).  BF16 rounds the softmax
+ *           weights to 11 significant bits; F32 carries 22.
+ *   q_start int32 [seqs + 1] (device): tokens q_start[b] .. q_start[b+1]-1
+ *           belong to sequence b; or NULL: max_q tokens each, tokens = seqs *
+ *           max_q.  Counts are cut at max_q; tokens of no sequence keep their
+ *           O.
+ *   own_pages int32 [seqs x ld_pages] (device): page of own token t is entry
+ *           t / page_tokens; entries past the length are not read, and a page
+ *           outside [0, pages) counts as not visible.
+ *   own_len int32 [seqs] (device), cut to [0, max_own].
+ *   max_own  host bound of own_len, ld_pages >= ceil(max_own / page_tokens).
+ *   prefix_pages int32 [ceil(prefix_len / page_tokens)] (device); prefix_len 0:
+ *           no prefix (prefix_pages may be NULL).
+ *   scale   finite.
+ *   O       [tokens x heads x head_dim] of dtype, strides as for
+ *           bitlinear_cache_read.
+ *   lse     fp32 [tokens x heads]: log(sum exp(s)), or NULL.
+ *   ws      >= bitlinear_attention_workspace_bytes(...) bytes, 16-byte aligned.
+ * heads is a multiple of cache->heads, at most 4096; tokens and seqs in
+ * [1, 2^20], max_q in [1, 2^20] with seqs * max_q at most 2^28, prefix_len and
+ * max_own in [0, 2^30].
+ */
+int64_t bitlinear_attention_workspace_bytes(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim,
+                                            int64_t seqs, int64_t max_q, int64_t max_own, int64_t prefix_len);
+
+int bitlinear_attention(const bitlinear_cache_t *cache, const void *Q, int dtype, int64_t tokens, int64_t heads,
+                        int64_t ldq_token, int64_t ldq_head, int64_t seqs, const int32_t *q_start, int64_t max_q,
+                        const int32_t *own_pages, int64_t ld_pages, const int32_t *own_len, int64_t max_own,
+                        const int32_t *prefix_pages, int64_t prefix_len, float scale, void *O, int64_t ldo_token,
+                        int64_t ldo_head, float *lse, void *ws, int64_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

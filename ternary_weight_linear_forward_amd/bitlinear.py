@@ -64,6 +64,17 @@ class Job(ctypes.Structure):
                 ("ldy", ctypes.c_int64)]
 
 
+class Cache(ctypes.Structure):
+    """bitlinear_cache_t: the int8 key / value cache (device pointers)."""
+    _fields_ = [("K", ctypes.c_void_p), ("K_scale", ctypes.c_void_p), ("V", ctypes.c_void_p),
+                ("V_scale", ctypes.c_void_p), ("pages", ctypes.c_int64), ("page_tokens", ctypes.c_int64),
+                ("heads", ctypes.c_int64), ("head_dim", ctypes.c_int64)]
+
+
+MAX_HEAD_DIM = 256
+_CACHE = ctypes.POINTER(Cache)
+_F32 = ctypes.c_float
+
 MAX_GROUP = 32
 _JOBS = ctypes.POINTER(Job)
 
@@ -101,6 +112,18 @@ _SIGNATURES = {
     "bitlinear_forward_ex": (
         [_P, _INT, _P, _I64, _I64, _I64, _P, _INT, _I64, _P, _P, _INT, _I64, _P, _I64, _P, _P, _I64, _INT, _P],
         _INT),
+    "bitlinear_norm_quantize": ([_P, _INT, _I64, _I64, _I64, _P, _I64, _P, _F32, _P, _INT, _I64, _P, _INT, _I64, _INT,
+                                 _P, _P], _INT),
+    "bitlinear_dequantize_act": ([_P, _I64, _P, _I64, _I64, _P, _INT, _I64, _P], _INT),
+    "bitlinear_norm_backward_workspace_bytes": ([_I64, _I64, _INT], _I64),
+    "bitlinear_norm_backward": ([_P, _I64, _P, _INT, _I64, _P, _F32, _P, _I64, _I64, _I64, _P, _I64, _P, _P, _I64, _P],
+                                _INT),
+    "bitlinear_cache_bytes": ([_I64, _I64, _I64, _I64], _I64),
+    "bitlinear_cache_write": ([_CACHE, _P, _I64, _I64, _P, _I64, _I64, _INT, _I64, _P, _P], _INT),
+    "bitlinear_cache_read": ([_CACHE, _P, _I64, _P, _I64, _I64, _P, _I64, _I64, _INT, _P], _INT),
+    "bitlinear_attention_workspace_bytes": ([_I64] * 8, _I64),
+    "bitlinear_attention": ([_CACHE, _P, _INT, _I64, _I64, _I64, _I64, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64,
+                             _F32, _P, _I64, _I64, _P, _P, _I64, _P], _INT),
 }
 EXPORTED = tuple(_SIGNATURES)
 
@@ -259,6 +282,53 @@ def bitlinear_forward_grouped_algo(jobs, njobs: int, layout: int, x_dtype: int, 
 def bitlinear_grouped_kernel_algo(jobs, njobs: int, layout: int, x_dtype: int, algo: int):
     r = _lib.bitlinear_grouped_kernel_algo(jobs, njobs, layout, x_dtype, algo)
     return None if r is None else r.decode()
+
+
+def bitlinear_norm_quantize(X, x_dtype, M, K, ldx, R, ldr, w, eps, H, h_dtype, ldh, Xq, q_dtype, ldq, layout, beta,
+                            stream) -> int:
+    return _lib.bitlinear_norm_quantize(X, x_dtype, M, K, ldx, R, ldr, w, eps, H, h_dtype, ldh, Xq, q_dtype, ldq,
+                                        layout, beta, stream)
+
+
+def bitlinear_dequantize_act(Xq, ldq, beta, M, K, V, v_dtype, ldv, stream) -> int:
+    return _lib.bitlinear_dequantize_act(Xq, ldq, beta, M, K, V, v_dtype, ldv, stream)
+
+
+def bitlinear_norm_backward_workspace_bytes(M: int, K: int, dw: int) -> int:
+    return _lib.bitlinear_norm_backward_workspace_bytes(M, K, dw)
+
+
+def bitlinear_norm_backward(dY, lddy, H, h_dtype, ldh, w, eps, dH, lddh, M, K, dX, lddx, dW, ws, ws_bytes,
+                            stream) -> int:
+    return _lib.bitlinear_norm_backward(dY, lddy, H, h_dtype, ldh, w, eps, dH, lddh, M, K, dX, lddx, dW, ws, ws_bytes,
+                                        stream)
+
+
+def bitlinear_cache_bytes(pages: int, page_tokens: int, heads: int, head_dim: int) -> int:
+    return _lib.bitlinear_cache_bytes(pages, page_tokens, heads, head_dim)
+
+
+def bitlinear_cache_write(cache, K, ldk_token, ldk_head, V, ldv_token, ldv_head, dtype, tokens, slots, stream) -> int:
+    return _lib.bitlinear_cache_write(cache, K, ldk_token, ldk_head, V, ldv_token, ldv_head, dtype, tokens, slots,
+                                      stream)
+
+
+def bitlinear_cache_read(cache, slots, tokens, K, ldk_token, ldk_head, V, ldv_token, ldv_head, dtype, stream) -> int:
+    return _lib.bitlinear_cache_read(cache, slots, tokens, K, ldk_token, ldk_head, V, ldv_token, ldv_head, dtype,
+                                     stream)
+
+
+def bitlinear_attention_workspace_bytes(tokens, heads, kv_heads, head_dim, seqs, max_q, max_own, prefix_len) -> int:
+    return _lib.bitlinear_attention_workspace_bytes(tokens, heads, kv_heads, head_dim, seqs, max_q, max_own,
+                                                    prefix_len)
+
+
+def bitlinear_attention(cache, Q, dtype, tokens, heads, ldq_token, ldq_head, seqs, q_start, max_q, own_pages, ld_pages,
+                        own_len, max_own, prefix_pages, prefix_len, scale, O, ldo_token, ldo_head, lse, ws, ws_bytes,
+                        stream) -> int:
+    return _lib.bitlinear_attention(cache, Q, dtype, tokens, heads, ldq_token, ldq_head, seqs, q_start, max_q,
+                                    own_pages, ld_pages, own_len, max_own, prefix_pages, prefix_len, scale, O,
+                                    ldo_token, ldo_head, lse, ws, ws_bytes, stream)
 
 
 # --- torch-tensor helpers (allocation + marshalling) ------------------------
@@ -496,3 +566,215 @@ def backward_dw(Xq, beta, dY, K: int, out=None, stream=None):
     _check(bitlinear_backward_dw(_ptr(Xq), Xq.stride(0), _ptr(beta), M, N, K, _ptr(dY), dY.stride(0), _ptr(out),
                                  out.stride(0), _stream(stream)), "bitlinear_backward_dw")
     return out
+
+
+def _rows_contiguous(t, where: str, *dtypes) -> None:
+    """Refuses a tensor whose last dimension has gaps, or of another dtype."""
+    if (dtypes and t.dtype not in dtypes) or (t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise BitlinearError(ERR_INVALID_ARG, where)
+
+
+def norm_quantize(X, w=None, eps: float = 1e-5, residual=None, H=None, keep_h: bool = True, layout: int | None = None,
+                  stream=None):
+    """RMS norm of X + residual with int8 output (bitlinear_norm_quantize).
+    X [M x K] fp32/bf16 (cuda, rows may be strided), residual [M x K] or None,
+    w fp32 [K] or None.  Returns (H, Xq, beta): H = X + residual in the
+    residual's dtype (X's without one; written to 'H' if given, which may be
+    the residual; None with keep_h=False); Xq int8 [M x ldq], ldq = K rounded
+    up to 16, or with a weight layout the 1-d tiled activations forward takes."""
+    torch = _torch()
+    name = "norm_quantize"
+    M, K = X.shape
+    fl = (torch.float32, torch.bfloat16)
+    _rows_contiguous(X, name, *fl)
+    ref = X if residual is None else residual
+    _rows_contiguous(ref, name, *fl)
+    if ref.shape != X.shape or (w is not None and (w.shape != (K,) or w.dtype != torch.float32 or
+                                                   (K > 1 and w.stride(0) != 1))):
+        raise BitlinearError(ERR_INVALID_ARG, name)
+    if H is None and keep_h:
+        H = torch.empty((M, K), dtype=ref.dtype, device=X.device)
+    if H is not None:
+        _rows_contiguous(H, name, ref.dtype)
+        if H.shape != X.shape:
+            raise BitlinearError(ERR_INVALID_ARG, name)
+    if layout is None:
+        ldq = (K + 15) // 16 * 16
+        Xq = torch.empty((M, ldq), dtype=torch.int8, device=X.device)
+    else:
+        ldq, nbytes = 0, bitlinear_act_tiled_bytes(M, K, layout)
+        if nbytes < 0:
+            raise BitlinearError(ERR_INVALID_ARG, name)
+        Xq = torch.empty(nbytes, dtype=torch.int8, device=X.device)
+    beta = torch.empty(M, dtype=torch.float32, device=X.device)
+    _check(_lib.bitlinear_norm_quantize(
+        X.data_ptr(), _dtype_code(X), M, K, _ld(X), _ptr(residual), 0 if residual is None else _ld(residual), _ptr(w),
+        eps, _ptr(H), _dtype_code(ref), 0 if H is None else _ld(H), Xq.data_ptr(), I8 if layout is None else I8_TILED,
+        ldq, LAYOUT_I2 if layout is None else layout, beta.data_ptr(), _stream(stream)), "bitlinear_norm_quantize")
+    _record(stream, H, Xq, beta)
+    return H, Xq, beta
+
+
+def _record(stream, *tensors) -> None:
+    """Tensors allocated here and used on another stream than the current one
+    must not be handed out again before that stream is done with them."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
+def _ld(t) -> int:
+    """Row stride of a 2-d tensor (the row length where there is one row)."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def dequantize_act(Xq, beta, K: int, dtype=None, out=None, stream=None):
+    """The values of int8 rows Xq [M x >=K] with beta [M]: q * (beta / 127), fp32 or bf16 [M x K]."""
+    torch = _torch()
+    M = Xq.shape[0]
+    if out is None:
+        out = torch.empty((M, K), dtype=dtype or torch.float32, device=Xq.device)
+    _check(_lib.bitlinear_dequantize_act(Xq.data_ptr(), _ld(Xq), beta.data_ptr(), M, K, out.data_ptr(),
+                                         _dtype_code(out), _ld(out), _stream(stream)), "bitlinear_dequantize_act")
+    _record(stream, out)
+    return out
+
+
+def norm_backward(dY, H, w=None, eps: float = 1e-5, dH=None, dX=None, want_dw: bool = True, ws=None, stream=None):
+    """Gradient of the norm (bitlinear_norm_backward): dY fp32 [M x K], H the
+    norm's kept sum, dH the gradient arriving through the residual stream (H's
+    dtype, or None).  Returns (dX in H's dtype, dW fp32 [K] or None)."""
+    torch = _torch()
+    name = "norm_backward"
+    M, K = H.shape
+    _rows_contiguous(dY, name, torch.float32)
+    _rows_contiguous(H, name, torch.float32, torch.bfloat16)
+    if dX is None:
+        dX = torch.empty((M, K), dtype=H.dtype, device=H.device)
+    for t in (dH, dX):
+        if t is not None:
+            _rows_contiguous(t, name, H.dtype)
+    if any(t is not None and t.shape != H.shape for t in (dY, dH, dX)) or \
+            (w is not None and (w.shape != (K,) or w.dtype != torch.float32 or (K > 1 and w.stride(0) != 1))):
+        raise BitlinearError(ERR_INVALID_ARG, name)
+    dW = torch.empty(K, dtype=torch.float32, device=H.device) if want_dw else None
+    nws = _lib.bitlinear_norm_backward_workspace_bytes(M, K, 1 if want_dw else 0)
+    if nws < 0:
+        raise BitlinearError(ERR_INVALID_ARG, name)
+    if nws > 0 and (ws is None or ws.numel() < nws):
+        ws = torch.empty(nws, dtype=torch.uint8, device=H.device)
+    _check(_lib.bitlinear_norm_backward(
+        dY.data_ptr(), _ld(dY), H.data_ptr(), _dtype_code(H), _ld(H), _ptr(w), eps, _ptr(dH),
+        0 if dH is None else _ld(dH), M, K, dX.data_ptr(), _ld(dX), _ptr(dW), _ptr(ws) if nws > 0 else None, nws,
+        _stream(stream)), "bitlinear_norm_backward")
+    _record(stream, dX, dW, ws)
+    return dX, dW
+
+
+class KVCache:
+    """The tensors of an int8 key / value cache (bitlinear_cache_t): k int8
+    [pages, heads, page_tokens, Dp], v int8 [pages, heads, page_tokens / 64, Dp,
+    64], their scales fp32 [pages, heads, page_tokens]; Dp is head_dim rounded
+    up to 16.  KVCache.empty allocates one."""
+
+    def __init__(self, k, v, k_scale, v_scale, head_dim: int):
+        torch = _torch()
+        pages, heads, page_tokens, dp = k.shape
+        if v.shape != (pages, heads, page_tokens // 64, dp, 64) or page_tokens % 64 or \
+                dp != (head_dim + 15) // 16 * 16 or k_scale.shape != k.shape[:3] or v_scale.shape != k.shape[:3] or \
+                k.dtype != torch.int8 or v.dtype != torch.int8 or k_scale.dtype != torch.float32 or \
+                v_scale.dtype != torch.float32 or not (k.is_contiguous() and v.is_contiguous() and
+                                                       k_scale.is_contiguous() and v_scale.is_contiguous()):
+            raise BitlinearError(ERR_INVALID_ARG, "KVCache")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.pages, self.heads, self.page_tokens, self.head_dim = pages, heads, page_tokens, head_dim
+        self.desc = Cache(k.data_ptr(), k_scale.data_ptr(), v.data_ptr(), v_scale.data_ptr(), pages, page_tokens,
+                          heads, head_dim)
+
+    @classmethod
+    def empty(cls, pages: int, heads: int, head_dim: int, page_tokens: int = 64, device="cuda"):
+        torch = _torch()
+        if bitlinear_cache_bytes(pages, page_tokens, heads, head_dim) < 0:
+            raise BitlinearError(ERR_INVALID_ARG, "KVCache")
+        dp = (head_dim + 15) // 16 * 16
+        new = lambda *s, dtype: torch.empty(s, dtype=dtype, device=device)  # noqa: E731
+        return cls(new(pages, heads, page_tokens, dp, dtype=torch.int8),
+                   new(pages, heads, page_tokens // 64, dp, 64, dtype=torch.int8),
+                   new(pages, heads, page_tokens, dtype=torch.float32),
+                   new(pages, heads, page_tokens, dtype=torch.float32), head_dim)
+
+
+def _kv_rows(cache, t, tokens, where):
+    torch = _torch()
+    _rows_contiguous(t, where, torch.float32, torch.bfloat16)
+    if t.shape != (tokens, cache.heads, cache.head_dim):
+        raise BitlinearError(ERR_INVALID_ARG, where)
+
+
+def cache_write(cache: KVCache, K, V, slots, stream=None) -> None:
+    """Quantise K, V [tokens x heads x head_dim] (fp32/bf16) into the cache's
+    slots (int64 [tokens]; a slot outside the cache is skipped)."""
+    torch = _torch()
+    n = slots.numel()
+    _kv_rows(cache, K, n, "cache_write")
+    _kv_rows(cache, V, n, "cache_write")
+    if K.dtype != V.dtype or slots.dtype != torch.int64 or not slots.is_contiguous():
+        raise BitlinearError(ERR_INVALID_ARG, "cache_write")
+    _check(_lib.bitlinear_cache_write(cache.desc, K.data_ptr(), K.stride(0), K.stride(1), V.data_ptr(), V.stride(0),
+                                      V.stride(1), _dtype_code(K), n, slots.data_ptr(), _stream(stream)),
+           "bitlinear_cache_write")
+
+
+def cache_read(cache: KVCache, slots, dtype=None, stream=None):
+    """(K, V) [tokens x heads x head_dim] of the cache's slots (zeros for a slot outside it)."""
+    torch = _torch()
+    n = slots.numel()
+    if slots.dtype != torch.int64 or not slots.is_contiguous():
+        raise BitlinearError(ERR_INVALID_ARG, "cache_read")
+    K = torch.empty((n, cache.heads, cache.head_dim), dtype=dtype or torch.bfloat16, device=slots.device)
+    V = torch.empty_like(K)
+    _check(_lib.bitlinear_cache_read(cache.desc, slots.data_ptr(), n, K.data_ptr(), K.stride(0), K.stride(1),
+                                     V.data_ptr(), V.stride(0), V.stride(1), _dtype_code(K), _stream(stream)),
+           "bitlinear_cache_read")
+    _record(stream, K, V)
+    return K, V
+
+
+def attention(cache: KVCache, Q, own_pages, own_len, max_own: int, prefix_pages=None, prefix_len: int = 0, q_start=None,
+              max_q: int = 1, scale: float | None = None, out=None, return_lse: bool = False, ws=None, stream=None):
+    """Attention of sequences that share a prefix (bitlinear_attention).
+    Q [tokens x heads x head_dim] fp32/bf16; own_pages int32 [seqs x pages],
+    own_len int32 [seqs] (at most max_own); prefix_pages int32; q_start int32
+    [seqs + 1] or None (max_q tokens each); scale 1 / sqrt(head_dim) by
+    default.  Returns O (Q's shape and dtype), or (O, lse fp32 [tokens x heads])."""
+    torch = _torch()
+    name = "attention"
+    tokens, heads, D = Q.shape
+    seqs = own_len.numel()
+    _rows_contiguous(Q, name, torch.float32, torch.bfloat16)
+    if out is None:
+        out = torch.empty((tokens, heads, D), dtype=Q.dtype, device=Q.device)
+    _rows_contiguous(out, name, Q.dtype)
+    pt = cache.page_tokens
+    ints = [t for t in (own_pages, own_len, q_start, prefix_pages) if t is not None]
+    if D != cache.head_dim or out.shape != Q.shape or any(t.dtype != torch.int32 for t in ints) or \
+            own_pages.dim() != 2 or own_pages.shape[0] != seqs or own_pages.shape[1] * pt < max_own or \
+            (own_pages.shape[1] > 1 and own_pages.stride(1) != 1) or not own_len.is_contiguous() or \
+            (q_start is not None and (q_start.numel() != seqs + 1 or not q_start.is_contiguous())) or \
+            (prefix_len > 0 and (prefix_pages is None or prefix_pages.numel() * pt < prefix_len or
+                                 not prefix_pages.is_contiguous())):
+        raise BitlinearError(ERR_INVALID_ARG, name)
+    nws = _lib.bitlinear_attention_workspace_bytes(tokens, heads, cache.heads, D, seqs, max_q, max_own, prefix_len)
+    if nws < 0:
+        raise BitlinearError(ERR_INVALID_ARG, name)
+    if nws > 0 and (ws is None or ws.numel() < nws):
+        ws = torch.empty(nws, dtype=torch.uint8, device=Q.device)
+    lse = torch.empty((tokens, heads), dtype=torch.float32, device=Q.device) if return_lse else None
+    _check(_lib.bitlinear_attention(
+        cache.desc, Q.data_ptr(), _dtype_code(Q), tokens, heads, Q.stride(0), Q.stride(1), seqs, _ptr(q_start), max_q,
+        own_pages.data_ptr(), _ld(own_pages), own_len.data_ptr(), max_own, _ptr(prefix_pages), prefix_len,
+        D ** -0.5 if scale is None else scale, out.data_ptr(), out.stride(0), out.stride(1), _ptr(lse),
+        _ptr(ws) if nws > 0 else None, nws, _stream(stream)), "bitlinear_attention")
+    _record(stream, out, lse, ws)
+    return (out, lse) if return_lse else out

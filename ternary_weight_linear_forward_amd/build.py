@@ -21,7 +21,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libbitlinear.so")
-SOURCES = ["api.cpp", "weights.hip", "act.hip", "gemv.hip", "group.hip", "gemm.hip", "backward.hip"]
+SOURCES = ["api.cpp", "api_layer.cpp", "weights.hip", "act.hip", "gemv.hip", "group.hip", "gemm.hip", "backward.hip",
+           "norm.hip", "cache.hip", "attention.hip"]
 
 
 def hipcc() -> str:

@@ -164,6 +164,73 @@ hipError_t launch_bwd_dx(const uint8_t *P2, const float *gamma, int64_t M, int64
 hipError_t launch_bwd_dw(const int8_t *Xq, int64_t ldq, const float *beta, int64_t M, int64_t N, int64_t K,
                          const float *dY, int64_t lddy, float *dW, int64_t lddw, hipStream_t stream);
 
+// ---- around the BitLinears (norm.hip, cache.hip, attention.hip) ------------
+struct NormArgs {
+    const void *X;
+    int x_dtype;
+    int64_t M, K, ldx;
+    const void *R; // or null
+    int64_t ldr;
+    const float *w; // or null
+    float eps;
+    void *H; // or null
+    int h_dtype;
+    int64_t ldh;
+    int8_t *Xq;
+    int layout; // tiled activation layout, or -1: rows of ldq bytes
+    int64_t ldq;
+    float *beta;
+};
+hipError_t launch_norm_quantize(const NormArgs &a, hipStream_t stream);
+hipError_t launch_dequantize_act(const int8_t *Xq, int64_t ldq, const float *beta, int64_t M, int64_t K, void *V,
+                                 int v_dtype, int64_t ldv, hipStream_t stream);
+
+struct NormBwdArgs {
+    const float *dY;
+    const void *H;
+    int h_dtype;
+    const float *w; // or null
+    float eps;
+    const void *dH; // or null
+    void *dX;
+    int64_t M, K, lddy, ldh, lddh, lddx;
+    float *dW; // or null
+    float *part;
+};
+int64_t norm_bwd_parts(int64_t M, int64_t K); // rows of K partial sums of dW
+hipError_t launch_norm_backward(const NormBwdArgs &a, hipStream_t stream);
+
+// The int8 cache as kernels see it (Dp: head_dim rounded up to 16).
+struct CacheView {
+    int8_t *K, *V;
+    float *Ks, *Vs;
+    int64_t slots; // pages * page_tokens
+    int pages, page_tokens, heads, D, Dp;
+};
+struct CacheRows { // K and V rows outside the cache, strides in elements
+    void *K, *V;
+    int64_t ldk_t, ldk_h, ldv_t, ldv_h;
+};
+hipError_t launch_cache_write(const CacheView &c, const CacheRows &r, int dtype, int64_t tokens, const int64_t *slots,
+                              hipStream_t stream);
+hipError_t launch_cache_read(const CacheView &c, const CacheRows &r, int dtype, int64_t tokens, const int64_t *slots,
+                             hipStream_t stream);
+
+struct AttnArgs {
+    CacheView c;
+    const void *Q;
+    void *O;
+    float *lse; // or null
+    const int32_t *q_start, *own_pages, *own_len, *prefix_pages;
+    int64_t ldq_t, ldq_h, ldo_t, ldo_h, ld_pages;
+    int dtype, tokens, heads, seqs, max_q, max_own, prefix;
+    float scale;
+    float *ws;
+};
+int64_t attn_workspace_bytes(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t seqs,
+                             int64_t max_q, int64_t max_own, int64_t prefix);
+hipError_t launch_attention(const AttnArgs &a, hipStream_t stream);
+
 // Names (as profilers print them, without the argument list) of the kernel a
 // product launch runs for a shape.
 void gemv_kernel_name(int layout, int64_t M, int64_t N, int64_t K, bool tiled, char *buf, size_t n);
