@@ -596,8 +596,9 @@ int bitlinear_norm_backward(const float *dY, int64_t lddy, const void *H, int h_
  *            + t % 4, so that 16 bytes are one lane's keys of two matrix-core
  *            operands.
  *   K_scale, V_scale  fp32: element (page * heads + head) * page_tokens + t.
- * K and V are bitlinear_cache_bytes bytes each, 16-byte aligned; the scales
- * have pages * heads * page_tokens elements each.  Bytes d >= head_dim are
+ * K and V are bitlinear_cache_bytes bytes each; the scales, which are never
+ * negative, have pages * heads * page_tokens elements each.  All four are
+ * 16-byte aligned.  Bytes d >= head_dim are
  * written with 0 along with a token.  A fresh cache needs no initial contents.
  */
 typedef struct {
@@ -668,8 +669,8 @@ int bitlinear_cache_read(const bitlinear_cache_t *cache, const int64_t *slots, i
  *   lse     fp32 [tokens x heads]: log(sum exp(s)), or NULL.
  *   ws      >= bitlinear_attention_workspace_bytes(...) bytes, 16-byte aligned.
  * heads is a multiple of cache->heads, at most 4096; tokens and seqs in
- * [1, 2^20], max_q in [1, 2^20] with seqs * max_q at most 2^28, prefix_len and
- * max_own in [0, 2^30].
+ * [1, 2^20], max_q in [1, 2^20], tokens * heads and seqs * max_q * heads at most
+ * 2^28, prefix_len and max_own in [0, 2^30].
  */
 int64_t bitlinear_attention_workspace_bytes(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim,
                                             int64_t seqs, int64_t max_q, int64_t max_own, int64_t prefix_len);

@@ -45,7 +45,7 @@ int check_cache(const bitlinear_cache_t *c, bl::CacheView *v, CacheSpans *sp)
     if (!c || !c->K || !c->V || !c->K_scale || !c->V_scale) return BITLINEAR_ERR_INVALID_ARG;
     const int64_t bytes = bitlinear_cache_bytes(c->pages, c->page_tokens, c->heads, c->head_dim);
     if (bytes < 0) return BITLINEAR_ERR_INVALID_ARG;
-    if (!aligned16(c->K) || !aligned16(c->V) || !aligned_to(c->K_scale, 4) || !aligned_to(c->V_scale, 4))
+    if (!aligned16(c->K) || !aligned16(c->V) || !aligned16(c->K_scale) || !aligned16(c->V_scale))
         return BITLINEAR_ERR_INVALID_ARG;
     const int64_t n = c->pages * c->heads * c->page_tokens;
     sp->s[0] = span_of(c->K, 1, bytes, bytes, 1);
@@ -76,7 +76,8 @@ bool hits(const CacheSpans &c, Span s)
 }
 
 constexpr int64_t kMaxCacheTokens = int64_t(1) << 24; // of one write or read
-constexpr int64_t kMaxQueries = int64_t(1) << 20, kMaxKeys = int64_t(1) << 30, kMaxHeads = 4096;
+constexpr int64_t kMaxQueries = int64_t(1) << 20, kMaxKeys = int64_t(1) << 30, kMaxHeads = 4096,
+                  kMaxRows = int64_t(1) << 28; // (query, head) rows of one call
 
 bool attn_sizes_ok(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t seqs, int64_t max_q,
                    int64_t max_own, int64_t prefix_len)
@@ -84,7 +85,8 @@ bool attn_sizes_ok(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head
     return tokens >= 1 && tokens <= kMaxQueries && seqs >= 1 && seqs <= kMaxQueries && max_q >= 1 &&
            max_q <= kMaxQueries && kv_heads >= 1 && heads >= kv_heads && heads <= kMaxHeads && heads % kv_heads == 0 &&
            head_dim >= 1 && head_dim <= BITLINEAR_MAX_HEAD_DIM && max_own >= 0 && max_own <= kMaxKeys &&
-           prefix_len >= 0 && prefix_len <= kMaxKeys && seqs <= (int64_t(1) << 28) / max_q;
+           prefix_len >= 0 && prefix_len <= kMaxKeys && seqs * max_q <= kMaxRows / heads &&
+           tokens <= kMaxRows / heads;
 }
 
 } // namespace
