@@ -585,8 +585,9 @@ int bitlinear_norm_backward(const float *dY, int64_t lddy, const void *H, int h_
 /*
  * A paged cache of keys and values in int8, with one binary32 scale per token
  * and head: a value is byte * scale, with scale = max|x| / 127 over the token's
- * head_dim values and byte = rint(x * (127 / max|x|)) as in the activation
- * quantiser.  A page holds page_tokens tokens (a multiple of 64) of every head;
+ * head_dim values and byte = rint(x * (127 * (1 / max|x|))), ties to even, each
+ * operation rounded to binary32 (at a power-of-two scale of the row, so that tiny
+ * rows keep their bytes).  A page holds page_tokens tokens (a multiple of 64) of every head;
  * slot = page * page_tokens + t names a place.  With Dp = head_dim rounded up to
  * 16:
  *   K        int8: byte ((page * heads + head) * page_tokens + t) * Dp + d.
