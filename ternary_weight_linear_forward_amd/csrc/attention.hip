@@ -17,17 +17,18 @@
 //    down to 2^-24 of the row's size; fp32 queries are two binary16 terms (22
 //    bits).  Scores are then t = <q', k> * K_scale and softmax runs in base 2 on
 //    c t with c = scale log2(e) 2^-e per row.
-//  - weights p = 2^(c (t - m)) are multiplied by V_scale / ref * PSCALE, ref the
-//    running power of two above the largest V_scale seen, and rounded to
-//    binary16 (11 bits; with fp32 queries two terms, 22 bits).  m is raised only
-//    when a score passes it by more than SLACK (base 2), so products stay below
-//    2^16.  Weights too small for a full binary16 number (a softmax of more than
-//    2^21 from its largest to its smallest weight) are multiplied in further
-//    rounds, brought up by STEP each, into sums of their own: a branch that
-//    blocks without such weights do not take.  l sums the unrounded p.
+//  - weights p = 2^(c t - m) are multiplied by V_scale / ref * PSCALE, ref a
+//    power of two above the V_scales seen, and rounded to binary16 (11 bits; with
+//    fp32 queries two terms, 22 bits).  m is any reference, not the maximum: it
+//    starts as the first block's and is raised to a block's when a weight of that
+//    block overflows binary16, so most blocks form no maximum.  Weights too small
+//    for a full binary16 number (p below 2^-21 of the largest) are multiplied in
+//    further rounds, brought up by STEP each, into sums of their own: a branch
+//    that blocks without such weights do not take.  l sums the unrounded p.
 #include "cache_core.h"
 #include "common.h"
 #include "launch.h"
+#include "rows.h"
 
 namespace bl {
 
@@ -44,11 +45,11 @@ template <int NS>
 struct WeightRange;
 template <>
 struct WeightRange<1> {
-    static constexpr float PSCALE = 0x1p7f, SLACK = 8.0f, LEAST = 0x1p-14f, STEP = 0x1p29f;
+    static constexpr float PSCALE = 0x1p7f, LEAST = 0x1p-14f, STEP = 0x1p29f;
 };
 template <>
 struct WeightRange<2> { // the second term of 2^-3 still has a full 2^-24 of its own
-    static constexpr float PSCALE = 0x1p14f, SLACK = 1.0f, LEAST = 0x1p-3f, STEP = 0x1p18f;
+    static constexpr float PSCALE = 0x1p14f, LEAST = 0x1p-3f, STEP = 0x1p18f;
 };
 
 // Weights to NS binary16 terms.
@@ -63,23 +64,45 @@ __device__ __forceinline__ void split_weights(const float (&w)[8], h8 (&p)[NS])
     }
 }
 
-// The weights that 'up' brings into [LEAST, LEAST STEP) (up = STEP, STEP^2, ..
-// in turn); the others 0.  Whether smaller ones are left.
+// A weight's share of a round: brought up by 'up' = STEP, STEP^2, .. into [LEAST,
+// LEAST STEP), 0 in the other rounds; up = 1: the weights of at least LEAST.
+// more: smaller ones are left.
 template <int NS>
-__device__ __forceinline__ bool round_weights(const float (&w)[8], float up, h8 (&p)[NS])
+__device__ __forceinline__ float round_share(float w, float up, bool &more)
 {
     using WR = WeightRange<NS>;
-    float x[8];
-    bool more = false;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const float y = w[e] * up;
-        more = more || (y > 0.0f && y < WR::LEAST);
-        x[e] = y >= WR::LEAST && y < WR::LEAST * WR::STEP ? y : 0.0f;
-    }
-    split_weights<NS>(x, p);
-    return more;
+    const float y = w * up;
+    more = more || (y > 0.0f && y < WR::LEAST);
+    return y >= WR::LEAST && (up == 1.0f || y < WR::LEAST * WR::STEP) ? y : 0.0f;
 }
+
+// Largest and smallest of NT operands' first terms (NaN if one is NaN).
+template <int NT, int NS>
+__device__ __forceinline__ void weight_range(const h8 (&p)[NT][NS], float &big, float &small)
+{
+    h2 hi, lo;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        union {
+            h8 v;
+            h2 x[4];
+        } u;
+        u.v = p[t][0];
+        if (t == 0) {
+            hi = __builtin_elementwise_maximum(u.x[0], u.x[1]);
+            lo = __builtin_elementwise_minimum(u.x[0], u.x[1]);
+        } else {
+            hi = __builtin_elementwise_maximum(__builtin_elementwise_maximum(hi, u.x[0]), u.x[1]);
+            lo = __builtin_elementwise_minimum(__builtin_elementwise_minimum(lo, u.x[0]), u.x[1]);
+        }
+        hi = __builtin_elementwise_maximum(__builtin_elementwise_maximum(hi, u.x[2]), u.x[3]);
+        lo = __builtin_elementwise_minimum(__builtin_elementwise_minimum(lo, u.x[2]), u.x[3]);
+    }
+    big = static_cast<float>(__builtin_elementwise_maximum(hi[0], hi[1]));
+    small = static_cast<float>(__builtin_elementwise_minimum(lo[0], lo[1]));
+}
+constexpr float H_MAX = 65504.0f;   // largest binary16
+constexpr float SUM_MAX = 0x1p100f; // a block's sum of p beyond which the reference is raised
 
 __device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
 
@@ -124,39 +147,41 @@ __device__ __forceinline__ float pow2_above(float v)
     return __uint_as_float(min(max(e, 16u), 253u) << 23);
 }
 
-// One part's rows and keys, the same for a whole workgroup.
+// One part's rows and keys, the same for a whole workgroup.  The keys are a list
+// of blocks of 64: nbp blocks of the prefix (0: none of them in this part's list),
+// then blocks of the sequence's own keys.
 struct AttnJob {
-    int kvh, row0, rows, tok0, n; // rows of the tile, first token, query tokens (own part)
-    int own;                      // own length, or -1: prefix
-    int blk0, blk1;               // blocks of 64 keys
+    int kvh, row0, rows, tok0, n; // head, rows of the tile, first token, query tokens
+    int nbp, prefix, own;         // prefix blocks and keys, own keys
+    int blk0, blk1;               // this part's blocks
     int part;
-    const int32_t *pages;
-    int keys; // all keys of the list
+    const int32_t *prefix_pages, *own_pages;
 };
 
-__device__ __forceinline__ bool attn_job(const AttnArgs &a, const AttnPlan &pl, int tile_rows_p, int tile_rows_o,
-                                         int wg, AttnJob &j)
+__device__ __forceinline__ bool attn_job(const AttnArgs &a, const AttnPlan &pl, int tile_rows, int wg, AttnJob &j)
 {
-    const int G = a.heads / a.c.heads;
+    const int G = a.heads / a.c.heads, nbp = (a.prefix + CACHE_BLOCK - 1) / CACHE_BLOCK;
+    j.prefix_pages = a.prefix_pages;
+    j.prefix = a.prefix;
     if (wg < pl.wgs_prefix) {
-        // consecutive workgroups go to different XCDs: kv heads and splits first, so
-        // that the row tiles of one piece of the cache are 8 apart or on one XCD
+        // the rows of every sequence against a piece of the prefix; consecutive workgroups
+        // take other heads and pieces, so that the row tiles of one piece lie on one XCD
         const int per = a.c.heads * pl.splits_prefix;
         const int tile = wg / per, r = wg % per;
         j.kvh = r % a.c.heads;
-        const int s = r / a.c.heads;
-        j.own = -1;
-        j.n = a.tokens;
+        j.part = r / a.c.heads;
         j.tok0 = 0;
-        j.row0 = tile * tile_rows_p;
-        j.rows = min(tile_rows_p, a.tokens * G - j.row0);
-        j.blk0 = s * pl.chunk_prefix;
-        j.keys = a.prefix;
-        j.blk1 = min(j.blk0 + pl.chunk_prefix, (a.prefix + CACHE_BLOCK - 1) / CACHE_BLOCK);
-        j.part = s;
-        j.pages = a.prefix_pages;
+        j.n = a.tokens;
+        j.row0 = tile * tile_rows;
+        j.rows = min(tile_rows, a.tokens * G - j.row0);
+        j.nbp = nbp;
+        j.own = 0;
+        j.own_pages = nullptr;
+        j.blk0 = j.part * pl.chunk_prefix;
+        j.blk1 = min(j.blk0 + pl.chunk_prefix, nbp);
         return true;
     }
+    // a sequence's rows against its own keys, after the prefix's where the plan joins them
     int r = wg - pl.wgs_prefix;
     j.kvh = r % a.c.heads;
     r /= a.c.heads;
@@ -171,24 +196,23 @@ __device__ __forceinline__ bool attn_job(const AttnArgs &a, const AttnPlan &pl, 
     }
     j.tok0 = first;
     j.n = n;
-    j.row0 = tile * tile_rows_o;
-    j.rows = min(tile_rows_o, n * G - j.row0);
+    j.row0 = tile * tile_rows;
+    j.rows = min(tile_rows, n * G - j.row0);
     if (j.rows <= 0) return false;
+    j.nbp = pl.joint ? nbp : 0;
     j.own = min(max(a.own_len[b], 0), a.max_own);
     const int last = attn_own_limit(j.own, n, (j.row0 + j.rows - 1) / G); // the tile's furthest key
-    j.keys = j.own;
     j.blk0 = s * pl.chunk_own;
-    j.blk1 = min(j.blk0 + pl.chunk_own, (last + CACHE_BLOCK - 1) / CACHE_BLOCK);
+    j.blk1 = min(j.blk0 + pl.chunk_own, j.nbp + (last + CACHE_BLOCK - 1) / CACHE_BLOCK);
     j.part = pl.splits_prefix + s;
-    j.pages = a.own_pages + b * a.ld_pages;
+    j.own_pages = a.own_pages + b * a.ld_pages;
     return true;
 }
 
-// Keys row rho (of the tile) sees; 0 past the tile's rows.
+// Own keys row rho (of the tile) sees; 0 past the tile's rows.
 __device__ __forceinline__ int row_limit(const AttnJob &j, int G, int rho)
 {
-    if (rho >= j.rows) return 0;
-    return j.own < 0 ? j.keys : attn_own_limit(j.own, j.n, (j.row0 + rho) / G);
+    return rho < j.rows ? attn_own_limit(j.own, j.n, (j.row0 + rho) / G) : 0;
 }
 
 // Workspace: o of every (part, token, head) [Dp], then (m, l) of every one.
@@ -197,12 +221,72 @@ __device__ __forceinline__ int64_t part_index(const AttnArgs &a, int part, int64
     return (static_cast<int64_t>(part) * a.tokens + tok) * a.heads + head;
 }
 
-// The page of block blk (bpp blocks a page), or -1 where it lies outside the cache.
-__device__ __forceinline__ int page_of(const AttnArgs &a, const AttnJob &j, int blk, int bpp)
+// Walks a job's blocks: the page of the block (-1 where it lies outside the
+// cache) and the block's first row in the page's head.
+struct PageWalk {
+    const int32_t *pages;
+    int blk, pi, po, bpp; // block, page list entry, block in the page, blocks a page
+    bool own;
+    __device__ __forceinline__ PageWalk(const AttnArgs &a, const AttnJob &j, int b) : bpp(a.c.page_tokens / CACHE_BLOCK)
+    {
+        blk = b;
+        own = b >= j.nbp;
+        pages = own ? j.own_pages : j.prefix_pages;
+        enter(own ? b - j.nbp : b);
+    }
+    __device__ __forceinline__ void enter(int rel)
+    {
+        pi = rel / bpp;
+        po = rel - pi * bpp;
+    }
+    __device__ __forceinline__ void step(const AttnJob &j, int n)
+    {
+        blk += n;
+        if (!own && blk >= j.nbp) {
+            own = true;
+            pages = j.own_pages;
+            enter(blk - j.nbp);
+        } else {
+            for (po += n; po >= bpp; po -= bpp) ++pi;
+        }
+    }
+    __device__ __forceinline__ int page(const AttnArgs &a) const
+    {
+        const int p = pages[pi];
+        return p >= 0 && p < a.c.pages ? p : -1;
+    }
+    __device__ __forceinline__ int64_t row(const AttnArgs &a, int page, int kvh) const
+    {
+        return cache_row0(a.c, page < 0 ? 0 : page, kvh) + po * CACHE_BLOCK;
+    }
+};
+
+// Four columns of a row's result: o / l, rounded once to the output's type.
+template <int DT>
+__device__ __forceinline__ void store_result(const AttnArgs &a, int64_t tok, int head, int col, f4 v)
 {
-    const int p = j.pages[blk / bpp];
-    return p >= 0 && p < a.c.pages ? p : -1;
+    const int64_t at = tok * a.ldo_t + head * a.ldo_h + col;
+    if (col + 4 <= a.c.D) {
+        if constexpr (DT == DT_F32) {
+            typedef float f4_any __attribute__((ext_vector_type(4), aligned(4)));
+            *reinterpret_cast<f4_any *>(static_cast<float *>(a.O) + at) = v;
+        } else {
+            const uint32_t lo = float_to_bf16_rne(v[0]) | static_cast<uint32_t>(float_to_bf16_rne(v[1])) << 16,
+                           hi = float_to_bf16_rne(v[2]) | static_cast<uint32_t>(float_to_bf16_rne(v[3])) << 16;
+            *reinterpret_cast<u2_any *>(static_cast<uint16_t *>(a.O) + at) = u2_any{lo, hi};
+        }
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (col + e < a.c.D) {
+            if constexpr (DT == DT_F32) static_cast<float *>(a.O)[at + e] = v[e];
+            else static_cast<uint16_t *>(a.O)[at + e] = float_to_bf16_rne(v[e]);
+        }
 }
+
+// log(sum e^s) from a base-2 reference and sum.
+__device__ __forceinline__ float lse_of(float m, float l) { return l > 0.0f ? (m + log2f(l)) * ATTN_LN2 : neg_inf(); }
 
 // A row's power of two: 2^e with max|q| 2^e in [2^13, 2^14); 1 for a zero row.
 __device__ __forceinline__ int row_exponent(float top)
@@ -220,10 +304,45 @@ __device__ __forceinline__ float row_factor(float scale, int e2)
     return scale != 0.0f ? fmaxf(ldexpf(fabsf(scale) * ATTN_LOG2E, -e2), 1.17549435e-38f) : 1.0f;
 }
 
-template <int DT>
-__device__ __forceinline__ float load_q(const AttnArgs &a, int64_t row_off, int d)
+// NV times eight query values of a row, the n-th at column col(n), zeros past
+// head_dim.  With head_dim a multiple of 8 the loads are unconditional (a column
+// past the row reads its start), so that they go out together.
+template <int DT, int NV, class Col>
+__device__ __forceinline__ void load_queries(const AttnArgs &a, int64_t off, const Col &col, float (&v)[NV][8])
 {
-    return d < a.c.D ? load_x<DT>(a.Q, row_off + d) : 0.0f;
+    if (a.c.D % 8 == 0) {
+#pragma unroll
+        for (int n = 0; n < NV; ++n) load8<DT>(a.Q, off + (col(n) < a.c.D ? col(n) : 0), 8, v[n]);
+#pragma unroll
+        for (int n = 0; n < NV; ++n)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[n][e] = col(n) < a.c.D ? v[n][e] : 0.0f;
+    } else {
+#pragma unroll
+        for (int n = 0; n < NV; ++n) load8<DT>(a.Q, off + col(n), a.c.D - col(n), v[n]);
+    }
+}
+
+// Eight query values times 2^e2 and the sign of scale as NS binary16 terms.
+template <int NS>
+__device__ __forceinline__ void query_terms(const float (&v)[8], int e2, float scale, h8 (&q)[NS])
+{
+    const float sgn = scale < 0.0f ? -1.0f : (scale > 0.0f ? 1.0f : 0.0f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float x = ldexpf(v[e], e2) * sgn;
+        const _Float16 hi = static_cast<_Float16>(x);
+        q[0][e] = hi;
+        if constexpr (NS == 2) q[1][e] = static_cast<_Float16>(x - static_cast<float>(hi));
+    }
+}
+
+__device__ __forceinline__ float max_abs8(const float (&v)[8])
+{
+    float t = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) t = fmaxf(t, fabsf(v[e]));
+    return t;
 }
 
 // ---------------------------------------------------------------------------
@@ -242,38 +361,28 @@ __global__ __launch_bounds__(256, DC == 4 ? 1 : 2) void k_attn_stream(const Attn
     constexpr int NS = DT == DT_F32 ? 2 : 1; // binary16 terms of queries and weights
     using WR = WeightRange<NS>;
     constexpr int DTILES = 4 * DC, DPAD = 64 * DC;
-    // [4 waves][16 rows][DPAD] sums, then [4][16] m, l
-    __shared__ __attribute__((aligned(16))) float lds[4 * 16 * (DPAD + 2)];
+    // [4 waves][16 rows][DPAD] sums, then [4][16] m, [4][16] l, [16] l of all
+    __shared__ __attribute__((aligned(16))) float lds[4 * 16 * (DPAD + 2) + 16];
     AttnJob j;
-    if (!attn_job(a, pl, 16, 16, blockIdx.x + pl.wg0, j)) return;
+    if (!attn_job(a, pl, 16, blockIdx.x + pl.wg0, j)) return;
     const int G = a.heads / a.c.heads, lane = lane_id(), wave = wave_id(), i = lane & 15, g = lane >> 4;
-    const int Dp = a.c.Dp, bpp = a.c.page_tokens / CACHE_BLOCK;
+    const int Dp = a.c.Dp;
 
-    h8 q[NS][DC][2]; // term, 64-column chunk, k-step
+    h8 q[DC][2][NS]; // 64-column chunk, k-step, term
     float c;
     {
         const int rr = i < j.rows ? j.row0 + i : j.row0;
         const int64_t off = (j.tok0 + static_cast<int64_t>(rr / G)) * a.ldq_t + (j.kvh * G + rr % G) * a.ldq_h;
-        float v[DC][16], top = 0.0f;
+        float v[2 * DC][8], top = 0.0f;
+        load_queries<DT>(a, off, [&](int n) { return 64 * (n / 2) + 16 * g + 8 * (n % 2); }, v);
 #pragma unroll
-        for (int cc = 0; cc < DC; ++cc)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                v[cc][e] = load_q<DT>(a, off, 64 * cc + 16 * g + e);
-                top = fmaxf(top, fabsf(v[cc][e]));
-            }
+        for (int n = 0; n < 2 * DC; ++n) top = fmaxf(top, max_abs8(v[n]));
         top = max_across32(max_across16(top));
         const int e2 = row_exponent(top);
-        const float sgn = a.scale < 0.0f ? -1.0f : (a.scale > 0.0f ? 1.0f : 0.0f);
 #pragma unroll
         for (int cc = 0; cc < DC; ++cc)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const float x = ldexpf(v[cc][e], e2) * sgn;
-                const _Float16 hi = static_cast<_Float16>(x);
-                q[0][cc][e / 8][e % 8] = hi;
-                if constexpr (NS == 2) q[1][cc][e / 8][e % 8] = static_cast<_Float16>(x - static_cast<float>(hi));
-            }
+            for (int h = 0; h < 2; ++h) query_terms<NS>(v[2 * cc + h], e2, a.scale, q[cc][h]);
         c = row_factor(a.scale, e2);
     }
     // below the smallest limit of the tile's rows no key is masked
@@ -286,7 +395,9 @@ __global__ __launch_bounds__(256, DC == 4 ? 1 : 2) void k_attn_stream(const Attn
     f4 o[DTILES];
 #pragma unroll
     for (int d = 0; d < DTILES; ++d) o[d] = f4{0.0f, 0.0f, 0.0f, 0.0f};
-    float m = neg_inf(), l = 0.0f, ref = 0.0f;
+    // m: the row's reference in base 2 (0 until it is set), ref: of the V_scales
+    float m = 0.0f, l = 0.0f, ref = 0.0f, vscale = 0.0f;
+    bool set = false;
     u4 kb[4][DC], vb[DTILES];
     f4 ks[4], vs[4];
     // byte offsets of this lane inside a block (columns past Dp read column 0: the queries hold zeros there)
@@ -295,37 +406,39 @@ __global__ __launch_bounds__(256, DC == 4 ? 1 : 2) void k_attn_stream(const Attn
     for (int cc = 0; cc < DC; ++cc) koff[cc] = i * Dp + (64 * cc + 16 * g < Dp ? 64 * cc + 16 * g : 0);
 #pragma unroll
     for (int d = 0; d < DTILES; ++d) voff[d] = (16 * d < Dp ? 16 * d + i : i) * CACHE_BLOCK + 16 * g;
-    auto row_of = [&](int page, int blk) {
-        return cache_row0(a.c, page < 0 ? 0 : page, j.kvh) + blk % bpp * CACHE_BLOCK;
-    };
     auto load_k = [&](int64_t row) {
         const int8_t *p = a.c.K + row * Dp;
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int cc = 0; cc < DC; ++cc) kb[t][cc] = *reinterpret_cast<const u4 *>(p + 16 * t * Dp + koff[cc]);
+    };
+    auto load_v = [&](int64_t row) { // and the scales
+        const int8_t *p = a.c.V + row * Dp;
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             ks[t] = *reinterpret_cast<const f4 *>(a.c.Ks + row + 16 * t + 4 * g);
             vs[t] = *reinterpret_cast<const f4 *>(a.c.Vs + row + 16 * t + 4 * g);
         }
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int cc = 0; cc < DC; ++cc) kb[t][cc] = *reinterpret_cast<const u4 *>(p + 16 * t * Dp + koff[cc]);
-    };
-    auto load_v = [&](int64_t row) {
-        const int8_t *p = a.c.V + row * Dp;
-#pragma unroll
         for (int d = 0; d < DTILES; ++d) vb[d] = *reinterpret_cast<const u4 *>(p + voff[d]);
     };
     int blk = j.blk0 + wave;
-    int page = blk < j.blk1 ? page_of(a, j, blk, bpp) : -1;
+    PageWalk walk(a, j, blk);
+    int page = -1, npage = -1;
     if (blk < j.blk1) {
-        const int64_t row = row_of(page, blk);
+        page = walk.page(a);
+        const int64_t row = walk.row(a, page, j.kvh);
         load_k(row);
         load_v(row);
+        walk.step(j, 4);
+        if (blk + 4 < j.blk1) npage = walk.page(a);
     }
     for (; blk < j.blk1; blk += 4) {
-        const int next = blk + 4;
-        const int npage = next < j.blk1 ? page_of(a, j, next, bpp) : -1;
-        const int k0 = blk * CACHE_BLOCK;
+        // this block's list: its first key, the keys there are, those this row sees
+        const bool pre = blk < j.nbp;
+        const int k0 = (pre ? blk : blk - j.nbp) * CACHE_BLOCK;
+        const int all = page < 0 ? 0 : (pre ? j.prefix : j.own), mine = page < 0 ? 0 : (pre ? j.prefix : lim);
         f4 s[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
@@ -336,96 +449,114 @@ __global__ __launch_bounds__(256, DC == 4 ? 1 : 2) void k_attn_stream(const Attn
                 for (int h = 0; h < 2; ++h) {
                     const h8 kf = bytes_to_h8(kb[t][cc][2 * h], kb[t][cc][2 * h + 1]);
 #pragma unroll
-                    for (int z = 0; z < NS; ++z) s[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, q[z][cc][h], s[t], 0, 0, 0);
+                    for (int z = 0; z < NS; ++z) s[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, q[cc][h][z], s[t], 0, 0, 0);
                 }
         }
-        f4 vf[4];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            s[t] *= ks[t];
-            vf[t] = vs[t];
-        }
-        if (page < 0 || k0 + CACHE_BLOCK > lim_min) {
-            const int all = page < 0 ? 0 : j.keys, mine = page < 0 ? 0 : lim;
+        for (int t = 0; t < 4; ++t) s[t] *= ks[t] * c;
+        const bool masked = page < 0 || k0 + CACHE_BLOCK > (pre ? j.prefix : lim_min);
+        if (masked) {
 #pragma unroll
             for (int t = 0; t < 4; ++t)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int key = k0 + 16 * t + 4 * g + r;
                     s[t][r] = key < mine ? s[t][r] : neg_inf();
-                    vf[t][r] = key < all ? vf[t][r] : 0.0f;
+                    vs[t][r] = key < all ? vs[t][r] : 0.0f;
                 }
         }
-        // the next block's keys and scales, while this block's weights are formed
-        const int64_t nrow = row_of(npage, next);
-        if (next < j.blk1) load_k(nrow);
-        float vtop = 0.0f, top = neg_inf();
+        // the next block's keys, while this block's weights are formed
+        const bool next = blk + 4 < j.blk1;
+        const int64_t nrow = walk.row(a, npage, j.kvh);
+        if (next) load_k(nrow);
+        h8 p[2][NS];
+        float sum = 0.0f, big, small;
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            vtop = fmaxf(fmaxf(fmaxf(vtop, vf[t][0]), fmaxf(vf[t][1], vf[t][2])), vf[t][3]);
-            top = fmaxf(fmaxf(fmaxf(top, s[t][0]), fmaxf(s[t][1], s[t][2])), s[t][3]);
+        for (int h = 0; h < 2; ++h) {
+            float w[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float x = __builtin_amdgcn_exp2f(s[2 * h + e / 4][e % 4] - m);
+                sum += x;
+                w[e] = x * (vs[2 * h + e / 4][e % 4] * vscale);
+            }
+            split_weights<NS>(w, p[h]);
         }
-        vtop = max_across32(max_across16(vtop));
-        top = max_across32(max_across16(top));
-        // (m = -inf: any finite score raises it)
-        const bool raise = top > neg_inf() && !((top - m) * c <= WR::SLACK);
-        if (vtop > ref || __any(raise)) { // (vtop is the same in every lane)
-            const float m2 = raise ? fmaxf(m, top) : m;
-            float f = raise ? __builtin_amdgcn_exp2f((m - m2) * c) : 1.0f;
-            m = m2;
+        weight_range(p, big, small);
+        if (masked) { // (masked weights are 0 and call for no round)
+            small = WR::LEAST;
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                small = s[e / 4][e % 4] > neg_inf() ? fminf(small, static_cast<float>(p[e / 8][0][e % 8])) : small;
+        }
+        if (__any((!set && k0 < mine) || ref == 0.0f || !(big <= H_MAX) || !(sum <= SUM_MAX) || small < WR::LEAST)) {
+            // the general form: references brought to this block's largest, small weights in rounds
+            float vtop = 0.0f, top = neg_inf();
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                vtop = fmaxf(fmaxf(fmaxf(vtop, vs[t][0]), fmaxf(vs[t][1], vs[t][2])), vs[t][3]);
+                top = fmaxf(fmaxf(fmaxf(top, s[t][0]), fmaxf(s[t][1], s[t][2])), s[t][3]);
+            }
+            vtop = max_across32(max_across16(vtop));
+            top = max_across32(max_across16(top));
+            const bool raise = top > neg_inf() && (!set || top > m);
+            float f = raise && set ? __builtin_amdgcn_exp2f(m - top) : 1.0f;
+            m = raise ? top : m;
+            set = set || raise;
             l *= f;
             if (vtop > ref) {
                 const float ref2 = pow2_above(vtop);
                 f *= ref / ref2;
                 ref = ref2;
+                vscale = WR::PSCALE / ref;
             }
 #pragma unroll
             for (int d = 0; d < DTILES; ++d) o[d] *= f;
-        }
-        const float mc = m > neg_inf() ? m * c : 0.0f, vscale = ref > 0.0f ? WR::PSCALE / ref : 0.0f;
-        float w[2][8], least = WR::LEAST;
+            sum = 0.0f;
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+            for (int t = 0; t < 4; ++t)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][r], c, -mc));
-                l += p;
-                w[t / 2][4 * (t % 2) + r] = p * (vf[t][r] * vscale);
-                least = fminf(least, w[t / 2][4 * (t % 2) + r]);
-            }
-        if (__any(least < WR::LEAST)) {
-            // weights below LEAST: rounds of their own, each brought up by STEP
-            float up = WR::STEP, down = 1.0f / WR::STEP;
-            for (bool more = true; more; up *= WR::STEP, down *= 1.0f / WR::STEP) {
-                h8 p[2][NS];
+                for (int r = 0; r < 4; ++r) {
+                    s[t][r] = __builtin_amdgcn_exp2f(s[t][r] - m);
+                    sum += s[t][r];
+                    s[t][r] *= vs[t][r] * vscale;
+                }
+            auto share = [&](float up, bool &more) {
                 more = false;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) more = round_weights<NS>(w[h], up, p[h]) || more;
-                more = __any(more);
+                for (int h = 0; h < 2; ++h) {
+                    float w[8];
 #pragma unroll
-                for (int d = 0; d < DTILES; ++d) {
-                    f4 x = f4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        // (opaque: else the conversions of all tiles are shared with the product below and kept)
-                        uint32_t v0 = vb[d][2 * h], v1 = vb[d][2 * h + 1];
-                        asm("" : "+v"(v0), "+v"(v1));
-                        const h8 vv = bytes_to_h8(v0, v1);
-#pragma unroll
-                        for (int z = 0; z < NS; ++z) x = __builtin_amdgcn_mfma_f32_16x16x32_f16(vv, p[h][z], x, 0, 0, 0);
-                    }
-                    o[d] += x * down;
-                    __builtin_amdgcn_sched_barrier(0); // one tile's registers at a time
+                    for (int e = 0; e < 8; ++e) w[e] = round_share<NS>(s[2 * h + e / 4][e % 4], up, more);
+                    split_weights<NS>(w, p[h]);
                 }
+                more = __any(more);
+            };
+            bool more;
+            share(1.0f, more);
+            if (more) {
+                for (float up = WR::STEP, down = 1.0f / WR::STEP; more; up *= WR::STEP, down *= 1.0f / WR::STEP) {
+                    share(up, more);
+#pragma unroll
+                    for (int d = 0; d < DTILES; ++d) {
+                        f4 x = f4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            // (opaque: else the conversions of all tiles are shared with the product below and kept)
+                            uint32_t v0 = vb[d][2 * h], v1 = vb[d][2 * h + 1];
+                            asm volatile("" : "+v"(v0), "+v"(v1));
+                            const h8 vv = bytes_to_h8(v0, v1);
+#pragma unroll
+                            for (int z = 0; z < NS; ++z) x = __builtin_amdgcn_mfma_f32_16x16x32_f16(vv, p[h][z], x, 0, 0, 0);
+                        }
+                        o[d] += x * down;
+                        __builtin_amdgcn_sched_barrier(0); // one tile's registers at a time
+                    }
+                }
+                share(1.0f, more);
             }
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) w[h][e] = w[h][e] >= WR::LEAST ? w[h][e] : 0.0f;
         }
-        h8 p[2][NS];
-        split_weights<NS>(w[0], p[0]);
-        split_weights<NS>(w[1], p[1]);
+        l += sum;
 #pragma unroll
         for (int d = 0; d < DTILES; ++d)
 #pragma unroll
@@ -434,15 +565,19 @@ __global__ __launch_bounds__(256, DC == 4 ? 1 : 2) void k_attn_stream(const Attn
 #pragma unroll
                 for (int z = 0; z < NS; ++z) o[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vv, p[h][z], o[d], 0, 0, 0);
             }
-        if (next < j.blk1) load_v(nrow);
         page = npage;
+        if (next) {
+            load_v(nrow);
+            walk.step(j, 4);
+            npage = blk + 8 < j.blk1 ? walk.page(a) : -1;
+        }
     }
 
     // add the waves: largest m of each row, every wave's sums brought to it
     float *ml = lds + 4 * 16 * DPAD;
     l += __shfl_xor(l, 16);
     l += __shfl_xor(l, 32);
-    m = m > neg_inf() ? m * c : neg_inf();
+    m = set ? m : neg_inf();
     if (g == 0) {
         ml[wave * 16 + i] = m;
         ml[64 + wave * 16 + i] = l;
@@ -460,22 +595,35 @@ __global__ __launch_bounds__(256, DC == 4 ? 1 : 2) void k_attn_stream(const Attn
     __syncthreads();
     f4 *po = reinterpret_cast<f4 *>(a.ws);
     float2 *pml = reinterpret_cast<float2 *>(a.ws + pl.ml_off);
+    float *sums = ml + 128; // l of the rows, and m
+    if (threadIdx.x < 16) {
+        float top = neg_inf(), sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) top = fmaxf(top, ml[w * 16 + threadIdx.x]);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const float mw = ml[w * 16 + threadIdx.x];
+            if (mw > neg_inf()) sum += ml[64 + w * 16 + threadIdx.x] * __builtin_amdgcn_exp2f(mw - top);
+        }
+        sums[threadIdx.x] = sum;
+        const int rr = j.row0 + static_cast<int>(threadIdx.x);
+        if (static_cast<int>(threadIdx.x) < j.rows) {
+            const int64_t tok = j.tok0 + rr / G;
+            const int head = j.kvh * G + rr % G;
+            if (!pl.direct) pml[part_index(a, j.part, tok, head)] = make_float2(top, sum);
+            else if (a.lse) a.lse[tok * a.heads + head] = lse_of(top, sum);
+        }
+    }
+    if (pl.direct) __syncthreads();
     for (int e = threadIdx.x; e < j.rows * (Dp / 4); e += 256) {
         const int rho = e / (Dp / 4), d4 = e % (Dp / 4), rr = j.row0 + rho;
         f4 sum = f4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int w = 0; w < 4; ++w) sum += *reinterpret_cast<const f4 *>(lds + (w * 16 + rho) * DPAD + 4 * d4);
-        po[part_index(a, j.part, j.tok0 + rr / G, j.kvh * G + rr % G) * (Dp / 4) + d4] = sum;
-    }
-    if (static_cast<int>(threadIdx.x) < j.rows) {
-        const int rho = threadIdx.x, rr = j.row0 + rho;
-        float top = neg_inf(), sum = 0.0f;
-        for (int w = 0; w < 4; ++w) top = fmaxf(top, ml[w * 16 + rho]);
-        for (int w = 0; w < 4; ++w) {
-            const float mw = ml[w * 16 + rho];
-            if (mw > neg_inf()) sum += ml[64 + w * 16 + rho] * __builtin_amdgcn_exp2f(mw - top);
-        }
-        pml[part_index(a, j.part, j.tok0 + rr / G, j.kvh * G + rr % G)] = make_float2(top, sum);
+        const int64_t tok = j.tok0 + rr / G;
+        const int head = j.kvh * G + rr % G;
+        if (pl.direct) store_result<DT>(a, tok, head, 4 * d4, sum * (sums[rho] > 0.0f ? 1.0f / sums[rho] : 0.0f));
+        else po[part_index(a, j.part, tok, head) * (Dp / 4) + d4] = sum;
     }
 }
 
@@ -489,48 +637,46 @@ __global__ __launch_bounds__(256, DC == 4 ? 1 : 2) void k_attn_stream(const Attn
 // and V is laid out in LDS in that order: weights never leave their lane.
 // Bound: vector ALU (softmax) and matrix cores.
 // ---------------------------------------------------------------------------
-constexpr int TILE_ROWS_ATTN = 128;
-
-template <int DT, int DC>
-__global__ __launch_bounds__(256, DC == 4 ? 1 : 2) void k_attn_tile(const AttnArgs a, const AttnPlan pl)
+template <int DT, int DC, int NW>
+__global__ __launch_bounds__(64 * NW, DC == 4 ? 1 : 2) void k_attn_tile(const AttnArgs a, const AttnPlan pl)
 {
     constexpr int NS = DT == DT_F32 ? 2 : 1;
     using WR = WeightRange<NS>;
-    constexpr int DPAD = 64 * DC, KSTEPS = DPAD / 16, DT32 = DPAD / 32, UNITS = DC; // 16-byte units per thread
+    constexpr int DPAD = 64 * DC, KSTEPS = DPAD / 16, DT32 = DPAD / 32;
+    constexpr int UNITS = 4 * DC / NW; // 16-byte units per thread
     constexpr int KBYTES = 64 * DPAD * 2, BUF = 2 * KBYTES + 512;
     // two buffers of K, V (binary16), K_scale, V_scale of a block
     __shared__ __attribute__((aligned(16))) uint8_t smem[2 * BUF];
     AttnJob j;
-    if (!attn_job(a, pl, TILE_ROWS_ATTN, TILE_ROWS_ATTN, blockIdx.x + pl.wg0, j)) return;
+    if (!attn_job(a, pl, 32 * NW, blockIdx.x + pl.wg0, j)) return;
     const int G = a.heads / a.c.heads, lane = lane_id(), wave = wave_id(), i = lane & 31, hf = lane >> 5;
-    const int Dp = a.c.Dp, bpp = a.c.page_tokens / CACHE_BLOCK, tid = threadIdx.x;
+    const int Dp = a.c.Dp, tid = threadIdx.x;
     const int rho = 32 * wave + i;
 
-    h8 q[NS][KSTEPS];
+    // one power of two for all rows (what smaller rows lose is 2^-39 of the tile's largest score)
+    h8 q[KSTEPS][NS];
     float c;
     {
         const int rr = rho < j.rows ? j.row0 + rho : j.row0;
         const int64_t off = (j.tok0 + static_cast<int64_t>(rr / G)) * a.ldq_t + (j.kvh * G + rr % G) * a.ldq_h;
-        float top = 0.0f;
-        for (int d = 8 * hf; d < a.c.D; d += 16)
-            for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(load_q<DT>(a, off, d + e)));
-        top = max_across32(top);
+        float v[KSTEPS][8], top = 0.0f;
+        load_queries<DT>(a, off, [&](int n) { return 16 * n + 8 * hf; }, v);
+#pragma unroll
+        for (int k = 0; k < KSTEPS; ++k) top = fmaxf(top, max_abs8(v[k]));
+        top = wave_max_nonneg(top);
+        float *tops = reinterpret_cast<float *>(smem);
+        if (lane == 0) tops[wave] = top;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < NW; ++w) top = fmaxf(top, tops[w]);
+        __syncthreads();
         const int e2 = row_exponent(top);
-        const float sgn = a.scale < 0.0f ? -1.0f : (a.scale > 0.0f ? 1.0f : 0.0f);
 #pragma unroll
-        for (int k = 0; k < KSTEPS; ++k)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float x = ldexpf(load_q<DT>(a, off, 16 * k + 8 * hf + e), e2) * sgn;
-                const _Float16 hi = static_cast<_Float16>(x);
-                q[0][k][e] = hi;
-                if constexpr (NS == 2) q[1][k][e] = static_cast<_Float16>(x - static_cast<float>(hi));
-            }
+        for (int k = 0; k < KSTEPS; ++k) query_terms<NS>(v[k], e2, a.scale, q[k]);
         c = row_factor(a.scale, e2);
     }
     const int lim = row_limit(j, G, rho);
     // a wave whose rows all lie past the tile multiplies nothing
-    const bool wave_live = 32 * wave < j.rows;
     int lim_min = rho < j.rows ? lim : 0x7fffffff, lim_max = lim;
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) {
@@ -539,35 +685,42 @@ __global__ __launch_bounds__(256, DC == 4 ? 1 : 2) void k_attn_tile(const AttnAr
     }
     lim_min = __builtin_amdgcn_readfirstlane(lim_min);
     lim_max = __builtin_amdgcn_readfirstlane(lim_max);
+    const int prefix_max = 32 * wave < j.rows ? j.prefix : 0;
 
     u4 kreg[UNITS], vreg[UNITS];
+    // this thread's bytes of a block; columns past Dp read the row's start (the queries hold zeros
+    // there), V's rows past Dp its first rows (their sums are not stored)
+    int koff[UNITS], voff[UNITS];
+#pragma unroll
+    for (int u = 0; u < UNITS; ++u) {
+        const int id = tid + 64 * NW * u, col = 16 * (id % (4 * DC));
+        koff[u] = id / (4 * DC) * Dp + (col < Dp ? col : 0);
+        voff[u] = (id / 4 < Dp ? id : id % 4) * 16;
+    }
     float ksr = 0.0f, vsr = 0.0f;
-    int page = -1;
-    auto fetch = [&](int blk) {
-        page = page_of(a, j, blk, bpp);
-        const int64_t row = cache_row0(a.c, page < 0 ? 0 : page, j.kvh) + blk % bpp * CACHE_BLOCK;
+    // A block's bytes and scales into registers.
+    auto fetch = [&](int blk, int page, int64_t row) {
         const int8_t *pk = a.c.K + row * Dp, *pv = a.c.V + row * Dp;
 #pragma unroll
         for (int u = 0; u < UNITS; ++u) {
-            const int id = tid + 256 * u, key = id / (4 * DC), col = 16 * (id % (4 * DC));
-            kreg[u] = col < Dp ? *reinterpret_cast<const u4 *>(pk + key * Dp + col) : u4{0, 0, 0, 0};
-            vreg[u] = id / 4 < Dp ? *reinterpret_cast<const u4 *>(pv + id * 16) : u4{0, 0, 0, 0};
+            kreg[u] = *reinterpret_cast<const u4 *>(pk + koff[u]);
+            vreg[u] = *reinterpret_cast<const u4 *>(pv + voff[u]);
         }
-        const int key = blk * CACHE_BLOCK + lane;
-        const bool seen = page >= 0 && key < j.keys;
+        const bool seen = page >= 0 && (blk < j.nbp ? blk * CACHE_BLOCK + lane < j.prefix
+                                                    : (blk - j.nbp) * CACHE_BLOCK + lane < j.own);
         ksr = a.c.Ks[row + lane];
         vsr = a.c.Vs[row + lane];
         ksr = seen ? ksr : 0.0f;
         vsr = seen ? vsr : 0.0f;
     };
-    float ref = 0.0f;
+    float ref = 0.0f, vscale = 0.0f;
     // Writes the fetched block into a buffer; returns the factor its V_scale's
     // reference asks the sums to be multiplied with (the same in every wave).
     auto stage = [&](int buf) -> float {
         uint8_t *base = smem + buf * BUF;
 #pragma unroll
         for (int u = 0; u < UNITS; ++u) {
-            const int id = tid + 256 * u, key = id / (4 * DC), cu = id % (4 * DC);
+            const int id = tid + 64 * NW * u, key = id / (4 * DC), cu = id % (4 * DC);
             // K: 16-byte unit (column / 8) * 64 + key, keys permuted by the unit pair so that
             // the eight units of a row fall into different banks
             h8 *pk = reinterpret_cast<h8 *>(base);
@@ -593,11 +746,12 @@ __global__ __launch_bounds__(256, DC == 4 ? 1 : 2) void k_attn_tile(const AttnAr
             const float ref2 = pow2_above(vtop);
             f = ref / ref2;
             ref = ref2;
+            vscale = WR::PSCALE / ref;
         }
         if (wave == 0) {
             float *sc = reinterpret_cast<float *>(base + 2 * KBYTES);
-            sc[lane] = ksr;
-            sc[64 + lane] = ref > 0.0f ? vsr * (WR::PSCALE / ref) : 0.0f;
+            sc[lane] = fmaxf(ksr * c, 1.17549435e-38f); // (a masked score is -inf: never times 0)
+            sc[64 + lane] = vsr * vscale;
         }
         return f;
     };
@@ -607,160 +761,239 @@ __global__ __launch_bounds__(256, DC == 4 ? 1 : 2) void k_attn_tile(const AttnAr
     for (int d = 0; d < DT32; ++d)
 #pragma unroll
         for (int r = 0; r < 16; ++r) o[d][r] = 0.0f;
-    float m = neg_inf(), l = 0.0f;
+    float m = 0.0f, l = 0.0f; // m: the row's reference in base 2, 0 until it is set
+    bool set = false;
+    // page: of the block being multiplied; page1: of the next, whose bytes are
+    // fetched meanwhile; the one after that is looked up a block ahead
+    PageWalk walk(a, j, j.blk0);
+    int page = -1, page1 = -1;
     if (j.blk0 < j.blk1) {
-        fetch(j.blk0);
+        page = walk.page(a);
+        fetch(j.blk0, page, walk.row(a, page, j.kvh));
         (void)stage(0);
+        walk.step(j, 1);
+        if (j.blk0 + 1 < j.blk1) page1 = walk.page(a);
     }
-    int cur_page = page;
     __syncthreads();
     for (int blk = j.blk0; blk < j.blk1; ++blk) {
         const int buf = (blk - j.blk0) & 1;
         const uint8_t *base = smem + buf * BUF;
-        const int this_page = cur_page;
-        if (blk + 1 < j.blk1) fetch(blk + 1);
-        const int k0 = blk * CACHE_BLOCK;
-        if (wave_live && this_page >= 0 && k0 < lim_max) {
+        const bool next = blk + 1 < j.blk1;
+        int page2 = -1;
+        if (next) {
+            fetch(blk + 1, page1, walk.row(a, page1, j.kvh));
+            walk.step(j, 1);
+            if (blk + 2 < j.blk1) page2 = walk.page(a);
+        }
+        // this block's list: its first key and those this row sees
+        const bool pre = blk < j.nbp;
+        const int k0 = (pre ? blk : blk - j.nbp) * CACHE_BLOCK, mine = pre ? j.prefix : lim;
+        if (page >= 0 && k0 < (pre ? prefix_max : lim_max)) {
             const h8 *pk = reinterpret_cast<const h8 *>(base), *pv = reinterpret_cast<const h8 *>(base + KBYTES);
             const f4 *sc = reinterpret_cast<const f4 *>(base + 2 * KBYTES);
             f16v s[2];
+            f4 kq[2][2], vq[2][2]; // scales of two 16-key tiles: keys 16 t + 8 x + 4 hf ..
+            auto read_scales = [&](int t) {
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    kq[t % 2][x] = sc[4 * t + 2 * x + hf];
+                    vq[t % 2][x] = sc[16 + 4 * t + 2 * x + hf];
+                }
+            };
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) s[t][r] = 0.0f;
+            // operands are read two k-steps ahead of their products (the barriers keep
+            // the compiler from sinking the reads to their uses, one LDS latency each)
+            h8 kf[3][2];
+            auto read_k = [&](int k) {
 #pragma unroll
-            for (int k = 0; k < KSTEPS; ++k)
+                for (int t = 0; t < 2; ++t) kf[k % 3][t] = pk[(2 * k + hf) * 64 + ((32 * t + i) ^ (k & 7))];
+            };
+            read_k(0);
+            read_k(1);
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const h8 kf = pk[(2 * k + hf) * 64 + ((32 * t + i) ^ (k & 7))];
+            for (int k = 0; k < KSTEPS; ++k) {
+                if (k + 2 < KSTEPS) read_k(k + 2);
+                if (k + 1 == KSTEPS) read_scales(0);
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                    for (int z = 0; z < NS; ++z) s[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, q[z][k], s[t], 0, 0, 0);
-                }
+                for (int z = 0; z < NS; ++z)
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const f4 kq = sc[8 * t + 2 * x + hf];
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) s[t][4 * x + r] *= kq[r];
-                }
-            if (k0 + CACHE_BLOCK > lim_min) {
+                    for (int t = 0; t < 2; ++t)
+                        s[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf[k % 3][t], q[k][z], s[t], 0, 0, 0);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            const bool masked = k0 + CACHE_BLOCK > (pre ? j.prefix : lim_min);
+            if (masked) {
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
 #pragma unroll
                     for (int r = 0; r < 16; ++r) {
                         const int key = k0 + 32 * t + 8 * (r / 4) + 4 * hf + r % 4;
-                        s[t][r] = key < lim ? s[t][r] : neg_inf();
+                        s[t][r] = key < mine ? s[t][r] : neg_inf();
                     }
             }
-            float top = neg_inf();
+            // element e of 16-key tile t is key 16 t + 8 (e / 4) + 4 hf + e % 4
+            auto score = [&](int t, int e) { return s[t / 2][8 * (t % 2) + e]; };
+            h8 p[4][NS];
+            float sum = 0.0f, big, small;
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+            for (int t = 0; t < 4; ++t) {
+                if (t < 3) read_scales(t + 1);
+                __builtin_amdgcn_sched_barrier(0);
+                float w[8];
 #pragma unroll
-                for (int r = 0; r < 16; ++r) top = fmaxf(top, s[t][r]);
-            top = max_across32(top);
-            const bool raise = top > neg_inf() && !((top - m) * c <= WR::SLACK);
-            if (__any(raise)) {
-                const float m2 = raise ? fmaxf(m, top) : m;
-                const float f = raise ? __builtin_amdgcn_exp2f((m - m2) * c) : 1.0f;
-                m = m2;
-                l *= f;
-#pragma unroll
-                for (int d = 0; d < DT32; ++d) o[d] *= f;
+                for (int e = 0; e < 8; ++e) {
+                    const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(score(t, e), kq[t % 2][e / 4][e % 4], -m));
+                    sum += y;
+                    w[e] = y * vq[t % 2][e / 4][e % 4];
+                }
+                split_weights<NS>(w, p[t]);
             }
-            const float mc = m > neg_inf() ? m * c : 0.0f;
-            float w[4][8], least = WR::LEAST; // weights by 16-key tile
+            weight_range(p, big, small);
+            if (masked) { // (masked weights are 0 and call for no round)
+                small = WR::LEAST;
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const f4 vq = sc[16 + 4 * t + 2 * x + hf];
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t / 2][8 * (t % 2) + 4 * x + r], c, -mc));
-                        l += p;
-                        w[t][4 * x + r] = p * vq[r];
-                        least = fminf(least, w[t][4 * x + r]);
-                    }
-                }
-            if (__any(least < WR::LEAST)) {
-                // weights below LEAST: rounds of their own, each brought up by STEP
-                float up = WR::STEP, down = 1.0f / WR::STEP;
-                for (bool more = true; more; up *= WR::STEP, down *= 1.0f / WR::STEP) {
-                    h8 p[4][NS];
-                    more = false;
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) more = round_weights<NS>(w[t], up, p[t]) || more;
-                    more = __any(more);
-#pragma unroll
-                    for (int d = 0; d < DT32; ++d) {
-                        f16v x;
-#pragma unroll
-                        for (int r = 0; r < 16; ++r) x[r] = 0.0f;
-#pragma unroll
-                        for (int t = 0; t < 4; ++t) {
-                            const h8 vv = pv[(2 * t + hf) * DPAD + 32 * d + i];
-#pragma unroll
-                            for (int z = 0; z < NS; ++z) x = __builtin_amdgcn_mfma_f32_32x32x16_f16(vv, p[t][z], x, 0, 0, 0);
-                        }
-                        o[d] += x * down;
-                        __builtin_amdgcn_sched_barrier(0); // one tile's registers at a time
-                    }
-                }
+                for (int e = 0; e < 32; ++e)
+                    small = score(e / 8, e % 8) > neg_inf() ? fminf(small, static_cast<float>(p[e / 8][0][e % 8])) : small;
+            }
+            if (__any((!set && k0 < mine) || !(big <= H_MAX) || !(sum <= SUM_MAX) || small < WR::LEAST)) {
+                // the general form: the reference brought to this block's largest score, small weights in
+                // rounds (the scales are read again, not kept)
+                int at = hf;
+                asm volatile("" : "+v"(at));
+                float top = neg_inf();
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) w[t][e] = w[t][e] >= WR::LEAST ? w[t][e] : 0.0f;
-            }
+                    for (int x = 0; x < 2; ++x) {
+                        const f4 k4 = sc[4 * t + 2 * x + at];
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                h8 p[NS];
-                split_weights<NS>(w[t], p);
+                        for (int r = 0; r < 4; ++r) {
+                            s[t / 2][8 * (t % 2) + 4 * x + r] *= k4[r];
+                            top = fmaxf(top, score(t, 4 * x + r));
+                        }
+                    }
+                top = max_across32(top);
+                const bool raise = top > neg_inf() && (!set || top > m);
+                const float f = raise && set ? __builtin_amdgcn_exp2f(m - top) : 1.0f;
+                m = raise ? top : m;
+                set = set || raise;
+                l *= f;
 #pragma unroll
-                for (int d = 0; d < DT32; ++d) {
-                    const h8 vv = pv[(2 * t + hf) * DPAD + 32 * d + i];
+                for (int d = 0; d < DT32; ++d) o[d] *= f;
+                sum = 0.0f;
 #pragma unroll
-                    for (int z = 0; z < NS; ++z) o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vv, p[z], o[d], 0, 0, 0);
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const f4 v4 = sc[16 + 4 * t + 2 * x + at];
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const float y = __builtin_amdgcn_exp2f(score(t, 4 * x + r) - m);
+                            sum += y;
+                            s[t / 2][8 * (t % 2) + 4 * x + r] = y * v4[r];
+                        }
+                    }
+                auto share = [&](float up, bool &more) {
+                    more = false;
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        float w[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) w[e] = round_share<NS>(score(t, e), up, more);
+                        split_weights<NS>(w, p[t]);
+                    }
+                    more = __any(more);
+                };
+                bool more;
+                share(1.0f, more);
+                if (more) {
+                    for (float up = WR::STEP, down = 1.0f / WR::STEP; more; up *= WR::STEP, down *= 1.0f / WR::STEP) {
+                        share(up, more);
+#pragma unroll
+                        for (int d = 0; d < DT32; ++d) {
+                            f16v x;
+#pragma unroll
+                            for (int r = 0; r < 16; ++r) x[r] = 0.0f;
+#pragma unroll
+                            for (int t = 0; t < 4; ++t) {
+                                const h8 vv = pv[(2 * t + hf) * DPAD + 32 * d + i];
+#pragma unroll
+                                for (int z = 0; z < NS; ++z) x = __builtin_amdgcn_mfma_f32_32x32x16_f16(vv, p[t][z], x, 0, 0, 0);
+                            }
+                            o[d] += x * down;
+                            __builtin_amdgcn_sched_barrier(0); // one tile's registers at a time
+                        }
+                    }
+                    share(1.0f, more);
                 }
             }
+            l += sum;
+            h8 vv[2][DT32];
+#pragma unroll
+            for (int d = 0; d < DT32; ++d) vv[0][d] = pv[hf * DPAD + 32 * d + i];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                if (t < 3)
+#pragma unroll
+                    for (int d = 0; d < DT32; ++d) vv[(t + 1) % 2][d] = pv[(2 * (t + 1) + hf) * DPAD + 32 * d + i];
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int z = 0; z < NS; ++z)
+#pragma unroll
+                    for (int d = 0; d < DT32; ++d)
+                        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vv[t % 2][d], p[t][z], o[d], 0, 0, 0);
+            }
         }
-        if (blk + 1 < j.blk1) {
+        if (next) {
             const float f = stage(buf ^ 1);
             if (f != 1.0f) {
 #pragma unroll
                 for (int d = 0; d < DT32; ++d) o[d] *= f;
             }
-            cur_page = page;
         }
+        page = page1;
+        page1 = page2;
         __syncthreads();
     }
     l += __shfl_xor(l, 32);
     if (rho < j.rows) {
-        const int rr = j.row0 + rho;
-        const int64_t at = part_index(a, j.part, j.tok0 + rr / G, j.kvh * G + rr % G);
+        const int rr = j.row0 + rho, head = j.kvh * G + rr % G;
+        const int64_t tok = j.tok0 + rr / G, at = part_index(a, j.part, tok, head);
         f4 *po = reinterpret_cast<f4 *>(a.ws) + at * (Dp / 4);
-        const float f = ref / WR::PSCALE;
+        const float f = ref / WR::PSCALE * (!pl.direct ? 1.0f : (l > 0.0f ? 1.0f / l : 0.0f));
 #pragma unroll
         for (int d = 0; d < DT32; ++d)
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 const int col = 32 * d + 8 * x + 4 * hf;
-                if (col < Dp) po[col / 4] = f4{o[d][4 * x], o[d][4 * x + 1], o[d][4 * x + 2], o[d][4 * x + 3]} * f;
+                const f4 v = f4{o[d][4 * x], o[d][4 * x + 1], o[d][4 * x + 2], o[d][4 * x + 3]} * f;
+                if (pl.direct) store_result<DT>(a, tok, head, col, v);
+                else if (col < Dp) po[col / 4] = v;
             }
-        if (hf == 0)
-            reinterpret_cast<float2 *>(a.ws + pl.ml_off)[at] = make_float2(m > neg_inf() ? m * c : neg_inf(), l);
+        if (hf == 0) {
+            if (!pl.direct) reinterpret_cast<float2 *>(a.ws + pl.ml_off)[at] = make_float2(set ? m : neg_inf(), l);
+            else if (a.lse) a.lse[tok * a.heads + head] = lse_of(m, l);
+        }
     }
 }
 
-// Joins the parts of every row: a wave per (token, head), lanes the columns.
-template <int DT>
+// Joins the parts of every row.  LPR lanes of four columns each cover a row.  With
+// few parts (WIDE false) a group of LPR lanes takes a row and goes through its
+// parts four at a time; with many, a wave takes a row, its lanes reading the (m, l)
+// of 64 parts at once and 64 / LPR parts' sums side by side.
+template <int DT, int LPR, bool WIDE>
 __global__ __launch_bounds__(256) void k_attn_join(const AttnArgs a, const AttnPlan pl, int64_t rows)
 {
-    const int64_t r = static_cast<int64_t>(blockIdx.x) * 4 + wave_id();
+    constexpr int PER = WIDE ? 64 : LPR; // lanes a row
+    const int64_t r = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / PER;
     if (r >= rows) return;
-    const int head = static_cast<int>(r % a.heads);
+    const int head = static_cast<int>(r % a.heads), lane = lane_id();
     const int64_t bi = r / a.heads;
-    const int b = static_cast<int>(bi / a.max_q), i = static_cast<int>(bi % a.max_q), lane = lane_id();
+    const int b = static_cast<int>(bi / a.max_q), i = static_cast<int>(bi % a.max_q);
     int first = b * a.max_q, n = a.max_q;
     if (a.q_start) {
         first = a.q_start[b];
@@ -769,33 +1002,78 @@ __global__ __launch_bounds__(256) void k_attn_join(const AttnArgs a, const AttnP
     }
     if (i >= n) return;
     const int64_t tok = static_cast<int64_t>(first) + i;
-    const int parts = pl.splits_prefix + pl.splits_own, Dp = a.c.Dp;
+    const int parts = pl.splits_prefix + pl.splits_own, Dp = a.c.Dp, col = 4 * (lane % LPR);
     const float2 *pml = reinterpret_cast<const float2 *>(a.ws + pl.ml_off);
-    float top = neg_inf();
-    for (int p = 0; p < parts; ++p) top = fmaxf(top, pml[part_index(a, p, tok, head)].x);
-    float l = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (top > neg_inf())
-        for (int p = 0; p < parts; ++p) {
-            const int64_t at = part_index(a, p, tok, head);
-            const float2 x = pml[at];
-            if (!(x.x > neg_inf())) continue;
-            const float f = __builtin_amdgcn_exp2f(x.x - top);
-            l += x.y * f;
+    float top = neg_inf(), l = 0.0f;
+    f4 o = f4{0.0f, 0.0f, 0.0f, 0.0f};
+    if constexpr (!WIDE) {
+        for (int p0 = 0; p0 < parts; p0 += 4) {
+            float2 x[4];
+            f4 v[4];
+            float t = top;
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (lane + 64 * k < a.c.D) o[k] += a.ws[at * Dp + lane + 64 * k] * f;
+            for (int u = 0; u < 4; ++u) {
+                const int64_t at = part_index(a, min(p0 + u, parts - 1), tok, head);
+                x[u] = pml[at];
+                v[u] = *reinterpret_cast<const f4 *>(a.ws + at * Dp + (col < Dp ? col : 0));
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                if (p0 + u >= parts) x[u] = make_float2(neg_inf(), 0.0f);
+                t = fmaxf(t, x[u].x);
+            }
+            if (!(t > neg_inf())) continue;
+            const float f = __builtin_amdgcn_exp2f(top - t);
+            l *= f;
+            o *= f;
+            top = t;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const float w = __builtin_amdgcn_exp2f(x[u].x - top); // 0 for a part without keys, whose sums are 0
+                l += x[u].y * w;
+                o += v[u] * w;
+            }
         }
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+    } else {
+        for (int p0 = 0; p0 < parts; p0 += 64) {
+            const float2 x = p0 + lane < parts ? pml[part_index(a, p0 + lane, tok, head)] : make_float2(neg_inf(), 0.0f);
+            float t = x.x;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const int d = lane + 64 * k;
-        if (d >= a.c.D) continue;
-        const int64_t at = tok * a.ldo_t + head * a.ldo_h + d;
-        if constexpr (DT == DT_F32) static_cast<float *>(a.O)[at] = o[k] * inv;
-        else static_cast<uint16_t *>(a.O)[at] = float_to_bf16_rne(o[k] * inv);
+            for (int s = 32; s > 0; s >>= 1) t = fmaxf(t, __shfl_xor(t, s));
+            if (!(t > neg_inf())) continue;
+            if (t > top) {
+                const float f = __builtin_amdgcn_exp2f(top - t); // (0 the first time)
+                l *= f;
+                o *= f;
+                top = t;
+            }
+            const float f = __builtin_amdgcn_exp2f(x.x - top); // this lane's part; 0 for one without keys
+            l += x.y * f;
+            const int here = min(64, parts - p0);
+            for (int p = 0; p < here; p += 8 * (64 / LPR)) {
+                f4 v[8];
+                float w[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const int q = p + u * (64 / LPR) + lane / LPR;
+                    w[u] = __shfl(f, q & 63);
+                    w[u] = q < here ? w[u] : 0.0f;
+                    v[u] = *reinterpret_cast<const f4 *>(a.ws + part_index(a, p0 + min(q, here - 1), tok, head) * Dp +
+                                                         (col < Dp ? col : 0));
+                }
+#pragma unroll
+                for (int u = 0; u < 8; ++u) o += v[u] * w[u];
+            }
+        }
+#pragma unroll
+        for (int s = 32; s > 0; s >>= 1) l += __shfl_xor(l, s);
+#pragma unroll
+        for (int s = LPR; s < 64; s <<= 1)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] += __shfl_xor(o[e], s);
     }
-    if (a.lse && lane == 0)
-        a.lse[tok * a.heads + head] = l > 0.0f ? (top + log2f(l)) * ATTN_LN2 : neg_inf();
+    if (lane % PER < LPR) store_result<DT>(a, tok, head, col, o * (l > 0.0f ? 1.0f / l : 0.0f));
+    if (a.lse && lane % PER == 0) a.lse[tok * a.heads + head] = lse_of(top, l);
 }
 
 // ---- host -------------------------------------------------------------------
@@ -803,39 +1081,61 @@ namespace {
 
 int64_t div_up(int64_t x, int64_t y) { return (x + y - 1) / y; }
 
-// Rows a workgroup takes: 16 with k_attn_stream, 128 with k_attn_tile.
-int tile_rows(int64_t rows) { return rows <= 16 ? 16 : TILE_ROWS_ATTN; }
+// Rows a workgroup takes: 16 with k_attn_stream, 128 or 256 (4 or 8 waves) with
+// k_attn_tile.  Eight waves share one staging of the keys where their registers
+// allow two waves per SIMD (head_dim in (64, 128]).
+int tile_rows(int64_t rows, int64_t head_dim)
+{
+    return rows <= 16 ? 16 : rows <= 128 || head_dim <= 64 || head_dim > 128 ? 128 : 256;
+}
 
-// Workgroups a launch should have: two for each of the 256 CUs.
-constexpr int64_t kAttnWgs = 512;
+// Splits of 'blocks' key blocks for 'wgs' workgroups of 'rows' rows: the count with
+// the least time, in blocks, of all rounds of the 256 CUs (two workgroups each; one
+// of eight waves), a workgroup costing its blocks and about four more for its start
+// and end; a split more costs its sums' way through memory.
+void choose_splits(int64_t wgs, int64_t blocks, int rows, int *chunk, int *splits)
+{
+    *chunk = *splits = 0;
+    if (blocks == 0) return;
+    const int64_t slots = rows == 256 ? 256 : 512, least = rows == 16 ? 4 : 2; // (k_attn_stream: a block for each wave)
+    int64_t best = -1;
+    for (int64_t s = 1; s <= 64 && (s == 1 || div_up(blocks, s) >= least); ++s) {
+        const int64_t c = div_up(blocks, s), n = div_up(blocks, c);
+        const int64_t cost = div_up(wgs * n, slots) * (c + 4) + n / 8;
+        if (best < 0 || cost < best) {
+            best = cost;
+            *chunk = static_cast<int>(c);
+            *splits = static_cast<int>(n);
+        }
+    }
+}
+
+// Reading the prefix again for each sequence costs less than a launch and a join
+// of their own up to about this many bytes (a launch and its join are near 8 us).
+constexpr int64_t kJointBytes = int64_t(16) << 20;
 
 AttnPlan attn_plan(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t seqs, int64_t max_q,
                    int64_t max_own, int64_t prefix)
 {
     AttnPlan p;
-    const int64_t G = heads / kv_heads, nbp = div_up(prefix, CACHE_BLOCK), nbo = div_up(max_own, CACHE_BLOCK);
-    auto split = [](int64_t wgs, int64_t blocks, int64_t least, int *chunk, int *splits) {
-        if (blocks == 0) {
-            *chunk = *splits = 0;
-            return;
-        }
-        int64_t s = kAttnWgs / wgs;
-        const int64_t most = div_up(blocks, least);
-        s = s < 1 ? 1 : (s > most ? most : s);
-        *chunk = static_cast<int>(div_up(blocks, s));
-        *splits = static_cast<int>(div_up(blocks, *chunk));
-    };
-    p.rows_prefix = tile_rows(tokens * G);
-    p.rows_own = tile_rows(max_q * G);
+    const int64_t G = heads / kv_heads, dp = div_up(head_dim, 16) * 16;
+    const int64_t nbp = div_up(prefix, CACHE_BLOCK), nbo = div_up(max_own, CACHE_BLOCK);
+    p.rows_prefix = tile_rows(tokens * G, head_dim);
+    p.rows_own = tile_rows(max_q * G, head_dim);
     p.tiles_own = static_cast<int>(div_up(max_q * G, p.rows_own));
-    const int64_t tp = div_up(tokens * G, p.rows_prefix);
-    split(tp * kv_heads, nbp, 4, &p.chunk_prefix, &p.splits_prefix);
-    split(seqs * p.tiles_own * kv_heads, nbo, 4, &p.chunk_own, &p.splits_own);
+    // one pass over prefix and own keys where a sequence fills row tiles of its own anyway, or the
+    // prefix is short
+    p.joint = nbp > 0 && (p.rows_own > 16 || 2 * prefix * kv_heads * dp * (seqs - 1) <= kJointBytes);
+    const int64_t tp = p.joint || nbp == 0 ? 0 : div_up(tokens * G, p.rows_prefix);
+    p.chunk_prefix = p.splits_prefix = 0;
+    if (tp > 0) choose_splits(tp * kv_heads, nbp, p.rows_prefix, &p.chunk_prefix, &p.splits_prefix);
+    choose_splits(seqs * p.tiles_own * kv_heads, p.joint ? nbp + nbo : nbo, p.rows_own, &p.chunk_own, &p.splits_own);
     p.wgs_prefix = static_cast<int>(tp * kv_heads * p.splits_prefix);
     p.wgs_own = static_cast<int>(seqs * p.tiles_own * kv_heads * p.splits_own);
     p.wg0 = 0;
-    const int64_t parts = p.splits_prefix + p.splits_own, dp = div_up(head_dim, 16) * 16;
-    p.ml_off = parts * tokens * heads * dp;
+    const int64_t parts = p.splits_prefix + p.splits_own;
+    p.direct = parts == 1 && p.splits_own == 1;
+    p.ml_off = p.direct ? 0 : parts * tokens * heads * dp;
     return p;
 }
 
@@ -847,15 +1147,17 @@ hipError_t launch_part(const AttnArgs &a, AttnPlan pl, int rows, int wg0, int wg
     const int dc = a.c.Dp <= 64 ? 1 : a.c.Dp <= 128 ? 2 : 4;
     const dim3 grid(static_cast<unsigned>(wgs)), block(256);
 #define BL_STREAM(DC) hipLaunchKernelGGL((k_attn_stream<DT, DC>), grid, block, 0, st, a, pl)
-#define BL_TILE(DC) hipLaunchKernelGGL((k_attn_tile<DT, DC>), grid, block, 0, st, a, pl)
+#define BL_TILE(DC, NW) hipLaunchKernelGGL((k_attn_tile<DT, DC, NW>), grid, dim3(64 * NW), 0, st, a, pl)
     if (rows == 16) {
         if (dc == 1) BL_STREAM(1);
         else if (dc == 2) BL_STREAM(2);
         else BL_STREAM(4);
+    } else if (rows == 128) {
+        if (dc == 1) BL_TILE(1, 4);
+        else if (dc == 2) BL_TILE(2, 4);
+        else BL_TILE(4, 4);
     } else {
-        if (dc == 1) BL_TILE(1);
-        else if (dc == 2) BL_TILE(2);
-        else BL_TILE(4);
+        BL_TILE(2, 8);
     }
 #undef BL_STREAM
 #undef BL_TILE
@@ -868,8 +1170,22 @@ hipError_t launch_attn(const AttnArgs &a, const AttnPlan &pl, hipStream_t st)
     hipError_t e = launch_part<DT>(a, pl, pl.rows_prefix, 0, pl.wgs_prefix, st);
     if (e == hipSuccess) e = launch_part<DT>(a, pl, pl.rows_own, pl.wgs_prefix, pl.wgs_own, st);
     if (e != hipSuccess) return e;
+    if (pl.direct) return hipSuccess;
     const int64_t rows = static_cast<int64_t>(a.seqs) * a.max_q * a.heads;
-    hipLaunchKernelGGL(k_attn_join<DT>, dim3(static_cast<unsigned>(div_up(rows, 4))), dim3(256), 0, st, a, pl, rows);
+    const bool wide = pl.splits_prefix + pl.splits_own > 12;
+    const int lpr = a.c.Dp <= 64 ? 16 : a.c.Dp <= 128 ? 32 : 64;
+    const dim3 grid(static_cast<unsigned>(div_up(rows * (wide ? 64 : lpr), 256))), block(256);
+#define BL_JOIN(LPR, WIDE) hipLaunchKernelGGL((k_attn_join<DT, LPR, WIDE>), grid, block, 0, st, a, pl, rows)
+    if (wide) {
+        if (lpr == 16) BL_JOIN(16, true);
+        else if (lpr == 32) BL_JOIN(32, true);
+        else BL_JOIN(64, true);
+    } else {
+        if (lpr == 16) BL_JOIN(16, false);
+        else if (lpr == 32) BL_JOIN(32, false);
+        else BL_JOIN(64, false);
+    }
+#undef BL_JOIN
     return hipGetLastError();
 }
 
@@ -879,7 +1195,7 @@ int64_t attn_workspace_bytes(int64_t tokens, int64_t heads, int64_t kv_heads, in
                              int64_t max_q, int64_t max_own, int64_t prefix)
 {
     const AttnPlan p = attn_plan(tokens, heads, kv_heads, head_dim, seqs, max_q, max_own, prefix);
-    return (p.ml_off + 2 * (p.splits_prefix + p.splits_own) * tokens * heads) * 4;
+    return p.direct ? 0 : (p.ml_off + 2 * (p.splits_prefix + p.splits_own) * tokens * heads) * 4;
 }
 
 hipError_t launch_attention(const AttnArgs &a, hipStream_t stream)
