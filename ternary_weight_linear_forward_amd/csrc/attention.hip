@@ -104,6 +104,21 @@ __device__ __forceinline__ void weight_range(const h8 (&p)[NT][NS], float &big, 
 constexpr float H_MAX = 65504.0f;   // largest binary16
 constexpr float SUM_MAX = 0x1p100f; // a block's sum of p beyond which the reference is raised
 
+// Power of two at or above v > 0 (as a factor that never overflows).
+__device__ __forceinline__ float pow2_above(float v)
+{
+    const uint32_t e = (__float_as_uint(v) + 0x007fffffu) >> 23;
+    return __uint_as_float(min(max(e, 16u), 253u) << 23);
+}
+
+// Small weights: what a row's weights can be multiplied with so that the largest so
+// far, have, comes to [2^13, 2^14) (a power of two, at least 1; sums stay in range).
+__device__ __forceinline__ float lift(float have, float sum)
+{
+    const float f = 0x1p13f / pow2_above(fmaxf(have, 0x1p-80f)), room = 0x1p90f / pow2_above(fmaxf(sum, 1.0f));
+    return fmaxf(1.0f, fminf(f, room));
+}
+
 __device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
 
 // Own keys query i of a sequence sees: own_len - n + i + 1, within [0, own_len].
@@ -131,20 +146,69 @@ __device__ __forceinline__ h8 bytes_to_h8(uint32_t a, uint32_t b)
     return r.v;
 }
 
-__device__ __forceinline__ float max_across32(float v) // lanes l, l ^ 32
+// v of this lane and of lane ^ 32 (lane ^ 16), in both lanes: the swap of a
+// register's halves (rows) with a copy's.
+__device__ __forceinline__ void halves32(float v, float &a, float &b)
 {
-    return fmaxf(v, __shfl_xor(v, 32));
+#if defined(__HIP_DEVICE_COMPILE__)
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    a = __uint_as_float(r[0]);
+    b = __uint_as_float(r[1]);
+#else
+    a = b = v;
+#endif
 }
-__device__ __forceinline__ float max_across16(float v) // lanes l, l ^ 16
+__device__ __forceinline__ void halves16(float v, float &a, float &b)
 {
-    return fmaxf(v, __shfl_xor(v, 16));
+#if defined(__HIP_DEVICE_COMPILE__)
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    a = __uint_as_float(r[0]);
+    b = __uint_as_float(r[1]);
+#else
+    a = b = v;
+#endif
+}
+__device__ __forceinline__ float max_across32(float v)
+{
+    float a, b;
+    halves32(v, a, b);
+    return fmaxf(a, b);
+}
+__device__ __forceinline__ float max_across16(float v)
+{
+    float a, b;
+    halves16(v, a, b);
+    return fmaxf(a, b);
+}
+__device__ __forceinline__ float sum_across32(float v)
+{
+    float a, b;
+    halves32(v, a, b);
+    return a + b;
+}
+__device__ __forceinline__ float sum_across16(float v)
+{
+    float a, b;
+    halves16(v, a, b);
+    return a + b;
 }
 
-// Power of two at or above v > 0 (as a factor that never overflows).
-__device__ __forceinline__ float pow2_above(float v)
+// A load at a uniform address and a lane's offset in bytes: global_load with a
+// scalar base, so that no 64-bit sums are kept across a loop.  The address space is
+// named because the compiler may not see through the empty asm, and a flat load
+// would count among the LDS's: every wait for an operand read would wait for it.
+template <class T>
+__device__ __forceinline__ T load_at(const void *base, uint32_t offset)
 {
-    const uint32_t e = (__float_as_uint(v) + 0x007fffffu) >> 23;
-    return __uint_as_float(min(max(e, 16u), 253u) << 23);
+#if defined(__HIP_DEVICE_COMPILE__)
+    typedef const __attribute__((address_space(1))) uint8_t *bytes_t;
+    typedef const __attribute__((address_space(1))) T *at_t;
+    bytes_t p = reinterpret_cast<bytes_t>(reinterpret_cast<uintptr_t>(base));
+    asm volatile("" : "+s"(p), "+v"(offset));
+    return *reinterpret_cast<at_t>(p + offset);
+#else
+    return T();
+#endif
 }
 
 // One part's rows and keys, the same for a whole workgroup.  The keys are a list
@@ -288,6 +352,31 @@ __device__ __forceinline__ void store_result(const AttnArgs &a, int64_t tok, int
 // log(sum e^s) from a base-2 reference and sum.
 __device__ __forceinline__ float lse_of(float m, float l) { return l > 0.0f ? (m + log2f(l)) * ATTN_LN2 : neg_inf(); }
 
+// The rows of 64 blocks of a job, lane x holding block first + x: the block's first
+// row in units of tokens (page, head and place in the page), or -1 for a page
+// outside the cache or a block past the job's.  One lane is then one read of a
+// register, with no page list or division in the loop over blocks.
+struct RowTable {
+    int lo, hi;
+    __device__ __forceinline__ void load(const AttnArgs &a, const AttnJob &j, int first)
+    {
+        const int blk = first + lane_id(), bpp = a.c.page_tokens / CACHE_BLOCK;
+        int64_t row = -1;
+        if (blk < j.blk1) {
+            const int rel = blk < j.nbp ? blk : blk - j.nbp, pi = rel / bpp;
+            const int page = (blk < j.nbp ? j.prefix_pages : j.own_pages)[pi];
+            if (page >= 0 && page < a.c.pages) row = cache_row0(a.c, page, j.kvh) + (rel - pi * bpp) * CACHE_BLOCK;
+        }
+        lo = static_cast<int>(row);
+        hi = static_cast<int>(row >> 32);
+    }
+    __device__ __forceinline__ int64_t at(int x) const // x uniform
+    {
+        return static_cast<int64_t>(__builtin_amdgcn_readlane(hi, x)) << 32 |
+               static_cast<uint32_t>(__builtin_amdgcn_readlane(lo, x));
+    }
+};
+
 // A row's power of two: 2^e with max|q| 2^e in [2^13, 2^14); 1 for a zero row.
 __device__ __forceinline__ int row_exponent(float top)
 {
@@ -398,10 +487,11 @@ __global__ __launch_bounds__(256, DC == 4 ? 1 : 2) void k_attn_stream(const Attn
     // m: the row's reference in base 2 (0 until it is set), ref: of the V_scales
     float m = 0.0f, l = 0.0f, ref = 0.0f, vscale = 0.0f;
     bool set = false;
+    float have = 0.0f; // the largest weight so far (of a row: what this lane saw of it)
     u4 kb[4][DC], vb[DTILES];
     f4 ks[4], vs[4];
     // byte offsets of this lane inside a block (columns past Dp read column 0: the queries hold zeros there)
-    int koff[DC], voff[DTILES];
+    uint32_t koff[DC], voff[DTILES]; // (unsigned: one register beside a uniform base)
 #pragma unroll
     for (int cc = 0; cc < DC; ++cc) koff[cc] = i * Dp + (64 * cc + 16 * g < Dp ? 64 * cc + 16 * g : 0);
 #pragma unroll
@@ -411,14 +501,15 @@ __global__ __launch_bounds__(256, DC == 4 ? 1 : 2) void k_attn_stream(const Attn
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
-            for (int cc = 0; cc < DC; ++cc) kb[t][cc] = *reinterpret_cast<const u4 *>(p + 16 * t * Dp + koff[cc]);
+            for (int cc = 0; cc < DC; ++cc) kb[t][cc] = *reinterpret_cast<const u4 *>(p + 16 * t * Dp + static_cast<uint64_t>(koff[cc]));
     };
     auto load_v = [&](int64_t row) { // and the scales
         const int8_t *p = a.c.V + row * Dp;
+        const float *pks = a.c.Ks + row, *pvs = a.c.Vs + row;
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-            ks[t] = *reinterpret_cast<const f4 *>(a.c.Ks + row + 16 * t + 4 * g);
-            vs[t] = *reinterpret_cast<const f4 *>(a.c.Vs + row + 16 * t + 4 * g);
+            ks[t] = *reinterpret_cast<const f4 *>(pks + 16 * t + static_cast<uint32_t>(4 * g));
+            vs[t] = *reinterpret_cast<const f4 *>(pvs + 16 * t + static_cast<uint32_t>(4 * g));
         }
 #pragma unroll
         for (int d = 0; d < DTILES; ++d) vb[d] = *reinterpret_cast<const u4 *>(p + voff[d]);
@@ -470,7 +561,7 @@ __global__ __launch_bounds__(256, DC == 4 ? 1 : 2) void k_attn_stream(const Attn
         const int64_t nrow = walk.row(a, npage, j.kvh);
         if (next) load_k(nrow);
         h8 p[2][NS];
-        float sum = 0.0f, big, small;
+        float sum = 0.0f;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             float w[8];
@@ -482,8 +573,9 @@ __global__ __launch_bounds__(256, DC == 4 ? 1 : 2) void k_attn_stream(const Attn
             }
             split_weights<NS>(w, p[h]);
         }
+        float big, small;
         weight_range(p, big, small);
-        if (masked) { // (masked weights are 0 and call for no round)
+        if (masked) { // (masked weights are 0 and call for nothing)
             small = WR::LEAST;
 #pragma unroll
             for (int e = 0; e < 16; ++e)
@@ -499,7 +591,9 @@ __global__ __launch_bounds__(256, DC == 4 ? 1 : 2) void k_attn_stream(const Attn
             }
             vtop = max_across32(max_across16(vtop));
             top = max_across32(max_across16(top));
-            const bool raise = top > neg_inf() && (!set || top > m);
+            big = max_across32(max_across16(big));
+            sum = max_across32(max_across16(sum));
+            const bool raise = top > neg_inf() && (!set || (top > m && (!(big <= H_MAX) || !(sum <= SUM_MAX))));
             float f = raise && set ? __builtin_amdgcn_exp2f(m - top) : 1.0f;
             m = raise ? top : m;
             set = set || raise;
@@ -513,6 +607,8 @@ __global__ __launch_bounds__(256, DC == 4 ? 1 : 2) void k_attn_stream(const Attn
 #pragma unroll
             for (int d = 0; d < DTILES; ++d) o[d] *= f;
             sum = 0.0f;
+            big = 0.0f;
+            small = WR::LEAST;
 #pragma unroll
             for (int t = 0; t < 4; ++t)
 #pragma unroll
@@ -520,14 +616,35 @@ __global__ __launch_bounds__(256, DC == 4 ? 1 : 2) void k_attn_stream(const Attn
                     s[t][r] = __builtin_amdgcn_exp2f(s[t][r] - m);
                     sum += s[t][r];
                     s[t][r] *= vs[t][r] * vscale;
+                    big = fmaxf(big, s[t][r]);
+                    small = s[t][r] > 0.0f ? fminf(small, s[t][r]) : small;
                 }
+            have = max_across32(max_across16(fmaxf(have * f, big)));
+            big = 0.0f; // (it is in have)
+            if (__any(small < WR::LEAST)) {
+                small = -max_across32(max_across16(-small));
+                const float up = small < WR::LEAST ? lift(have, max_across32(max_across16(l + sum))) : 1.0f;
+                m -= __builtin_log2f(up);
+                l *= up;
+                sum *= up;
+                have *= up;
+#pragma unroll
+                for (int d = 0; d < DTILES; ++d) o[d] *= up;
+#pragma unroll
+                for (int t = 0; t < 4; ++t) s[t] *= up;
+                small *= up;
+            }
+            const bool rounds = __any(small < WR::LEAST);
             auto share = [&](float up, bool &more) {
                 more = false;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     float w[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) w[e] = round_share<NS>(s[2 * h + e / 4][e % 4], up, more);
+                    for (int e = 0; e < 8; ++e) {
+                        const float y = s[2 * h + e / 4][e % 4];
+                        w[e] = rounds ? round_share<NS>(y, up, more) : y;
+                    }
                     split_weights<NS>(w, p[h]);
                 }
                 more = __any(more);
@@ -557,6 +674,7 @@ __global__ __launch_bounds__(256, DC == 4 ? 1 : 2) void k_attn_stream(const Attn
             }
         }
         l += sum;
+        have = fmaxf(have, big);
 #pragma unroll
         for (int d = 0; d < DTILES; ++d)
 #pragma unroll
@@ -575,8 +693,7 @@ __global__ __launch_bounds__(256, DC == 4 ? 1 : 2) void k_attn_stream(const Attn
 
     // add the waves: largest m of each row, every wave's sums brought to it
     float *ml = lds + 4 * 16 * DPAD;
-    l += __shfl_xor(l, 16);
-    l += __shfl_xor(l, 32);
+    l = sum_across32(sum_across16(l));
     m = set ? m : neg_inf();
     if (g == 0) {
         ml[wave * 16 + i] = m;
@@ -628,30 +745,84 @@ __global__ __launch_bounds__(256, DC == 4 ? 1 : 2) void k_attn_stream(const Attn
 }
 
 // ---------------------------------------------------------------------------
-// Many rows: k_attn_tile.  A workgroup takes 128 rows (a wave 32) and a chunk of
-// keys; blocks of 64 keys are converted to binary16 once for the workgroup and
-// kept in two LDS buffers: the next block's bytes are fetched into registers
-// before a block is multiplied and written after it, one barrier a block.
-// S^T = K Q^T in 32 x 32 tiles leaves a lane (row = lane % 32, half = lane / 32)
-// keys 8 x + 4 half + {0..3}; two such quads are one operand of O^T += V^T P^T,
-// and V is laid out in LDS in that order: weights never leave their lane.
-// Bound: vector ALU (softmax) and matrix cores.
+// Many rows: k_attn_tile.  A workgroup of NW waves takes 32 NW rows (a wave 32)
+// and a chunk of keys; blocks of 64 keys are converted to binary16 once for the
+// workgroup and kept in LDS, two of K and two of V.  S^T = K Q^T in 32 x 32 tiles
+// leaves a lane (row = lane % 32, half = lane / 32) keys 8 x + 4 half + {0..3}; two
+// such quads are one operand of O^T += V^T P^T, and V is laid out in LDS in that
+// order: weights never leave their lane.
+//
+// A block n is two phases of a wave: P(n), products (sums of block n - 1, scores of
+// block n, beside the conversion of the next K and this V), and W(n), its weights.
+// P keeps the matrix cores busy and W the vector ALU, so with eight waves the
+// second four run one phase behind the first: of the two waves of a SIMD one is in
+// P while the other is in W (a barrier after every phase; measured without the
+// shift, both do the same phase and neither unit is busy half the time).  What P(n)
+// writes (K of n + 1, V of n, scales of n + 1) takes places that nothing has read
+// since the barrier before either half's P(n), and is read from the phase after
+// both halves' P(n) on.  With four waves the other workgroup of the CU fills in.
+// Operands are read from LDS some steps ahead; the bytes converted next are in
+// flight from memory in registers for a whole block.
+// Bound: vector ALU (weights, conversion) beside matrix cores.
 // ---------------------------------------------------------------------------
+constexpr bool tile_one_wave(int dt, int dc) { return dc == 4 || (dt == DT_F32 && dc == 2); }
+
 template <int DT, int DC, int NW>
-__global__ __launch_bounds__(64 * NW, DC == 4 ? 1 : 2) void k_attn_tile(const AttnArgs a, const AttnPlan pl)
+__global__ __launch_bounds__(64 * NW, tile_one_wave(DT, DC) ? 1 : 2) void k_attn_tile(const AttnArgs a, const AttnPlan pl)
 {
     constexpr int NS = DT == DT_F32 ? 2 : 1;
     using WR = WeightRange<NS>;
     constexpr int DPAD = 64 * DC, KSTEPS = DPAD / 16, DT32 = DPAD / 32;
-    constexpr int UNITS = 4 * DC / NW; // 16-byte units per thread
-    constexpr int KBYTES = 64 * DPAD * 2, BUF = 2 * KBYTES + 512;
-    // two buffers of K, V (binary16), K_scale, V_scale of a block
-    __shared__ __attribute__((aligned(16))) uint8_t smem[2 * BUF];
+    constexpr int UNITS = 4 * DC / NW; // 16-byte units of K (and V) per thread
+    // K in LDS: 16-byte unit of 8 columns c8 of a key at ((c8 / 2 + KSTEPS (c8 % 2)) KROW + key); the odd
+    // row puts the units of one key into different banks, and an operand's place is a constant apart
+    // for every k-step
+    constexpr int KROW = 65, KBYTES = 2 * KSTEPS * KROW * 16, VBYTES = 64 * DPAD * 2;
+    // two blocks of K, two of V (binary16), three of K_scale and V_scale
+    __shared__ __attribute__((aligned(16))) uint8_t smem[2 * KBYTES + 2 * VBYTES + 3 * 512];
+    auto k_at = [&](int n) { return smem + n * KBYTES; };
+    auto v_at = [&](int n) { return smem + 2 * KBYTES + n * VBYTES; };
+    auto scales_at = [&](int n) { return reinterpret_cast<float *>(smem + 2 * (KBYTES + VBYTES) + n * 512); };
     AttnJob j;
     if (!attn_job(a, pl, 32 * NW, blockIdx.x + pl.wg0, j)) return;
     const int G = a.heads / a.c.heads, lane = lane_id(), wave = wave_id(), i = lane & 31, hf = lane >> 5;
-    const int Dp = a.c.Dp, tid = threadIdx.x;
-    const int rho = 32 * wave + i;
+    const int Dp = a.c.Dp, tid = threadIdx.x, rho = 32 * wave + i;
+
+    u4 kreg[UNITS] = {}, vreg[UNITS] = {};
+    // this thread's bytes of a block; columns past Dp read the row's start (the queries hold zeros
+    // there), V's rows past Dp its first rows (their sums are not stored)
+    uint32_t koff[UNITS], voff[UNITS]; // (unsigned: one register beside a uniform base)
+#pragma unroll
+    for (int u = 0; u < UNITS; ++u) {
+        const int id = tid + 64 * NW * u, col = 16 * (id % (4 * DC));
+        koff[u] = id / (4 * DC) * Dp + (col < Dp ? col : 0);
+        voff[u] = (id / 4 < Dp ? id : id % 4) * 16;
+    }
+    float ksr = 0.0f, vsr = 0.0f;
+    int seen = 0; // keys of the fetched block that there are
+    // A block's bytes into registers: K and the scales, and V.
+    auto fetch_k = [&](int blk, int64_t at) {
+        const int64_t row = at < 0 ? 0 : at;
+#pragma unroll
+        for (int u = 0; u < UNITS; ++u) kreg[u] = load_at<u4>(a.c.K + row * Dp, koff[u]);
+        ksr = load_at<float>(a.c.Ks + row, 4 * lane);
+        vsr = load_at<float>(a.c.Vs + row, 4 * lane);
+        // (applied where the scales are written: a use here would wait for the loads)
+        seen = at < 0 ? 0 : (blk < j.nbp ? j.prefix - blk * CACHE_BLOCK : j.own - (blk - j.nbp) * CACHE_BLOCK);
+    };
+    auto fetch_v = [&](int64_t at) {
+#pragma unroll
+        for (int u = 0; u < UNITS; ++u) vreg[u] = load_at<u4>(a.c.V + (at < 0 ? 0 : at) * Dp, voff[u]);
+    };
+    // rows of block n and of block n + 1, whose K is in registers
+    RowTable table;
+    int64_t row0 = -1, row1 = -1;
+    if (j.blk0 < j.blk1) { // (in flight while the queries are read)
+        table.load(a, j, j.blk0);
+        row0 = table.at(0);
+        fetch_k(j.blk0, row0);
+        fetch_v(row0);
+    }
 
     // one power of two for all rows (what smaller rows lose is 2^-39 of the tile's largest score)
     h8 q[KSTEPS][NS];
@@ -675,86 +846,49 @@ __global__ __launch_bounds__(64 * NW, DC == 4 ? 1 : 2) void k_attn_tile(const At
         for (int k = 0; k < KSTEPS; ++k) query_terms<NS>(v[k], e2, a.scale, q[k]);
         c = row_factor(a.scale, e2);
     }
+    // own keys the lane's row sees, and the least of the wave's rows: below it nothing is masked
     const int lim = row_limit(j, G, rho);
-    // a wave whose rows all lie past the tile multiplies nothing
-    int lim_min = rho < j.rows ? lim : 0x7fffffff, lim_max = lim;
+    int lim_min = rho < j.rows ? lim : 0x7fffffff;
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1) {
-        lim_min = min(lim_min, __shfl_xor(lim_min, x));
-        lim_max = max(lim_max, __shfl_xor(lim_max, x));
-    }
+    for (int x = 16; x > 0; x >>= 1) lim_min = min(lim_min, __shfl_xor(lim_min, x));
     lim_min = __builtin_amdgcn_readfirstlane(lim_min);
-    lim_max = __builtin_amdgcn_readfirstlane(lim_max);
-    const int prefix_max = 32 * wave < j.rows ? j.prefix : 0;
 
-    u4 kreg[UNITS], vreg[UNITS];
-    // this thread's bytes of a block; columns past Dp read the row's start (the queries hold zeros
-    // there), V's rows past Dp its first rows (their sums are not stored)
-    int koff[UNITS], voff[UNITS];
-#pragma unroll
-    for (int u = 0; u < UNITS; ++u) {
-        const int id = tid + 64 * NW * u, col = 16 * (id % (4 * DC));
-        koff[u] = id / (4 * DC) * Dp + (col < Dp ? col : 0);
-        voff[u] = (id / 4 < Dp ? id : id % 4) * 16;
-    }
-    float ksr = 0.0f, vsr = 0.0f;
-    // A block's bytes and scales into registers.
-    auto fetch = [&](int blk, int page, int64_t row) {
-        const int8_t *pk = a.c.K + row * Dp, *pv = a.c.V + row * Dp;
-#pragma unroll
-        for (int u = 0; u < UNITS; ++u) {
-            kreg[u] = *reinterpret_cast<const u4 *>(pk + koff[u]);
-            vreg[u] = *reinterpret_cast<const u4 *>(pv + voff[u]);
-        }
-        const bool seen = page >= 0 && (blk < j.nbp ? blk * CACHE_BLOCK + lane < j.prefix
-                                                    : (blk - j.nbp) * CACHE_BLOCK + lane < j.own);
-        ksr = a.c.Ks[row + lane];
-        vsr = a.c.Vs[row + lane];
-        ksr = seen ? ksr : 0.0f;
-        vsr = seen ? vsr : 0.0f;
+    float ref = 0.0f, vscale = 0.0f, grow = 1.0f;
+    // Writing the fetched bytes, step by step.  V: unit (2 T + g % 2) * DPAD + d holds
+    // quads g and g + 2 of 16-key tile T.
+    auto stage_k = [&](int n, uint8_t *to) {
+        const int u = n / 2, part = n % 2, id = tid + 64 * NW * u, key = id / (4 * DC), cu = id % (4 * DC);
+        reinterpret_cast<h8 *>(to)[(cu + KSTEPS * part) * KROW + key] = bytes_to_h8(kreg[u][2 * part], kreg[u][2 * part + 1]);
     };
-    float ref = 0.0f, vscale = 0.0f;
-    // Writes the fetched block into a buffer; returns the factor its V_scale's
-    // reference asks the sums to be multiplied with (the same in every wave).
-    auto stage = [&](int buf) -> float {
-        uint8_t *base = smem + buf * BUF;
-#pragma unroll
-        for (int u = 0; u < UNITS; ++u) {
-            const int id = tid + 64 * NW * u, key = id / (4 * DC), cu = id % (4 * DC);
-            // K: 16-byte unit (column / 8) * 64 + key, keys permuted by the unit pair so that
-            // the eight units of a row fall into different banks
-            h8 *pk = reinterpret_cast<h8 *>(base);
-            pk[2 * cu * 64 + (key ^ (cu & 7))] = bytes_to_h8(kreg[u][0], kreg[u][1]);
-            pk[(2 * cu + 1) * 64 + (key ^ (cu & 7))] = bytes_to_h8(kreg[u][2], kreg[u][3]);
-            // V: unit (2 T + g % 2) * DPAD + d holds quads g and g + 2 of 16-key tile T
-            const int d = id / 4, g = id % 4;
-            uint2 *pv = reinterpret_cast<uint2 *>(base + KBYTES);
-#pragma unroll
-            for (int t = 0; t < 4; t += 2) {
-                union {
-                    h8 v;
-                    uint2 w[2];
-                } x;
-                x.v = bytes_to_h8(vreg[u][t], vreg[u][t + 1]);
-                pv[((2 * t + (g & 1)) * DPAD + d) * 2 + (g >> 1)] = x.w[0];
-                pv[((2 * (t + 1) + (g & 1)) * DPAD + d) * 2 + (g >> 1)] = x.w[1];
-            }
-        }
-        const float vtop = wave_max_nonneg(vsr);
-        float f = 1.0f;
-        if (vtop > ref) {
-            const float ref2 = pow2_above(vtop);
-            f = ref / ref2;
+    auto stage_v = [&](int n, uint8_t *to) {
+        const int u = n / 2, t = 2 * (n % 2), id = tid + 64 * NW * u, d = id / 4, g = id % 4;
+        uint2 *pv = reinterpret_cast<uint2 *>(to);
+        union {
+            h8 v;
+            uint2 w[2];
+        } x;
+        x.v = bytes_to_h8(vreg[u][t], vreg[u][t + 1]);
+        pv[((2 * t + (g & 1)) * DPAD + d) * 2 + (g >> 1)] = x.w[0];
+        pv[((2 * (t + 1) + (g & 1)) * DPAD + d) * 2 + (g >> 1)] = x.w[1];
+    };
+    // The scales, and the reference of the V_scales with the factor it asks the sums to be multiplied
+    // with before that block's are added (the same in every wave).
+    auto stage_scales = [&](float *to) {
+        grow = 1.0f;
+        ksr = lane < seen ? ksr : 0.0f;
+        vsr = lane < seen ? vsr : 0.0f;
+        if (__any(vsr > ref)) {
+            const float ref2 = pow2_above(wave_max_nonneg(vsr));
+            grow = ref / ref2;
             ref = ref2;
             vscale = WR::PSCALE / ref;
         }
         if (wave == 0) {
-            float *sc = reinterpret_cast<float *>(base + 2 * KBYTES);
-            sc[lane] = fmaxf(ksr * c, 1.17549435e-38f); // (a masked score is -inf: never times 0)
-            sc[64 + lane] = vsr * vscale;
+            to[lane] = fmaxf(ksr * c, 1.17549435e-38f); // (a masked score is -inf: never times 0)
+            to[64 + lane] = vsr * vscale;
         }
-        return f;
     };
+    constexpr int STAGE_STEPS = 4 * UNITS + 1;
 
     f16v o[DT32];
 #pragma unroll
@@ -763,69 +897,115 @@ __global__ __launch_bounds__(64 * NW, DC == 4 ? 1 : 2) void k_attn_tile(const At
         for (int r = 0; r < 16; ++r) o[d][r] = 0.0f;
     float m = 0.0f, l = 0.0f; // m: the row's reference in base 2, 0 until it is set
     bool set = false;
-    // page: of the block being multiplied; page1: of the next, whose bytes are
-    // fetched meanwhile; the one after that is looked up a block ahead
-    PageWalk walk(a, j, j.blk0);
-    int page = -1, page1 = -1;
+    float have = 0.0f; // the row's largest weight so far (what this lane saw of it)
+    f16v s[2];   // the block's scores
+    h8 p[4][NS]; // its weights, whose values are added in the next P
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+#pragma unroll
+        for (int z = 0; z < NS; ++z)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) p[x][z][e] = static_cast<_Float16>(0.0f);
+    // element e of 16-key tile t is key 16 t + 8 (e / 4) + 4 hf + e % 4
+    auto score = [&](int t, int e) { return s[t / 2][8 * (t % 2) + e]; };
+    // The weights of the round 'up' (1: those of at least LEAST) as operands; whether smaller ones are left.
+    auto share = [&](float up) {
+        bool more = false;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            float w[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = round_share<NS>(score(t, e), up, more);
+            split_weights<NS>(w, p[t]);
+        }
+        return static_cast<bool>(__any(more));
+    };
+    // Operands of P's products in the order of their use: SUM_OPS of the last block's V (16-key tile by
+    // 16-key tile, 32 columns by 32), then SCORE_OPS of K (k-step by k-step, 32 keys by 32), read AHEAD
+    // of their use.
+    constexpr int SUM_OPS = 4 * DT32, SCORE_OPS = 2 * KSTEPS, AHEAD = 8;
+    h8 ring[AHEAD];
+    const h8 *pk = nullptr, *pv = nullptr;
+    auto read_op = [&](int n) {
+        if (n < SUM_OPS) ring[n % AHEAD] = pv[(2 * (n / DT32) + hf) * DPAD + 32 * (n % DT32) + i];
+        else if (n < SUM_OPS + SCORE_OPS)
+            ring[n % AHEAD] = pk[((n - SUM_OPS) / 2 + KSTEPS * hf) * KROW + 32 * ((n - SUM_OPS) % 2) + i];
+    };
+    // Step n of adding the last block's weighted values.
+    auto sum_step = [&](int n) {
+#pragma unroll
+        for (int z = 0; z < NS; ++z)
+            o[n % DT32] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ring[n % AHEAD], p[n / DT32][z], o[n % DT32], 0, 0, 0);
+    };
+
     if (j.blk0 < j.blk1) {
-        page = walk.page(a);
-        fetch(j.blk0, page, walk.row(a, page, j.kvh));
-        (void)stage(0);
-        walk.step(j, 1);
-        if (j.blk0 + 1 < j.blk1) page1 = walk.page(a);
+#pragma unroll
+        for (int n = 0; n < 2 * UNITS; ++n) stage_k(n, k_at(0));
+        stage_scales(scales_at(0));
+        // (the first P adds zero weights of a block that is not there: its V must be finite)
+        for (int n = tid; n < VBYTES / 16; n += 64 * NW) reinterpret_cast<u4 *>(v_at(1))[n] = u4{0, 0, 0, 0};
+        if (j.blk0 + 1 < j.blk1) {
+            row1 = table.at(1);
+            fetch_k(j.blk0 + 1, row1);
+        }
     }
     __syncthreads();
+    const bool behind = NW == 8 && wave >= 4; // the half that runs one phase later
+    if (behind) __syncthreads();
+    int kbuf = 0, sbuf = 0; // places of block n's K (V the same) and scales
     for (int blk = j.blk0; blk < j.blk1; ++blk) {
-        const int buf = (blk - j.blk0) & 1;
-        const uint8_t *base = smem + buf * BUF;
-        const bool next = blk + 1 < j.blk1;
-        int page2 = -1;
-        if (next) {
-            fetch(blk + 1, page1, walk.row(a, page1, j.kvh));
-            walk.step(j, 1);
-            if (blk + 2 < j.blk1) page2 = walk.page(a);
-        }
-        // this block's list: its first key and those this row sees
+        const int snext = sbuf == 2 ? 0 : sbuf + 1;
+        // this block's list: its first key and those a row sees
         const bool pre = blk < j.nbp;
-        const int k0 = (pre ? blk : blk - j.nbp) * CACHE_BLOCK, mine = pre ? j.prefix : lim;
-        if (page >= 0 && k0 < (pre ? prefix_max : lim_max)) {
-            const h8 *pk = reinterpret_cast<const h8 *>(base), *pv = reinterpret_cast<const h8 *>(base + KBYTES);
-            const f4 *sc = reinterpret_cast<const f4 *>(base + 2 * KBYTES);
-            f16v s[2];
-            f4 kq[2][2], vq[2][2]; // scales of two 16-key tiles: keys 16 t + 8 x + 4 hf ..
-            auto read_scales = [&](int t) {
+        const int k0 = (pre ? blk : blk - j.nbp) * CACHE_BLOCK, mine = row0 < 0 ? 0 : (pre ? j.prefix : lim);
+        const bool masked = row0 < 0 || k0 + CACHE_BLOCK > (pre ? j.prefix : lim_min);
+        // ---- P(blk) ----
+        pk = reinterpret_cast<const h8 *>(k_at(kbuf));
+        pv = reinterpret_cast<const h8 *>(v_at(kbuf ^ 1));
+        const float grown = grow; // asked for by this block's scales
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    kq[t % 2][x] = sc[4 * t + 2 * x + hf];
-                    vq[t % 2][x] = sc[16 + 4 * t + 2 * x + hf];
-                }
-            };
+        for (int n = 0; n < AHEAD; ++n) read_op(n);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+        for (int n = 0; n < SUM_OPS; ++n) {
+            sum_step(n);
+            read_op(n + AHEAD);
+            __builtin_amdgcn_sched_barrier(0);
+        }
 #pragma unroll
-                for (int r = 0; r < 16; ++r) s[t][r] = 0.0f;
-            // operands are read two k-steps ahead of their products (the barriers keep
-            // the compiler from sinking the reads to their uses, one LDS latency each)
-            h8 kf[3][2];
-            auto read_k = [&](int k) {
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
-                for (int t = 0; t < 2; ++t) kf[k % 3][t] = pk[(2 * k + hf) * 64 + ((32 * t + i) ^ (k & 7))];
-            };
-            read_k(0);
-            read_k(1);
+            for (int r = 0; r < 16; ++r) s[t][r] = 0.0f;
 #pragma unroll
-            for (int k = 0; k < KSTEPS; ++k) {
-                if (k + 2 < KSTEPS) read_k(k + 2);
-                if (k + 1 == KSTEPS) read_scales(0);
-                __builtin_amdgcn_sched_barrier(0);
+        for (int n = 0; n < SCORE_OPS; ++n) {
+            const int k = n / 2, t = n % 2, at = SUM_OPS + n;
 #pragma unroll
-                for (int z = 0; z < NS; ++z)
+            for (int z = 0; z < NS; ++z)
+                s[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ring[at % AHEAD], q[k][z], s[t], 0, 0, 0);
+            read_op(at + AHEAD);
+            // (after the last block the next K is bytes nothing reads)
 #pragma unroll
-                    for (int t = 0; t < 2; ++t)
-                        s[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf[k % 3][t], q[k][z], s[t], 0, 0, 0);
+            for (int x = n * STAGE_STEPS / SCORE_OPS; x < (n + 1) * STAGE_STEPS / SCORE_OPS; ++x) {
+                if (x < 2 * UNITS) stage_k(x, k_at(kbuf ^ 1));
+                else if (x < 4 * UNITS) stage_v(x - 2 * UNITS, v_at(kbuf));
+                else stage_scales(scales_at(snext));
             }
             __builtin_amdgcn_sched_barrier(0);
-            const bool masked = k0 + CACHE_BLOCK > (pre ? j.prefix : lim_min);
+        }
+        const int64_t this_row = row0;
+        row0 = row1;
+        if (blk + 1 < j.blk1) fetch_v(row1);
+        if (blk + 2 < j.blk1) {
+            const int x = blk + 2 - j.blk0;
+            if (x % 64 == 0) table.load(a, j, blk + 2);
+            row1 = table.at(x % 64);
+            fetch_k(blk + 2, row1);
+        }
+        if constexpr (NW == 8) __syncthreads();
+
+        // ---- W(blk) ----
+        {
+            const f4 *sc = reinterpret_cast<const f4 *>(scales_at(sbuf));
             if (masked) {
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
@@ -835,34 +1015,46 @@ __global__ __launch_bounds__(64 * NW, DC == 4 ? 1 : 2) void k_attn_tile(const At
                         s[t][r] = key < mine ? s[t][r] : neg_inf();
                     }
             }
-            // element e of 16-key tile t is key 16 t + 8 (e / 4) + 4 hf + e % 4
-            auto score = [&](int t, int e) { return s[t / 2][8 * (t % 2) + e]; };
-            h8 p[4][NS];
-            float sum = 0.0f, big, small;
+            // two keys a step; scales of a quad of keys, 8 x + 4 hf .., are read two quads ahead
+            f4 kq[3], vq[3];
+            auto read_scales = [&](int x) {
+                kq[x % 3] = sc[2 * x + hf];
+                vq[x % 3] = sc[16 + 2 * x + hf];
+            };
+            float sum = 0.0f;
+            read_scales(0);
+            read_scales(1);
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                if (t < 3) read_scales(t + 1);
-                __builtin_amdgcn_sched_barrier(0);
-                float w[8];
+            for (int n = 0; n < 16; ++n) {
+                const int t = n / 4, e = 2 * (n % 4), quad = n / 2;
+                if (n % 2 == 0 && quad + 2 < 8) read_scales(quad + 2);
+                float w[2];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float y = __builtin_amdgcn_exp2f(__builtin_fmaf(score(t, e), kq[t % 2][e / 4][e % 4], -m));
+                for (int x = 0; x < 2; ++x) {
+                    const float y =
+                        __builtin_amdgcn_exp2f(__builtin_fmaf(score(t, e + x), kq[quad % 3][(e + x) % 4], -m));
                     sum += y;
-                    w[e] = y * vq[t % 2][e / 4][e % 4];
+                    w[x] = y * vq[quad % 3][(e + x) % 4];
                 }
-                split_weights<NS>(w, p[t]);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const _Float16 hi = static_cast<_Float16>(w[x]);
+                    p[t][0][e + x] = hi;
+                    if constexpr (NS == 2) p[t][1][e + x] = static_cast<_Float16>(w[x] - static_cast<float>(hi));
+                }
+                if (n % 2 == 1) __builtin_amdgcn_sched_barrier(0);
             }
+            float big, small;
             weight_range(p, big, small);
-            if (masked) { // (masked weights are 0 and call for no round)
+            if (masked) { // (masked weights are 0 and call for nothing)
                 small = WR::LEAST;
 #pragma unroll
                 for (int e = 0; e < 32; ++e)
                     small = score(e / 8, e % 8) > neg_inf() ? fminf(small, static_cast<float>(p[e / 8][0][e % 8])) : small;
             }
-            if (__any((!set && k0 < mine) || !(big <= H_MAX) || !(sum <= SUM_MAX) || small < WR::LEAST)) {
-                // the general form: the reference brought to this block's largest score, small weights in
-                // rounds (the scales are read again, not kept)
-                int at = hf;
+            if (grown != 1.0f || __any((!set && k0 < mine) || !(big <= H_MAX) || !(sum <= SUM_MAX) || small < WR::LEAST)) {
+                // the general form: the references brought to the block's, small weights in rounds
+                int at = hf; // (the scales are read again, not kept)
                 asm volatile("" : "+v"(at));
                 float top = neg_inf();
 #pragma unroll
@@ -877,14 +1069,18 @@ __global__ __launch_bounds__(64 * NW, DC == 4 ? 1 : 2) void k_attn_tile(const At
                         }
                     }
                 top = max_across32(top);
-                const bool raise = top > neg_inf() && (!set || top > m);
+                big = max_across32(big);
+                sum = max_across32(sum);
+                const bool raise = top > neg_inf() && (!set || (top > m && (!(big <= H_MAX) || !(sum <= SUM_MAX))));
                 const float f = raise && set ? __builtin_amdgcn_exp2f(m - top) : 1.0f;
                 m = raise ? top : m;
                 set = set || raise;
                 l *= f;
 #pragma unroll
-                for (int d = 0; d < DT32; ++d) o[d] *= f;
+                for (int d = 0; d < DT32; ++d) o[d] *= f * grown;
                 sum = 0.0f;
+                big = 0.0f;
+                small = WR::LEAST;
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
 #pragma unroll
@@ -893,73 +1089,88 @@ __global__ __launch_bounds__(64 * NW, DC == 4 ? 1 : 2) void k_attn_tile(const At
 #pragma unroll
                         for (int r = 0; r < 4; ++r) {
                             const float y = __builtin_amdgcn_exp2f(score(t, 4 * x + r) - m);
+                            const float w = y * v4[r];
                             sum += y;
-                            s[t / 2][8 * (t % 2) + 4 * x + r] = y * v4[r];
+                            s[t / 2][8 * (t % 2) + 4 * x + r] = w;
+                            big = fmaxf(big, w);
+                            small = w > 0.0f ? fminf(small, w) : small;
                         }
                     }
-                auto share = [&](float up, bool &more) {
-                    more = false;
+                have = max_across32(fmaxf(have * (f * grown), big));
+                big = 0.0f; // (it is in have)
+                if (__any(small < WR::LEAST)) {
+                    small = -max_across32(-small);
+                    const float up = small < WR::LEAST ? lift(have, max_across32(l + sum)) : 1.0f;
+                    m -= __builtin_log2f(up);
+                    l *= up;
+                    sum *= up;
+                    have *= up;
+#pragma unroll
+                    for (int d = 0; d < DT32; ++d) o[d] *= up;
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) s[t] *= up;
+                    small *= up;
+                }
+                if (!__any(small < WR::LEAST)) {
 #pragma unroll
                     for (int t = 0; t < 4; ++t) {
                         float w[8];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) w[e] = round_share<NS>(score(t, e), up, more);
+                        for (int e = 0; e < 8; ++e) w[e] = score(t, e);
                         split_weights<NS>(w, p[t]);
                     }
-                    more = __any(more);
-                };
-                bool more;
-                share(1.0f, more);
-                if (more) {
-                    for (float up = WR::STEP, down = 1.0f / WR::STEP; more; up *= WR::STEP, down *= 1.0f / WR::STEP) {
-                        share(up, more);
+                } else if (share(1.0f)) {
+                    // rounds, with V's bytes from memory (another wave may not have written them to LDS yet)
+                    const uint8_t *v8 = reinterpret_cast<const uint8_t *>(a.c.V + (this_row < 0 ? 0 : this_row) * Dp);
+                    uint32_t lane_d = i; // (opaque: addresses are formed here, not kept across the blocks)
+                    asm volatile("" : "+v"(lane_d));
+                    float down = 1.0f / WR::STEP;
+                    bool more = true;
+                    for (float up = WR::STEP; more; up *= WR::STEP, down *= 1.0f / WR::STEP) {
+                        more = share(up);
 #pragma unroll
                         for (int d = 0; d < DT32; ++d) {
+                            const uint32_t col = 32 * d + lane_d;
+                            const uint32_t *row = reinterpret_cast<const uint32_t *>(
+                                v8 + (static_cast<int>(col) < Dp ? col : 0u) * CACHE_BLOCK);
                             f16v x;
 #pragma unroll
                             for (int r = 0; r < 16; ++r) x[r] = 0.0f;
 #pragma unroll
-                            for (int t = 0; t < 4; ++t) {
-                                const h8 vv = pv[(2 * t + hf) * DPAD + 32 * d + i];
+                            for (int t = 0; t < 4; ++t) { // quads hf and hf + 2 of tile t
+                                const h8 vv = bytes_to_h8(row[4 * hf + t], row[4 * (hf + 2) + t]);
 #pragma unroll
-                                for (int z = 0; z < NS; ++z) x = __builtin_amdgcn_mfma_f32_32x32x16_f16(vv, p[t][z], x, 0, 0, 0);
+                                for (int z = 0; z < NS; ++z)
+                                    x = __builtin_amdgcn_mfma_f32_32x32x16_f16(vv, p[t][z], x, 0, 0, 0);
                             }
                             o[d] += x * down;
                             __builtin_amdgcn_sched_barrier(0); // one tile's registers at a time
                         }
                     }
-                    share(1.0f, more);
+                    (void)share(1.0f);
                 }
             }
             l += sum;
-            h8 vv[2][DT32];
-#pragma unroll
-            for (int d = 0; d < DT32; ++d) vv[0][d] = pv[hf * DPAD + 32 * d + i];
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                if (t < 3)
-#pragma unroll
-                    for (int d = 0; d < DT32; ++d) vv[(t + 1) % 2][d] = pv[(2 * (t + 1) + hf) * DPAD + 32 * d + i];
-                __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-                for (int z = 0; z < NS; ++z)
-#pragma unroll
-                    for (int d = 0; d < DT32; ++d)
-                        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vv[t % 2][d], p[t][z], o[d], 0, 0, 0);
-            }
+            have = fmaxf(have, big);
         }
-        if (next) {
-            const float f = stage(buf ^ 1);
-            if (f != 1.0f) {
-#pragma unroll
-                for (int d = 0; d < DT32; ++d) o[d] *= f;
-            }
-        }
-        page = page1;
-        page1 = page2;
+        kbuf ^= 1;
+        sbuf = snext;
         __syncthreads();
     }
-    l += __shfl_xor(l, 32);
+    pk = nullptr;
+    pv = reinterpret_cast<const h8 *>(v_at(kbuf ^ 1));
+    if (j.blk0 < j.blk1) {
+#pragma unroll
+        for (int n = 0; n < SUM_OPS; ++n) {
+            if (n % AHEAD == 0) {
+#pragma unroll
+                for (int x = 0; x < AHEAD; ++x) read_op(n + x);
+            }
+            sum_step(n);
+        }
+    }
+    if (NW == 8 && !behind) __syncthreads();
+    l = sum_across32(l);
     if (rho < j.rows) {
         const int rr = j.row0 + rho, head = j.kvh * G + rr % G;
         const int64_t tok = j.tok0 + rr / G, at = part_index(a, j.part, tok, head);
@@ -1081,23 +1292,25 @@ namespace {
 
 int64_t div_up(int64_t x, int64_t y) { return (x + y - 1) / y; }
 
-// Rows a workgroup takes: 16 with k_attn_stream, 128 or 256 (4 or 8 waves) with
-// k_attn_tile.  Eight waves share one staging of the keys where their registers
-// allow two waves per SIMD (head_dim in (64, 128]).
-int tile_rows(int64_t rows, int64_t head_dim)
+// Rows a workgroup takes: 16 with k_attn_stream, 128 or 256 (four or eight waves)
+// with k_attn_tile.  Eight waves share a conversion of the keys; they need two
+// waves a SIMD.
+int tile_rows(int64_t rows, int64_t head_dim, int dtype)
 {
-    return rows <= 16 ? 16 : rows <= 128 || head_dim <= 64 || head_dim > 128 ? 128 : 256;
+    return rows <= 16 ? 16 : rows <= 128 || head_dim <= 64 || head_dim > 128 || dtype == DT_F32 ? 128 : 256;
 }
 
-// Splits of 'blocks' key blocks for 'wgs' workgroups of 'rows' rows: the count with
-// the least time, in blocks, of all rounds of the 256 CUs (two workgroups each; one
-// of eight waves), a workgroup costing its blocks and about four more for its start
-// and end; a split more costs its sums' way through memory.
-void choose_splits(int64_t wgs, int64_t blocks, int rows, int *chunk, int *splits)
+// Splits of 'blocks' key blocks for 'wgs' workgroups: the count with the least
+// time, in blocks, of all rounds of the 256 CUs, a workgroup costing its blocks and
+// about four more for its start and end; a split more costs its sums' way through
+// memory.
+void choose_splits(int64_t wgs, int64_t blocks, int rows, int64_t head_dim, int dtype, int *chunk, int *splits)
 {
     *chunk = *splits = 0;
     if (blocks == 0) return;
-    const int64_t slots = rows == 256 ? 256 : 512, least = rows == 16 ? 4 : 2; // (k_attn_stream: a block for each wave)
+    const int dc = head_dim <= 64 ? 1 : head_dim <= 128 ? 2 : 4;
+    const bool alone = rows == 16 ? dc == 4 : rows == 256 || tile_one_wave(dtype, dc); // one workgroup a CU, or two
+    const int64_t slots = alone ? 256 : 512, least = rows == 16 ? 4 : 2; // (k_attn_stream: a block for each wave)
     int64_t best = -1;
     for (int64_t s = 1; s <= 64 && (s == 1 || div_up(blocks, s) >= least); ++s) {
         const int64_t c = div_up(blocks, s), n = div_up(blocks, c);
@@ -1115,21 +1328,21 @@ void choose_splits(int64_t wgs, int64_t blocks, int rows, int *chunk, int *split
 constexpr int64_t kJointBytes = int64_t(16) << 20;
 
 AttnPlan attn_plan(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t seqs, int64_t max_q,
-                   int64_t max_own, int64_t prefix)
+                   int64_t max_own, int64_t prefix, int dtype)
 {
     AttnPlan p;
     const int64_t G = heads / kv_heads, dp = div_up(head_dim, 16) * 16;
     const int64_t nbp = div_up(prefix, CACHE_BLOCK), nbo = div_up(max_own, CACHE_BLOCK);
-    p.rows_prefix = tile_rows(tokens * G, head_dim);
-    p.rows_own = tile_rows(max_q * G, head_dim);
+    p.rows_prefix = tile_rows(tokens * G, head_dim, dtype);
+    p.rows_own = tile_rows(max_q * G, head_dim, dtype);
     p.tiles_own = static_cast<int>(div_up(max_q * G, p.rows_own));
     // one pass over prefix and own keys where a sequence fills row tiles of its own anyway, or the
     // prefix is short
     p.joint = nbp > 0 && (p.rows_own > 16 || 2 * prefix * kv_heads * dp * (seqs - 1) <= kJointBytes);
     const int64_t tp = p.joint || nbp == 0 ? 0 : div_up(tokens * G, p.rows_prefix);
     p.chunk_prefix = p.splits_prefix = 0;
-    if (tp > 0) choose_splits(tp * kv_heads, nbp, p.rows_prefix, &p.chunk_prefix, &p.splits_prefix);
-    choose_splits(seqs * p.tiles_own * kv_heads, p.joint ? nbp + nbo : nbo, p.rows_own, &p.chunk_own, &p.splits_own);
+    if (tp > 0) choose_splits(tp * kv_heads, nbp, p.rows_prefix, head_dim, dtype, &p.chunk_prefix, &p.splits_prefix);
+    choose_splits(seqs * p.tiles_own * kv_heads, p.joint ? nbp + nbo : nbo, p.rows_own, head_dim, dtype, &p.chunk_own, &p.splits_own);
     p.wgs_prefix = static_cast<int>(tp * kv_heads * p.splits_prefix);
     p.wgs_own = static_cast<int>(seqs * p.tiles_own * kv_heads * p.splits_own);
     p.wg0 = 0;
@@ -1156,7 +1369,7 @@ hipError_t launch_part(const AttnArgs &a, AttnPlan pl, int rows, int wg0, int wg
         if (dc == 1) BL_TILE(1, 4);
         else if (dc == 2) BL_TILE(2, 4);
         else BL_TILE(4, 4);
-    } else {
+    } else if constexpr (DT == DT_BF16) {
         BL_TILE(2, 8);
     }
 #undef BL_STREAM
@@ -1191,16 +1404,23 @@ hipError_t launch_attn(const AttnArgs &a, const AttnPlan &pl, hipStream_t st)
 
 } // namespace
 
+// Room for either type's plan.
 int64_t attn_workspace_bytes(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t seqs,
                              int64_t max_q, int64_t max_own, int64_t prefix)
 {
-    const AttnPlan p = attn_plan(tokens, heads, kv_heads, head_dim, seqs, max_q, max_own, prefix);
-    return p.direct ? 0 : (p.ml_off + 2 * (p.splits_prefix + p.splits_own) * tokens * heads) * 4;
+    int64_t most = 0;
+    for (const int dtype : {DT_F32, DT_BF16}) {
+        const AttnPlan p = attn_plan(tokens, heads, kv_heads, head_dim, seqs, max_q, max_own, prefix, dtype);
+        const int64_t need = p.direct ? 0 : (p.ml_off + 2 * (p.splits_prefix + p.splits_own) * tokens * heads) * 4;
+        most = need > most ? need : most;
+    }
+    return most;
 }
 
 hipError_t launch_attention(const AttnArgs &a, hipStream_t stream)
 {
-    const AttnPlan p = attn_plan(a.tokens, a.heads, a.c.heads, a.c.D, a.seqs, a.max_q, a.max_own, a.prefix);
+    const AttnPlan p =
+        attn_plan(a.tokens, a.heads, a.c.heads, a.c.D, a.seqs, a.max_q, a.max_own, a.prefix, a.dtype);
     return a.dtype == DT_F32 ? launch_attn<DT_F32>(a, p, stream) : launch_attn<DT_BF16>(a, p, stream);
 }
 
