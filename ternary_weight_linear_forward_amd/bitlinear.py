@@ -338,14 +338,21 @@ def _torch():
 
 
 def _stream(stream=None) -> int:
+    if stream is not None:
+        return int(stream.cuda_stream)
     torch = _torch()
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return int(s.cuda_stream)
+    # the current stream's handle without a Stream object around it (0.4 us instead of 3)
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+
+
+_CODES: dict = {}
 
 
 def _dtype_code(t) -> int:
-    torch = _torch()
-    return {torch.float32: F32, torch.bfloat16: BF16, torch.int8: I8, torch.int32: I32}[t.dtype]
+    if not _CODES:
+        torch = _torch()
+        _CODES.update({torch.float32: F32, torch.bfloat16: BF16, torch.int8: I8, torch.int32: I32})
+    return _CODES[t.dtype]
 
 
 def _ptr(t) -> int | None:
@@ -568,10 +575,24 @@ def backward_dw(Xq, beta, dY, K: int, out=None, stream=None):
     return out
 
 
-def _rows_contiguous(t, where: str, *dtypes) -> None:
-    """Refuses a tensor whose last dimension has gaps, or of another dtype."""
-    if (dtypes and t.dtype not in dtypes) or (t.shape[-1] > 1 and t.stride(-1) != 1):
+def _row_stride(t, where: str, M: int, K: int, *dtypes) -> int:
+    """Row stride of a tensor [M x K] (at least K for a single row); refuses other
+    shapes, other dtypes and rows with gaps."""
+    if t.dtype not in dtypes or t.shape != (M, K):
         raise BitlinearError(ERR_INVALID_ARG, where)
+    ld, step = t.stride()
+    if step != 1 and K > 1:
+        raise BitlinearError(ERR_INVALID_ARG, where)
+    return ld if M > 1 else max(ld, K)
+
+
+def _norm_weight(w, K: int, where: str) -> int | None:
+    torch = _torch()
+    if w is None:
+        return None
+    if w.dtype != torch.float32 or w.shape != (K,) or (K > 1 and w.stride(0) != 1):
+        raise BitlinearError(ERR_INVALID_ARG, where)
+    return w.data_ptr()
 
 
 def norm_quantize(X, w=None, eps: float = 1e-5, residual=None, H=None, keep_h: bool = True, layout: int | None = None,
@@ -585,43 +606,41 @@ def norm_quantize(X, w=None, eps: float = 1e-5, residual=None, H=None, keep_h: b
     torch = _torch()
     name = "norm_quantize"
     M, K = X.shape
-    fl = (torch.float32, torch.bfloat16)
-    _rows_contiguous(X, name, *fl)
-    ref = X if residual is None else residual
-    _rows_contiguous(ref, name, *fl)
-    if ref.shape != X.shape or (w is not None and (w.shape != (K,) or w.dtype != torch.float32 or
-                                                   (K > 1 and w.stride(0) != 1))):
-        raise BitlinearError(ERR_INVALID_ARG, name)
-    if H is None and keep_h:
-        H = torch.empty((M, K), dtype=ref.dtype, device=X.device)
+    device = X.device
+    ldx = _row_stride(X, name, M, K, torch.float32, torch.bfloat16)
+    ref, ldr = X, 0
+    if residual is not None:
+        ref, ldr = residual, _row_stride(residual, name, M, K, torch.float32, torch.bfloat16)
+    wp = _norm_weight(w, K, name)
+    ldh = 0
     if H is not None:
-        _rows_contiguous(H, name, ref.dtype)
-        if H.shape != X.shape:
-            raise BitlinearError(ERR_INVALID_ARG, name)
+        ldh = _row_stride(H, name, M, K, ref.dtype)
+    elif keep_h:
+        H, ldh = torch.empty((M, K), dtype=ref.dtype, device=device), K
     if layout is None:
         ldq = (K + 15) // 16 * 16
-        Xq = torch.empty((M, ldq), dtype=torch.int8, device=X.device)
+        Xq = torch.empty((M, ldq), dtype=torch.int8, device=device)
     else:
         ldq, nbytes = 0, bitlinear_act_tiled_bytes(M, K, layout)
         if nbytes < 0:
             raise BitlinearError(ERR_INVALID_ARG, name)
-        Xq = torch.empty(nbytes, dtype=torch.int8, device=X.device)
-    beta = torch.empty(M, dtype=torch.float32, device=X.device)
+        Xq = torch.empty(nbytes, dtype=torch.int8, device=device)
+    beta = torch.empty(M, dtype=torch.float32, device=device)
     _check(_lib.bitlinear_norm_quantize(
-        X.data_ptr(), _dtype_code(X), M, K, _ld(X), _ptr(residual), 0 if residual is None else _ld(residual), _ptr(w),
-        eps, _ptr(H), _dtype_code(ref), 0 if H is None else _ld(H), Xq.data_ptr(), I8 if layout is None else I8_TILED,
-        ldq, LAYOUT_I2 if layout is None else layout, beta.data_ptr(), _stream(stream)), "bitlinear_norm_quantize")
-    _record(stream, H, Xq, beta)
+        X.data_ptr(), _dtype_code(X), M, K, ldx, _ptr(residual), ldr, wp, eps, _ptr(H), _dtype_code(ref), ldh,
+        Xq.data_ptr(), I8 if layout is None else I8_TILED, ldq, LAYOUT_I2 if layout is None else layout,
+        beta.data_ptr(), _stream(stream)), "bitlinear_norm_quantize")
+    if stream is not None:
+        _record(stream, H, Xq, beta)
     return H, Xq, beta
 
 
 def _record(stream, *tensors) -> None:
     """Tensors allocated here and used on another stream than the current one
     must not be handed out again before that stream is done with them."""
-    if stream is not None:
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
 
 
 def _ld(t) -> int:
@@ -632,12 +651,15 @@ def _ld(t) -> int:
 def dequantize_act(Xq, beta, K: int, dtype=None, out=None, stream=None):
     """The values of int8 rows Xq [M x >=K] with beta [M]: q * (beta / 127), fp32 or bf16 [M x K]."""
     torch = _torch()
-    M = Xq.shape[0]
+    M, ldq = Xq.shape[0], _ld(Xq)
     if out is None:
-        out = torch.empty((M, K), dtype=dtype or torch.float32, device=Xq.device)
-    _check(_lib.bitlinear_dequantize_act(Xq.data_ptr(), _ld(Xq), beta.data_ptr(), M, K, out.data_ptr(),
-                                         _dtype_code(out), _ld(out), _stream(stream)), "bitlinear_dequantize_act")
-    _record(stream, out)
+        out, ldv = torch.empty((M, K), dtype=dtype or torch.float32, device=Xq.device), K
+    else:
+        ldv = _ld(out)
+    _check(_lib.bitlinear_dequantize_act(Xq.data_ptr(), ldq, beta.data_ptr(), M, K, out.data_ptr(), _dtype_code(out),
+                                         ldv, _stream(stream)), "bitlinear_dequantize_act")
+    if stream is not None:
+        _record(stream, out)
     return out
 
 
@@ -648,16 +670,15 @@ def norm_backward(dY, H, w=None, eps: float = 1e-5, dH=None, dX=None, want_dw: b
     torch = _torch()
     name = "norm_backward"
     M, K = H.shape
-    _rows_contiguous(dY, name, torch.float32)
-    _rows_contiguous(H, name, torch.float32, torch.bfloat16)
+    dtype = H.dtype
+    lddy = _row_stride(dY, name, M, K, torch.float32)
+    ldh = _row_stride(H, name, M, K, torch.float32, torch.bfloat16)
+    lddh = 0 if dH is None else _row_stride(dH, name, M, K, dtype)
     if dX is None:
-        dX = torch.empty((M, K), dtype=H.dtype, device=H.device)
-    for t in (dH, dX):
-        if t is not None:
-            _rows_contiguous(t, name, H.dtype)
-    if any(t is not None and t.shape != H.shape for t in (dY, dH, dX)) or \
-            (w is not None and (w.shape != (K,) or w.dtype != torch.float32 or (K > 1 and w.stride(0) != 1))):
-        raise BitlinearError(ERR_INVALID_ARG, name)
+        dX, lddx = torch.empty((M, K), dtype=dtype, device=H.device), K
+    else:
+        lddx = _row_stride(dX, name, M, K, dtype)
+    wp = _norm_weight(w, K, name)
     dW = torch.empty(K, dtype=torch.float32, device=H.device) if want_dw else None
     nws = _lib.bitlinear_norm_backward_workspace_bytes(M, K, 1 if want_dw else 0)
     if nws < 0:
@@ -665,10 +686,10 @@ def norm_backward(dY, H, w=None, eps: float = 1e-5, dH=None, dX=None, want_dw: b
     if nws > 0 and (ws is None or ws.numel() < nws):
         ws = torch.empty(nws, dtype=torch.uint8, device=H.device)
     _check(_lib.bitlinear_norm_backward(
-        dY.data_ptr(), _ld(dY), H.data_ptr(), _dtype_code(H), _ld(H), _ptr(w), eps, _ptr(dH),
-        0 if dH is None else _ld(dH), M, K, dX.data_ptr(), _ld(dX), _ptr(dW), _ptr(ws) if nws > 0 else None, nws,
-        _stream(stream)), "bitlinear_norm_backward")
-    _record(stream, dX, dW, ws)
+        dY.data_ptr(), lddy, H.data_ptr(), _dtype_code(H), ldh, wp, eps, _ptr(dH), lddh, M, K, dX.data_ptr(), lddx,
+        _ptr(dW), _ptr(ws) if nws > 0 else None, nws, _stream(stream)), "bitlinear_norm_backward")
+    if stream is not None:
+        _record(stream, dX, dW, ws)
     return dX, dW
 
 
@@ -681,8 +702,9 @@ class KVCache:
     def __init__(self, k, v, k_scale, v_scale, head_dim: int):
         torch = _torch()
         pages, heads, page_tokens, dp = k.shape
+        scales = (pages, heads, page_tokens)
         if v.shape != (pages, heads, page_tokens // 64, dp, 64) or page_tokens % 64 or \
-                dp != (head_dim + 15) // 16 * 16 or k_scale.shape != k.shape[:3] or v_scale.shape != k.shape[:3] or \
+                dp != (head_dim + 15) // 16 * 16 or k_scale.shape != scales or v_scale.shape != scales or \
                 k.dtype != torch.int8 or v.dtype != torch.int8 or k_scale.dtype != torch.float32 or \
                 v_scale.dtype != torch.float32 or not (k.is_contiguous() and v.is_contiguous() and
                                                        k_scale.is_contiguous() and v_scale.is_contiguous()):
@@ -705,11 +727,15 @@ class KVCache:
                    new(pages, heads, page_tokens, dtype=torch.float32), head_dim)
 
 
-def _kv_rows(cache, t, tokens, where):
+def _kv_strides(cache, t, tokens, where):
+    """Token and head stride of a tensor [tokens x heads x head_dim] of the cache's heads."""
     torch = _torch()
-    _rows_contiguous(t, where, torch.float32, torch.bfloat16)
-    if t.shape != (tokens, cache.heads, cache.head_dim):
+    if (t.dtype != torch.bfloat16 and t.dtype != torch.float32) or t.shape != (tokens, cache.heads, cache.head_dim):
         raise BitlinearError(ERR_INVALID_ARG, where)
+    lt, lh, step = t.stride()
+    if step != 1 and cache.head_dim > 1:
+        raise BitlinearError(ERR_INVALID_ARG, where)
+    return lt, lh
 
 
 def cache_write(cache: KVCache, K, V, slots, stream=None) -> None:
@@ -717,13 +743,12 @@ def cache_write(cache: KVCache, K, V, slots, stream=None) -> None:
     slots (int64 [tokens]; a slot outside the cache is skipped)."""
     torch = _torch()
     n = slots.numel()
-    _kv_rows(cache, K, n, "cache_write")
-    _kv_rows(cache, V, n, "cache_write")
+    lkt, lkh = _kv_strides(cache, K, n, "cache_write")
+    lvt, lvh = _kv_strides(cache, V, n, "cache_write")
     if K.dtype != V.dtype or slots.dtype != torch.int64 or not slots.is_contiguous():
         raise BitlinearError(ERR_INVALID_ARG, "cache_write")
-    _check(_lib.bitlinear_cache_write(cache.desc, K.data_ptr(), K.stride(0), K.stride(1), V.data_ptr(), V.stride(0),
-                                      V.stride(1), _dtype_code(K), n, slots.data_ptr(), _stream(stream)),
-           "bitlinear_cache_write")
+    _check(_lib.bitlinear_cache_write(cache.desc, K.data_ptr(), lkt, lkh, V.data_ptr(), lvt, lvh, _dtype_code(K), n,
+                                      slots.data_ptr(), _stream(stream)), "bitlinear_cache_write")
 
 
 def cache_read(cache: KVCache, slots, dtype=None, stream=None):
@@ -732,12 +757,13 @@ def cache_read(cache: KVCache, slots, dtype=None, stream=None):
     n = slots.numel()
     if slots.dtype != torch.int64 or not slots.is_contiguous():
         raise BitlinearError(ERR_INVALID_ARG, "cache_read")
-    K = torch.empty((n, cache.heads, cache.head_dim), dtype=dtype or torch.bfloat16, device=slots.device)
+    H, D = cache.heads, cache.head_dim
+    K = torch.empty((n, H, D), dtype=dtype or torch.bfloat16, device=slots.device)
     V = torch.empty_like(K)
-    _check(_lib.bitlinear_cache_read(cache.desc, slots.data_ptr(), n, K.data_ptr(), K.stride(0), K.stride(1),
-                                     V.data_ptr(), V.stride(0), V.stride(1), _dtype_code(K), _stream(stream)),
-           "bitlinear_cache_read")
-    _record(stream, K, V)
+    _check(_lib.bitlinear_cache_read(cache.desc, slots.data_ptr(), n, K.data_ptr(), H * D, D, V.data_ptr(), H * D, D,
+                                     _dtype_code(K), _stream(stream)), "bitlinear_cache_read")
+    if stream is not None:
+        _record(stream, K, V)
     return K, V
 
 
@@ -752,16 +778,23 @@ def attention(cache: KVCache, Q, own_pages, own_len, max_own: int, prefix_pages=
     name = "attention"
     tokens, heads, D = Q.shape
     seqs = own_len.numel()
-    _rows_contiguous(Q, name, torch.float32, torch.bfloat16)
+    pt, i32 = cache.page_tokens, torch.int32
+    if (Q.dtype != torch.bfloat16 and Q.dtype != torch.float32) or D != cache.head_dim or own_pages.dim() != 2:
+        raise BitlinearError(ERR_INVALID_ARG, name)
+    lqt, lqh, step = Q.stride()
     if out is None:
-        out = torch.empty((tokens, heads, D), dtype=Q.dtype, device=Q.device)
-    _rows_contiguous(out, name, Q.dtype)
-    pt = cache.page_tokens
-    ints = [t for t in (own_pages, own_len, q_start, prefix_pages) if t is not None]
-    if D != cache.head_dim or out.shape != Q.shape or any(t.dtype != torch.int32 for t in ints) or \
-            own_pages.dim() != 2 or own_pages.shape[0] != seqs or own_pages.shape[1] * pt < max_own or \
-            (own_pages.shape[1] > 1 and own_pages.stride(1) != 1) or not own_len.is_contiguous() or \
-            (q_start is not None and (q_start.numel() != seqs + 1 or not q_start.is_contiguous())) or \
+        out, lot, loh, ostep = torch.empty((tokens, heads, D), dtype=Q.dtype, device=Q.device), heads * D, D, 1
+    else:
+        if out.dtype != Q.dtype or out.shape != Q.shape:
+            raise BitlinearError(ERR_INVALID_ARG, name)
+        lot, loh, ostep = out.stride()
+    rows, cols = own_pages.shape
+    ldp, pstep = own_pages.stride()
+    if (D > 1 and (step != 1 or ostep != 1)) or rows != seqs or cols * pt < max_own or (cols > 1 and pstep != 1) or \
+            own_pages.dtype != i32 or own_len.dtype != i32 or not own_len.is_contiguous() or \
+            (q_start is not None and (q_start.dtype != i32 or q_start.numel() != seqs + 1 or
+                                      not q_start.is_contiguous())) or \
+            (prefix_pages is not None and prefix_pages.dtype != i32) or \
             (prefix_len > 0 and (prefix_pages is None or prefix_pages.numel() * pt < prefix_len or
                                  not prefix_pages.is_contiguous())):
         raise BitlinearError(ERR_INVALID_ARG, name)
@@ -772,9 +805,10 @@ def attention(cache: KVCache, Q, own_pages, own_len, max_own: int, prefix_pages=
         ws = torch.empty(nws, dtype=torch.uint8, device=Q.device)
     lse = torch.empty((tokens, heads), dtype=torch.float32, device=Q.device) if return_lse else None
     _check(_lib.bitlinear_attention(
-        cache.desc, Q.data_ptr(), _dtype_code(Q), tokens, heads, Q.stride(0), Q.stride(1), seqs, _ptr(q_start), max_q,
-        own_pages.data_ptr(), _ld(own_pages), own_len.data_ptr(), max_own, _ptr(prefix_pages), prefix_len,
-        D ** -0.5 if scale is None else scale, out.data_ptr(), out.stride(0), out.stride(1), _ptr(lse),
+        cache.desc, Q.data_ptr(), _dtype_code(Q), tokens, heads, lqt, lqh, seqs, _ptr(q_start), max_q,
+        own_pages.data_ptr(), ldp if rows > 1 else max(ldp, cols), own_len.data_ptr(), max_own, _ptr(prefix_pages),
+        prefix_len, D ** -0.5 if scale is None else scale, out.data_ptr(), lot, loh, _ptr(lse),
         _ptr(ws) if nws > 0 else None, nws, _stream(stream)), "bitlinear_attention")
-    _record(stream, out, lse, ws)
+    if stream is not None:
+        _record(stream, out, lse, ws)
     return (out, lse) if return_lse else out
