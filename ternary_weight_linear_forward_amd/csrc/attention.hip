@@ -285,46 +285,6 @@ __device__ __forceinline__ int64_t part_index(const AttnArgs &a, int part, int64
     return (static_cast<int64_t>(part) * a.tokens + tok) * a.heads + head;
 }
 
-// Walks a job's blocks: the page of the block (-1 where it lies outside the
-// cache) and the block's first row in the page's head.
-struct PageWalk {
-    const int32_t *pages;
-    int blk, pi, po, bpp; // block, page list entry, block in the page, blocks a page
-    bool own;
-    __device__ __forceinline__ PageWalk(const AttnArgs &a, const AttnJob &j, int b) : bpp(a.c.page_tokens / CACHE_BLOCK)
-    {
-        blk = b;
-        own = b >= j.nbp;
-        pages = own ? j.own_pages : j.prefix_pages;
-        enter(own ? b - j.nbp : b);
-    }
-    __device__ __forceinline__ void enter(int rel)
-    {
-        pi = rel / bpp;
-        po = rel - pi * bpp;
-    }
-    __device__ __forceinline__ void step(const AttnJob &j, int n)
-    {
-        blk += n;
-        if (!own && blk >= j.nbp) {
-            own = true;
-            pages = j.own_pages;
-            enter(blk - j.nbp);
-        } else {
-            for (po += n; po >= bpp; po -= bpp) ++pi;
-        }
-    }
-    __device__ __forceinline__ int page(const AttnArgs &a) const
-    {
-        const int p = pages[pi];
-        return p >= 0 && p < a.c.pages ? p : -1;
-    }
-    __device__ __forceinline__ int64_t row(const AttnArgs &a, int page, int kvh) const
-    {
-        return cache_row0(a.c, page < 0 ? 0 : page, kvh) + po * CACHE_BLOCK;
-    }
-};
-
 // Four columns of a row's result: o / l, rounded once to the output's type.
 template <int DT>
 __device__ __forceinline__ void store_result(const AttnArgs &a, int64_t tok, int head, int col, f4 v)
@@ -352,15 +312,15 @@ __device__ __forceinline__ void store_result(const AttnArgs &a, int64_t tok, int
 // log(sum e^s) from a base-2 reference and sum.
 __device__ __forceinline__ float lse_of(float m, float l) { return l > 0.0f ? (m + log2f(l)) * ATTN_LN2 : neg_inf(); }
 
-// The rows of 64 blocks of a job, lane x holding block first + x: the block's first
+// The rows of 64 blocks of a job, lane x holding block first + step x: the block's first
 // row in units of tokens (page, head and place in the page), or -1 for a page
 // outside the cache or a block past the job's.  One lane is then one read of a
 // register, with no page list or division in the loop over blocks.
 struct RowTable {
     int lo, hi;
-    __device__ __forceinline__ void load(const AttnArgs &a, const AttnJob &j, int first)
+    __device__ __forceinline__ void load(const AttnArgs &a, const AttnJob &j, int first, int step)
     {
-        const int blk = first + lane_id(), bpp = a.c.page_tokens / CACHE_BLOCK;
+        const int blk = first + step * lane_id(), bpp = a.c.page_tokens / CACHE_BLOCK;
         int64_t row = -1;
         if (blk < j.blk1) {
             const int rel = blk < j.nbp ? blk : blk - j.nbp, pi = rel / bpp;
@@ -440,8 +400,9 @@ __device__ __forceinline__ float max_abs8(const float (&v)[8])
 // 16) loads 16 bytes of key 16 T + i (a K row's columns 64 c + 16 g ..) and 16
 // bytes of V's row d = 16 dt + i (keys 4g .. 4g + 3 of the four 16-key tiles).
 // S^T = K Q^T leaves keys 4g .. 4g + 3 of a tile in lane (row i, g), which is the
-// operand order of O^T += V^T P^T: the weights never leave their lane.  The four
-// waves of a workgroup take the chunk's blocks in turn and add their sums in LDS.
+// operand order of O^T += V^T P^T: the weights never leave their lane.  The waves of
+// a workgroup (one, two or four) take the chunk's blocks in turn and add their sums
+// in LDS.
 // Bound: HBM (the bytes of the cache); no LDS and no barrier in the loop.
 // ---------------------------------------------------------------------------
 template <int DT, int DC>
@@ -450,12 +411,49 @@ __global__ __launch_bounds__(256, DC == 4 ? 1 : 2) void k_attn_stream(const Attn
     constexpr int NS = DT == DT_F32 ? 2 : 1; // binary16 terms of queries and weights
     using WR = WeightRange<NS>;
     constexpr int DTILES = 4 * DC, DPAD = 64 * DC;
-    // [4 waves][16 rows][DPAD] sums, then [4][16] m, [4][16] l, [16] l of all
-    __shared__ __attribute__((aligned(16))) float lds[4 * 16 * (DPAD + 2) + 16];
+    // [waves][16 rows][DPAD] sums, then [waves][16] m, [waves][16] l, [16] l of all
+    extern __shared__ __attribute__((aligned(16))) float lds[];
+    const int waves = blockDim.x / 64;
     AttnJob j;
     if (!attn_job(a, pl, 16, blockIdx.x + pl.wg0, j)) return;
     const int G = a.heads / a.c.heads, lane = lane_id(), wave = wave_id(), i = lane & 15, g = lane >> 4;
     const int Dp = a.c.Dp;
+
+    u4 kb[4][DC], vb[DTILES];
+    f4 ks[4], vs[4];
+    // byte offsets of this lane inside a block (columns past Dp read column 0: the queries hold zeros there)
+    uint32_t koff[DC], voff[DTILES];
+#pragma unroll
+    for (int cc = 0; cc < DC; ++cc) koff[cc] = i * Dp + (64 * cc + 16 * g < Dp ? 64 * cc + 16 * g : 0);
+#pragma unroll
+    for (int d = 0; d < DTILES; ++d) voff[d] = (16 * d < Dp ? 16 * d + i : i) * CACHE_BLOCK + 16 * g;
+    auto load_k = [&](int64_t at) {
+        const int8_t *p = a.c.K + (at < 0 ? 0 : at) * Dp;
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int cc = 0; cc < DC; ++cc) kb[t][cc] = load_at<u4>(p + 16 * t * Dp, koff[cc]);
+    };
+    auto load_v = [&](int64_t at) { // and the scales
+        const int64_t row = at < 0 ? 0 : at;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            ks[t] = load_at<f4>(a.c.Ks + row + 16 * t, 16 * g);
+            vs[t] = load_at<f4>(a.c.Vs + row + 16 * t, 16 * g);
+        }
+#pragma unroll
+        for (int d = 0; d < DTILES; ++d) vb[d] = load_at<u4>(a.c.V + row * Dp, voff[d]);
+    };
+    // the wave's blocks, the first one in flight while the queries are read
+    RowTable table;
+    int blk = j.blk0 + wave, left = 0;
+    int64_t row = -1;
+    if (blk < j.blk1) {
+        table.load(a, j, blk, waves);
+        row = table.at(0);
+        load_k(row);
+        load_v(row);
+    }
 
     h8 q[DC][2][NS]; // 64-column chunk, k-step, term
     float c;
@@ -474,7 +472,7 @@ __global__ __launch_bounds__(256, DC == 4 ? 1 : 2) void k_attn_stream(const Attn
             for (int h = 0; h < 2; ++h) query_terms<NS>(v[2 * cc + h], e2, a.scale, q[cc][h]);
         c = row_factor(a.scale, e2);
     }
-    // below the smallest limit of the tile's rows no key is masked
+    // own keys the lane's row sees; below the smallest of the tile's no key is masked
     const int lim = row_limit(j, G, i);
     int lim_min = i < j.rows ? lim : 0x7fffffff;
 #pragma unroll
@@ -482,54 +480,23 @@ __global__ __launch_bounds__(256, DC == 4 ? 1 : 2) void k_attn_stream(const Attn
     lim_min = __builtin_amdgcn_readfirstlane(lim_min);
 
     f4 o[DTILES];
+    // m: the row's reference in base 2 (0 until it is set), have: its largest weight so far
+    // (what this lane saw of it), ref: the V_scales' power of two
+    float m = 0.0f, l = 0.0f, have = 0.0f, ref = 0.0f, vscale = 0.0f;
+    bool set = false;
 #pragma unroll
     for (int d = 0; d < DTILES; ++d) o[d] = f4{0.0f, 0.0f, 0.0f, 0.0f};
-    // m: the row's reference in base 2 (0 until it is set), ref: of the V_scales
-    float m = 0.0f, l = 0.0f, ref = 0.0f, vscale = 0.0f;
-    bool set = false;
-    float have = 0.0f; // the largest weight so far (of a row: what this lane saw of it)
-    u4 kb[4][DC], vb[DTILES];
-    f4 ks[4], vs[4];
-    // byte offsets of this lane inside a block (columns past Dp read column 0: the queries hold zeros there)
-    uint32_t koff[DC], voff[DTILES]; // (unsigned: one register beside a uniform base)
-#pragma unroll
-    for (int cc = 0; cc < DC; ++cc) koff[cc] = i * Dp + (64 * cc + 16 * g < Dp ? 64 * cc + 16 * g : 0);
-#pragma unroll
-    for (int d = 0; d < DTILES; ++d) voff[d] = (16 * d < Dp ? 16 * d + i : i) * CACHE_BLOCK + 16 * g;
-    auto load_k = [&](int64_t row) {
-        const int8_t *p = a.c.K + row * Dp;
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int cc = 0; cc < DC; ++cc) kb[t][cc] = *reinterpret_cast<const u4 *>(p + 16 * t * Dp + static_cast<uint64_t>(koff[cc]));
-    };
-    auto load_v = [&](int64_t row) { // and the scales
-        const int8_t *p = a.c.V + row * Dp;
-        const float *pks = a.c.Ks + row, *pvs = a.c.Vs + row;
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            ks[t] = *reinterpret_cast<const f4 *>(pks + 16 * t + static_cast<uint32_t>(4 * g));
-            vs[t] = *reinterpret_cast<const f4 *>(pvs + 16 * t + static_cast<uint32_t>(4 * g));
-        }
-#pragma unroll
-        for (int d = 0; d < DTILES; ++d) vb[d] = *reinterpret_cast<const u4 *>(p + voff[d]);
-    };
-    int blk = j.blk0 + wave;
-    PageWalk walk(a, j, blk);
-    int page = -1, npage = -1;
-    if (blk < j.blk1) {
-        page = walk.page(a);
-        const int64_t row = walk.row(a, page, j.kvh);
-        load_k(row);
-        load_v(row);
-        walk.step(j, 4);
-        if (blk + 4 < j.blk1) npage = walk.page(a);
-    }
-    for (; blk < j.blk1; blk += 4) {
-        // this block's list: its first key, the keys there are, those this row sees
+    for (; blk < j.blk1; blk += waves) {
+        // this block's list: its first key, the keys there are, those a row sees
         const bool pre = blk < j.nbp;
         const int k0 = (pre ? blk : blk - j.nbp) * CACHE_BLOCK;
-        const int all = page < 0 ? 0 : (pre ? j.prefix : j.own), mine = page < 0 ? 0 : (pre ? j.prefix : lim);
+        const int all = row < 0 ? 0 : (pre ? j.prefix : j.own), mine = row < 0 ? 0 : (pre ? j.prefix : lim);
+        const bool masked = row < 0 || k0 + CACHE_BLOCK > (pre ? j.prefix : lim_min);
+        const bool next = blk + waves < j.blk1;
+        if (next) {
+            if (++left % 64 == 0) table.load(a, j, blk + waves, waves);
+            row = table.at(left % 64);
+        }
         f4 s[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
@@ -545,23 +512,20 @@ __global__ __launch_bounds__(256, DC == 4 ? 1 : 2) void k_attn_stream(const Attn
         }
 #pragma unroll
         for (int t = 0; t < 4; ++t) s[t] *= ks[t] * c;
-        const bool masked = page < 0 || k0 + CACHE_BLOCK > (pre ? j.prefix : lim_min);
         if (masked) {
 #pragma unroll
             for (int t = 0; t < 4; ++t)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int key = k0 + 16 * t + 4 * g + r;
-                    s[t][r] = key < mine ? s[t][r] : neg_inf();
-                    vs[t][r] = key < all ? vs[t][r] : 0.0f;
+                for (int e = 0; e < 4; ++e) {
+                    const int key = k0 + 16 * t + 4 * g + e;
+                    s[t][e] = key < mine ? s[t][e] : neg_inf();
+                    vs[t][e] = key < all ? vs[t][e] : 0.0f;
                 }
         }
         // the next block's keys, while this block's weights are formed
-        const bool next = blk + 4 < j.blk1;
-        const int64_t nrow = walk.row(a, npage, j.kvh);
-        if (next) load_k(nrow);
+        if (next) load_k(row);
         h8 p[2][NS];
-        float sum = 0.0f;
+        float sum = 0.0f, big, small;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             float w[8];
@@ -573,7 +537,6 @@ __global__ __launch_bounds__(256, DC == 4 ? 1 : 2) void k_attn_stream(const Attn
             }
             split_weights<NS>(w, p[h]);
         }
-        float big, small;
         weight_range(p, big, small);
         if (masked) { // (masked weights are 0 and call for nothing)
             small = WR::LEAST;
@@ -583,43 +546,42 @@ __global__ __launch_bounds__(256, DC == 4 ? 1 : 2) void k_attn_stream(const Attn
         }
         if (__any((!set && k0 < mine) || ref == 0.0f || !(big <= H_MAX) || !(sum <= SUM_MAX) || small < WR::LEAST)) {
             // the general form: references brought to this block's largest, small weights in rounds
-            float vtop = 0.0f, top = neg_inf();
+            float vtop = 0.0f, grown = 1.0f;
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                vtop = fmaxf(fmaxf(fmaxf(vtop, vs[t][0]), fmaxf(vs[t][1], vs[t][2])), vs[t][3]);
-                top = fmaxf(fmaxf(fmaxf(top, s[t][0]), fmaxf(s[t][1], s[t][2])), s[t][3]);
-            }
+            for (int t = 0; t < 4; ++t) vtop = fmaxf(fmaxf(fmaxf(vtop, vs[t][0]), fmaxf(vs[t][1], vs[t][2])), vs[t][3]);
             vtop = max_across32(max_across16(vtop));
+            if (vtop > ref) {
+                const float ref2 = pow2_above(vtop);
+                grown = ref / ref2;
+                ref = ref2;
+                vscale = WR::PSCALE / ref;
+            }
+            float top = neg_inf();
+#pragma unroll
+            for (int t = 0; t < 4; ++t) top = fmaxf(fmaxf(fmaxf(top, s[t][0]), fmaxf(s[t][1], s[t][2])), s[t][3]);
             top = max_across32(max_across16(top));
             big = max_across32(max_across16(big));
             sum = max_across32(max_across16(sum));
             const bool raise = top > neg_inf() && (!set || (top > m && (!(big <= H_MAX) || !(sum <= SUM_MAX))));
-            float f = raise && set ? __builtin_amdgcn_exp2f(m - top) : 1.0f;
+            const float f = raise && set ? __builtin_amdgcn_exp2f(m - top) : 1.0f;
             m = raise ? top : m;
             set = set || raise;
             l *= f;
-            if (vtop > ref) {
-                const float ref2 = pow2_above(vtop);
-                f *= ref / ref2;
-                ref = ref2;
-                vscale = WR::PSCALE / ref;
-            }
 #pragma unroll
-            for (int d = 0; d < DTILES; ++d) o[d] *= f;
-            sum = 0.0f;
-            big = 0.0f;
+            for (int d = 0; d < DTILES; ++d) o[d] *= f * grown;
+            sum = big = 0.0f;
             small = WR::LEAST;
 #pragma unroll
             for (int t = 0; t < 4; ++t)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    s[t][r] = __builtin_amdgcn_exp2f(s[t][r] - m);
-                    sum += s[t][r];
-                    s[t][r] *= vs[t][r] * vscale;
-                    big = fmaxf(big, s[t][r]);
-                    small = s[t][r] > 0.0f ? fminf(small, s[t][r]) : small;
+                for (int e = 0; e < 4; ++e) {
+                    s[t][e] = __builtin_amdgcn_exp2f(s[t][e] - m);
+                    sum += s[t][e];
+                    s[t][e] *= vs[t][e] * vscale;
+                    big = fmaxf(big, s[t][e]);
+                    small = s[t][e] > 0.0f ? fminf(small, s[t][e]) : small;
                 }
-            have = max_across32(max_across16(fmaxf(have * f, big)));
+            have = max_across32(max_across16(fmaxf(have * (f * grown), big)));
             big = 0.0f; // (it is in have)
             if (__any(small < WR::LEAST)) {
                 small = -max_across32(max_across16(-small));
@@ -683,44 +645,35 @@ __global__ __launch_bounds__(256, DC == 4 ? 1 : 2) void k_attn_stream(const Attn
 #pragma unroll
                 for (int z = 0; z < NS; ++z) o[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vv, p[h][z], o[d], 0, 0, 0);
             }
-        page = npage;
-        if (next) {
-            load_v(nrow);
-            walk.step(j, 4);
-            npage = blk + 8 < j.blk1 ? walk.page(a) : -1;
-        }
+        if (next) load_v(row);
     }
 
     // add the waves: largest m of each row, every wave's sums brought to it
-    float *ml = lds + 4 * 16 * DPAD;
+    f4 *po = reinterpret_cast<f4 *>(a.ws);
+    float2 *pml = reinterpret_cast<float2 *>(a.ws + pl.ml_off);
+    float *ml = lds + waves * 16 * DPAD, *ll = ml + waves * 16, *sums = ll + waves * 16; // l of the rows
     l = sum_across32(sum_across16(l));
     m = set ? m : neg_inf();
     if (g == 0) {
         ml[wave * 16 + i] = m;
-        ml[64 + wave * 16 + i] = l;
+        ll[wave * 16 + i] = l;
     }
     __syncthreads();
     {
         float top = neg_inf();
-#pragma unroll
-        for (int w = 0; w < 4; ++w) top = fmaxf(top, ml[w * 16 + i]);
+        for (int w = 0; w < waves; ++w) top = fmaxf(top, ml[w * 16 + i]);
         const float f = m > neg_inf() ? __builtin_amdgcn_exp2f(m - top) * (ref / WR::PSCALE) : 0.0f;
         float *dst = lds + (wave * 16 + i) * DPAD;
 #pragma unroll
         for (int d = 0; d < DTILES; ++d) *reinterpret_cast<f4 *>(dst + 16 * d + 4 * g) = o[d] * f;
     }
     __syncthreads();
-    f4 *po = reinterpret_cast<f4 *>(a.ws);
-    float2 *pml = reinterpret_cast<float2 *>(a.ws + pl.ml_off);
-    float *sums = ml + 128; // l of the rows, and m
     if (threadIdx.x < 16) {
         float top = neg_inf(), sum = 0.0f;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) top = fmaxf(top, ml[w * 16 + threadIdx.x]);
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
+        for (int w = 0; w < waves; ++w) top = fmaxf(top, ml[w * 16 + threadIdx.x]);
+        for (int w = 0; w < waves; ++w) {
             const float mw = ml[w * 16 + threadIdx.x];
-            if (mw > neg_inf()) sum += ml[64 + w * 16 + threadIdx.x] * __builtin_amdgcn_exp2f(mw - top);
+            if (mw > neg_inf()) sum += ll[w * 16 + threadIdx.x] * __builtin_amdgcn_exp2f(mw - top);
         }
         sums[threadIdx.x] = sum;
         const int rr = j.row0 + static_cast<int>(threadIdx.x);
@@ -732,11 +685,10 @@ __global__ __launch_bounds__(256, DC == 4 ? 1 : 2) void k_attn_stream(const Attn
         }
     }
     if (pl.direct) __syncthreads();
-    for (int e = threadIdx.x; e < j.rows * (Dp / 4); e += 256) {
+    for (int e = threadIdx.x; e < j.rows * (Dp / 4); e += blockDim.x) {
         const int rho = e / (Dp / 4), d4 = e % (Dp / 4), rr = j.row0 + rho;
         f4 sum = f4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int w = 0; w < 4; ++w) sum += *reinterpret_cast<const f4 *>(lds + (w * 16 + rho) * DPAD + 4 * d4);
+        for (int w = 0; w < waves; ++w) sum += *reinterpret_cast<const f4 *>(lds + (w * 16 + rho) * DPAD + 4 * d4);
         const int64_t tok = j.tok0 + rr / G;
         const int head = j.kvh * G + rr % G;
         if (pl.direct) store_result<DT>(a, tok, head, 4 * d4, sum * (sums[rho] > 0.0f ? 1.0f / sums[rho] : 0.0f));
@@ -765,10 +717,8 @@ __global__ __launch_bounds__(256, DC == 4 ? 1 : 2) void k_attn_stream(const Attn
 // flight from memory in registers for a whole block.
 // Bound: vector ALU (weights, conversion) beside matrix cores.
 // ---------------------------------------------------------------------------
-constexpr bool tile_one_wave(int dt, int dc) { return dc == 4 || (dt == DT_F32 && dc == 2); }
-
 template <int DT, int DC, int NW>
-__global__ __launch_bounds__(64 * NW, tile_one_wave(DT, DC) ? 1 : 2) void k_attn_tile(const AttnArgs a, const AttnPlan pl)
+__global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(const AttnArgs a, const AttnPlan pl)
 {
     constexpr int NS = DT == DT_F32 ? 2 : 1;
     using WR = WeightRange<NS>;
@@ -818,7 +768,7 @@ __global__ __launch_bounds__(64 * NW, tile_one_wave(DT, DC) ? 1 : 2) void k_attn
     RowTable table;
     int64_t row0 = -1, row1 = -1;
     if (j.blk0 < j.blk1) { // (in flight while the queries are read)
-        table.load(a, j, j.blk0);
+        table.load(a, j, j.blk0, 1);
         row0 = table.at(0);
         fetch_k(j.blk0, row0);
         fetch_v(row0);
@@ -997,7 +947,7 @@ __global__ __launch_bounds__(64 * NW, tile_one_wave(DT, DC) ? 1 : 2) void k_attn
         if (blk + 1 < j.blk1) fetch_v(row1);
         if (blk + 2 < j.blk1) {
             const int x = blk + 2 - j.blk0;
-            if (x % 64 == 0) table.load(a, j, blk + 2);
+            if (x % 64 == 0) table.load(a, j, blk + 2, 1);
             row1 = table.at(x % 64);
             fetch_k(blk + 2, row1);
         }
@@ -1293,34 +1243,58 @@ namespace {
 int64_t div_up(int64_t x, int64_t y) { return (x + y - 1) / y; }
 
 // Rows a workgroup takes: 16 with k_attn_stream, 128 or 256 (four or eight waves)
-// with k_attn_tile.  Eight waves share a conversion of the keys; they need two
-// waves a SIMD.
+// with k_attn_tile.  Row tiles that read the cache again from L2 cost less than a
+// mostly empty tile of 128: bf16, 8 kv heads of 128, keys x rows, us of k_attn_stream
+// and of k_attn_tile: 60001 x 24: 48, 81; x 64: 69, 82; x 96: 95, 86; 12000 x 96: 37,
+// 50; x 128: 40, 52; x 256: 62, 59; x 1024: 187, 108.  With the registers of fp32
+// queries (two terms) and head_dim past 64, or of head_dim past 128, k_attn_stream
+// won at every size (400 query tokens x 4 on 2100 keys, heads of 256, bf16: 716, 838;
+// of 128, fp32: 758, 1109).  Eight waves share a conversion of the keys and need
+// registers for two waves a SIMD (fp32 queries do not leave them).
+constexpr int64_t kStreamRows = 96;
+
 int tile_rows(int64_t rows, int64_t head_dim, int dtype)
 {
-    return rows <= 16 ? 16 : rows <= 128 || head_dim <= 64 || head_dim > 128 || dtype == DT_F32 ? 128 : 256;
+    if (rows <= kStreamRows || head_dim > 128 || (dtype == DT_F32 && head_dim > 64)) return 16;
+    return rows <= 128 || head_dim <= 64 ? 128 : 256;
 }
 
-// Splits of 'blocks' key blocks for 'wgs' workgroups: the count with the least
-// time, in blocks, of all rounds of the 256 CUs, a workgroup costing its blocks and
-// about four more for its start and end; a split more costs its sums' way through
-// memory.
-void choose_splits(int64_t wgs, int64_t blocks, int rows, int64_t head_dim, int dtype, int *chunk, int *splits)
+// How 'wgs' workgroups' passes over 'blocks' key blocks are split: blocks of a
+// part, parts, waves of a workgroup.
+struct AttnCut {
+    int chunk, splits, waves;
+};
+
+// The cut with the least time, in eighths of a block, of all rounds of the card: a
+// wave (of k_attn_stream, whose waves take blocks in turn) or workgroup (of
+// k_attn_tile) costs its blocks and about four more for its start and end; waves
+// that join their sums, and a split more whose sums go through memory, cost the
+// eighths given, and the join itself, where there would be none (joined), four
+// blocks.  waves: those of k_attn_stream, 0 for any; others: workgroups of the same
+// launch.
+AttnCut choose_cut(int64_t wgs, int64_t blocks, int rows, int64_t head_dim, int waves, int64_t others, bool joined)
 {
-    *chunk = *splits = 0;
-    if (blocks == 0) return;
+    AttnCut best{0, 0, waves ? waves : 4};
+    if (blocks == 0) return best;
     const int dc = head_dim <= 64 ? 1 : head_dim <= 128 ? 2 : 4;
-    const bool alone = rows == 16 ? dc == 4 : rows == 256 || tile_one_wave(dtype, dc); // one workgroup a CU, or two
-    const int64_t slots = alone ? 256 : 512, least = rows == 16 ? 4 : 2; // (k_attn_stream: a block for each wave)
-    int64_t best = -1;
-    for (int64_t s = 1; s <= 64 && (s == 1 || div_up(blocks, s) >= least); ++s) {
-        const int64_t c = div_up(blocks, s), n = div_up(blocks, c);
-        const int64_t cost = div_up(wgs * n, slots) * (c + 4) + n / 8;
-        if (best < 0 || cost < best) {
-            best = cost;
-            *chunk = static_cast<int>(c);
-            *splits = static_cast<int>(n);
+    const bool stream = rows == 16;
+    int64_t least = -1;
+    for (int w = 1; w <= 8; w *= 2) {
+        if (stream ? w > 4 || (waves && w != waves) : w != rows / 32) continue;
+        const bool alone = stream ? dc == 4 : rows == 256; // one wave a SIMD, one workgroup a CU; or two
+        const int64_t slots = stream ? 256 * (4 / w) * (alone ? 1 : 2) : 256 * (alone ? 1 : 2);
+        for (int64_t s = 1; s <= 64 && (s == 1 || div_up(blocks, s) >= (stream ? w : 2)); ++s) {
+            const int64_t c = div_up(blocks, s), n = div_up(blocks, c);
+            const int64_t cost =
+                8 * div_up(wgs * n + others, slots) * ((stream ? div_up(c, w) : c) + 4) + n +
+                (stream && w > 1 ? 4 : 0) + (n > 1 && !joined ? 32 : 0);
+            if (least < 0 || cost < least) {
+                least = cost;
+                best = AttnCut{static_cast<int>(c), static_cast<int>(n), w};
+            }
         }
     }
+    return best;
 }
 
 // Reading the prefix again for each sequence costs less than a launch and a join
@@ -1338,12 +1312,22 @@ AttnPlan attn_plan(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head
     p.tiles_own = static_cast<int>(div_up(max_q * G, p.rows_own));
     // one pass over prefix and own keys where a sequence fills row tiles of its own anyway, or the
     // prefix is short
-    p.joint = nbp > 0 && (p.rows_own > 16 || 2 * prefix * kv_heads * dp * (seqs - 1) <= kJointBytes);
+    p.joint = nbp > 0 && (max_q * G >= 128 || 2 * prefix * kv_heads * dp * (seqs - 1) <= kJointBytes);
     const int64_t tp = p.joint || nbp == 0 ? 0 : div_up(tokens * G, p.rows_prefix);
-    p.chunk_prefix = p.splits_prefix = 0;
-    if (tp > 0) choose_splits(tp * kv_heads, nbp, p.rows_prefix, head_dim, dtype, &p.chunk_prefix, &p.splits_prefix);
-    choose_splits(seqs * p.tiles_own * kv_heads, p.joint ? nbp + nbo : nbo, p.rows_own, head_dim, dtype, &p.chunk_own, &p.splits_own);
+    p.together = tp > 0 && p.rows_prefix == 16;
+    AttnCut cut{0, 0, 4};
+    if (tp > 0)
+        cut = choose_cut(tp * kv_heads, nbp, p.rows_prefix, head_dim, 0, p.together && nbo > 0 ? seqs * p.tiles_own * kv_heads : 0,
+                         true);
+    p.chunk_prefix = cut.chunk;
+    p.splits_prefix = cut.splits;
+    p.waves_prefix = cut.waves;
     p.wgs_prefix = static_cast<int>(tp * kv_heads * p.splits_prefix);
+    cut = choose_cut(seqs * p.tiles_own * kv_heads, p.joint ? nbp + nbo : nbo, p.rows_own, head_dim,
+                     p.together ? p.waves_prefix : 0, p.together ? p.wgs_prefix : 0, tp > 0);
+    p.chunk_own = cut.chunk;
+    p.splits_own = cut.splits;
+    p.waves_own = cut.waves;
     p.wgs_own = static_cast<int>(seqs * p.tiles_own * kv_heads * p.splits_own);
     p.wg0 = 0;
     const int64_t parts = p.splits_prefix + p.splits_own;
@@ -1353,24 +1337,24 @@ AttnPlan attn_plan(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head
 }
 
 template <int DT>
-hipError_t launch_part(const AttnArgs &a, AttnPlan pl, int rows, int wg0, int wgs, hipStream_t st)
+hipError_t launch_part(const AttnArgs &a, AttnPlan pl, int rows, int waves, int wg0, int wgs, hipStream_t st)
 {
     if (wgs == 0) return hipSuccess;
     pl.wg0 = wg0;
     const int dc = a.c.Dp <= 64 ? 1 : a.c.Dp <= 128 ? 2 : 4;
-    const dim3 grid(static_cast<unsigned>(wgs)), block(256);
-#define BL_STREAM(DC) hipLaunchKernelGGL((k_attn_stream<DT, DC>), grid, block, 0, st, a, pl)
-#define BL_TILE(DC, NW) hipLaunchKernelGGL((k_attn_tile<DT, DC, NW>), grid, dim3(64 * NW), 0, st, a, pl)
+    const dim3 grid(static_cast<unsigned>(wgs)), block(64 * waves);
+    const size_t lds = (waves * 16 * (64 * dc + 2) + 16) * sizeof(float);
+#define BL_STREAM(DC) hipLaunchKernelGGL((k_attn_stream<DT, DC>), grid, block, lds, st, a, pl)
+#define BL_TILE(DC, NW) hipLaunchKernelGGL((k_attn_tile<DT, DC, NW>), grid, block, 0, st, a, pl)
     if (rows == 16) {
         if (dc == 1) BL_STREAM(1);
         else if (dc == 2) BL_STREAM(2);
         else BL_STREAM(4);
-    } else if (rows == 128) {
-        if (dc == 1) BL_TILE(1, 4);
-        else if (dc == 2) BL_TILE(2, 4);
-        else BL_TILE(4, 4);
+    } else if (dc == 1) {
+        BL_TILE(1, 4);
     } else if constexpr (DT == DT_BF16) {
-        BL_TILE(2, 8);
+        if (rows == 128) BL_TILE(2, 4);
+        else BL_TILE(2, 8);
     }
 #undef BL_STREAM
 #undef BL_TILE
@@ -1380,8 +1364,13 @@ hipError_t launch_part(const AttnArgs &a, AttnPlan pl, int rows, int wg0, int wg
 template <int DT>
 hipError_t launch_attn(const AttnArgs &a, const AttnPlan &pl, hipStream_t st)
 {
-    hipError_t e = launch_part<DT>(a, pl, pl.rows_prefix, 0, pl.wgs_prefix, st);
-    if (e == hipSuccess) e = launch_part<DT>(a, pl, pl.rows_own, pl.wgs_prefix, pl.wgs_own, st);
+    hipError_t e = hipSuccess;
+    if (pl.together) {
+        e = launch_part<DT>(a, pl, pl.rows_own, pl.waves_own, 0, pl.wgs_prefix + pl.wgs_own, st);
+    } else {
+        e = launch_part<DT>(a, pl, pl.rows_prefix, pl.waves_prefix, 0, pl.wgs_prefix, st);
+        if (e == hipSuccess) e = launch_part<DT>(a, pl, pl.rows_own, pl.waves_own, pl.wgs_prefix, pl.wgs_own, st);
+    }
     if (e != hipSuccess) return e;
     if (pl.direct) return hipSuccess;
     const int64_t rows = static_cast<int64_t>(a.seqs) * a.max_q * a.heads;
