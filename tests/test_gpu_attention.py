@@ -195,6 +195,31 @@ def test_sharp_and_flat_softmax(dtype):
         check(o, want, bound)
 
 
+@pytest.mark.parametrize("tokens,heads,kvh,D,dtype", [
+    (12, 8, 1, 128, "bf16"), (13, 16, 2, 64, "bf16"), (16, 8, 1, 128, "bf16"), (17, 8, 1, 100, "bf16"),
+    (40, 8, 1, 128, "bf16"), (12, 8, 1, 64, "f32"), (13, 8, 1, 64, "f32"), (40, 16, 2, 50, "f32"),
+    (40, 8, 1, 128, "f32"), (33, 8, 1, 256, "bf16")])
+def test_row_counts(tokens, heads, kvh, D, dtype):
+    """Rows of a prefix below and past every row tile's size (8 to a token), with references that have to move:
+    scores and values of a key block are small or large, block by block, so that weights leave the range of
+    binary16 on both sides of the first block's."""
+    print("attention rows", tokens, heads, kvh, D, dtype, flush=True)
+    own = [(7 * b) % 90 for b in range(tokens)]
+    st = Setup(kvh, D, 64, 700, own, seed=tokens + D)
+    sizes = np.array([1.0, 0.05, 6.0, 0.3, 12.0, 0.01, 20.0, 3.0])
+    values = np.array([1.0, 1e-6, 1.0, 300.0, 1e-3, 1.0, 1e4, 1e-9])
+    for j, page in enumerate(st.lists[0]):
+        st.ks[page] *= np.float32(sizes[j % 8])
+        st.vs[page] *= np.float32(values[j % 8])
+    qt, q = queries(tokens, heads, D, 11, dtype, size=2.0)
+    o, lse = bl.attention(st.cache(), qt, to_dev(st.table), to_dev(np.array(own, np.int32)), max(own),
+                          prefix_pages=to_dev(st.prefix_pages), prefix_len=700, return_lse=True)
+    torch.cuda.synchronize()
+    want, bound, wl, wb = reference(st, q, [1] * tokens, D ** -0.5, dtype)
+    check(o, want, bound)
+    assert np.all(np.abs(to_host(lse) - wl) <= wb)
+
+
 def test_zero_value_scales():
     """Tokens whose values are all zero (scale 0) take their share of the softmax."""
     st = Setup(1, 64, 64, 70, [10], seed=8)
