@@ -614,7 +614,8 @@ typedef struct {
 
 /* Bytes of K (and of V): pages * heads * page_tokens * Dp, or -1 for sizes
  * outside: pages, heads >= 1, page_tokens a multiple of 64 up to 2^20,
- * head_dim in [1, 256], heads <= 4096, pages * page_tokens <= 2^36. */
+ * head_dim in [1, 256], heads <= 4096, pages * page_tokens <= 2^36, pages * heads *
+ * page_tokens / 64 < 2^31. */
 int64_t bitlinear_cache_bytes(int64_t pages, int64_t page_tokens, int64_t heads, int64_t head_dim);
 
 /*

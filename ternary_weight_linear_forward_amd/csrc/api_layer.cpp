@@ -228,6 +228,7 @@ int64_t bitlinear_cache_bytes(int64_t pages, int64_t page_tokens, int64_t heads,
         page_tokens > (int64_t(1) << 20) || head_dim < 1 || head_dim > BITLINEAR_MAX_HEAD_DIM || pages > INT32_MAX ||
         pages > (int64_t(1) << 36) / page_tokens)
         return -1;
+    if (pages * heads * (page_tokens / 64) > INT32_MAX) return -1; // (kernels number the blocks in 32 bits)
     return pages * heads * page_tokens * round_up(head_dim, 16);
 }
 

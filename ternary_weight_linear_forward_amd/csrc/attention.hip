@@ -20,11 +20,12 @@
 //  - weights p = 2^(c t - m) are multiplied by V_scale / ref * PSCALE, ref a
 //    power of two above the V_scales seen, and rounded to binary16 (11 bits; with
 //    fp32 queries two terms, 22 bits).  m is any reference, not the maximum: it
-//    starts as the first block's and is raised to a block's when a weight of that
-//    block overflows binary16, so most blocks form no maximum.  Weights too small
-//    for a full binary16 number (p below 2^-21 of the largest) are multiplied in
-//    further rounds, brought up by STEP each, into sums of their own: a branch
-//    that blocks without such weights do not take.  l sums the unrounded p.
+//    starts as the first block's, is raised to a block's maximum when a weight of
+//    that block overflows binary16, and is lowered, so that the row's largest weight
+//    so far comes to 2^13, when one falls below a full binary16 number (p below
+//    2^-21 of the reference's): blocks form no maximum unless one of that happens.
+//    Weights that are too small even then are multiplied in further rounds, brought
+//    up by STEP each, into sums of their own.  l sums the unrounded p.
 #include "cache_core.h"
 #include "common.h"
 #include "launch.h"
@@ -103,6 +104,20 @@ __device__ __forceinline__ void weight_range(const h8 (&p)[NT][NS], float &big, 
 }
 constexpr float H_MAX = 65504.0f;   // largest binary16
 constexpr float SUM_MAX = 0x1p100f; // a block's sum of p beyond which the reference is raised
+
+// Whether a block's weights ask for the general form (bit operators: no branches).
+__device__ __forceinline__ bool calls_for_general(bool unset, float big, float sum, bool small)
+{
+    return unset | !(big <= H_MAX) | !(sum <= SUM_MAX) | small;
+}
+
+// What the compiler may not put off: it would keep all the terms until then.
+__device__ __forceinline__ void pin(float &v)
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+    asm volatile("" : "+v"(v));
+#endif
+}
 
 // Power of two at or above v > 0 (as a factor that never overflows).
 __device__ __forceinline__ float pow2_above(float v)
@@ -312,30 +327,39 @@ __device__ __forceinline__ void store_result(const AttnArgs &a, int64_t tok, int
 // log(sum e^s) from a base-2 reference and sum.
 __device__ __forceinline__ float lse_of(float m, float l) { return l > 0.0f ? (m + log2f(l)) * ATTN_LN2 : neg_inf(); }
 
-// The rows of 64 blocks of a job, lane x holding block first + step x: the block's first
-// row in units of tokens (page, head and place in the page), or -1 for a page
-// outside the cache or a block past the job's.  One lane is then one read of a
-// register, with no page list or division in the loop over blocks.
-struct RowTable {
-    int lo, hi;
+// Where 64 blocks of a job lie, lane x holding block first + step x: the number of
+// the block among all blocks of the cache (page, head and place in the page), 0 for a
+// page outside the cache or a block past the job's, whose bit of valid is 0.  A block
+// is then one read of a lane, with no page list, division or test in the loop.
+struct BlockTable {
+    int unit;
+    unsigned long long valid;
     __device__ __forceinline__ void load(const AttnArgs &a, const AttnJob &j, int first, int step)
     {
         const int blk = first + step * lane_id(), bpp = a.c.page_tokens / CACHE_BLOCK;
-        int64_t row = -1;
+        int page = -1;
+        unit = 0;
         if (blk < j.blk1) {
             const int rel = blk < j.nbp ? blk : blk - j.nbp, pi = rel / bpp;
-            const int page = (blk < j.nbp ? j.prefix_pages : j.own_pages)[pi];
-            if (page >= 0 && page < a.c.pages) row = cache_row0(a.c, page, j.kvh) + (rel - pi * bpp) * CACHE_BLOCK;
+            page = (blk < j.nbp ? j.prefix_pages : j.own_pages)[pi];
+            if (page >= 0 && page < a.c.pages)
+                unit = static_cast<int>(cache_row0(a.c, page, j.kvh) / CACHE_BLOCK) + rel - pi * bpp;
+            else page = -1;
         }
-        lo = static_cast<int>(row);
-        hi = static_cast<int>(row >> 32);
+        valid = __ballot(page >= 0);
     }
-    __device__ __forceinline__ int64_t at(int x) const // x uniform
-    {
-        return static_cast<int64_t>(__builtin_amdgcn_readlane(hi, x)) << 32 |
-               static_cast<uint32_t>(__builtin_amdgcn_readlane(lo, x));
-    }
+    __device__ __forceinline__ uint32_t at(int x) const { return __builtin_amdgcn_readlane(unit, x); } // x uniform
+    __device__ __forceinline__ bool there(int x) const { return valid >> x & 1; }
 };
+// A block's first byte of K (and V), and of its K_scales (and V_scales).
+__device__ __forceinline__ const int8_t *block_bytes(const int8_t *p, uint32_t unit, int Dp)
+{
+    return p + static_cast<uint64_t>(unit) * static_cast<uint32_t>(CACHE_BLOCK * Dp);
+}
+__device__ __forceinline__ const float *block_scales(const float *p, uint32_t unit)
+{
+    return p + static_cast<uint64_t>(unit) * CACHE_BLOCK;
+}
 
 // A row's power of two: 2^e with max|q| 2^e in [2^13, 2^14); 1 for a zero row.
 __device__ __forceinline__ int row_exponent(float top)
@@ -427,32 +451,34 @@ __global__ __launch_bounds__(256, DC == 4 ? 1 : 2) void k_attn_stream(const Attn
     for (int cc = 0; cc < DC; ++cc) koff[cc] = i * Dp + (64 * cc + 16 * g < Dp ? 64 * cc + 16 * g : 0);
 #pragma unroll
     for (int d = 0; d < DTILES; ++d) voff[d] = (16 * d < Dp ? 16 * d + i : i) * CACHE_BLOCK + 16 * g;
-    auto load_k = [&](int64_t at) {
-        const int8_t *p = a.c.K + (at < 0 ? 0 : at) * Dp;
+    auto load_k = [&](uint32_t unit) {
+        const int8_t *p = block_bytes(a.c.K, unit, Dp);
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
             for (int cc = 0; cc < DC; ++cc) kb[t][cc] = load_at<u4>(p + 16 * t * Dp, koff[cc]);
     };
-    auto load_v = [&](int64_t at) { // and the scales
-        const int64_t row = at < 0 ? 0 : at;
+    auto load_v = [&](uint32_t unit) { // and the scales
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-            ks[t] = load_at<f4>(a.c.Ks + row + 16 * t, 16 * g);
-            vs[t] = load_at<f4>(a.c.Vs + row + 16 * t, 16 * g);
+            ks[t] = load_at<f4>(block_scales(a.c.Ks, unit) + 16 * t, 16 * g);
+            vs[t] = load_at<f4>(block_scales(a.c.Vs, unit) + 16 * t, 16 * g);
         }
 #pragma unroll
-        for (int d = 0; d < DTILES; ++d) vb[d] = load_at<u4>(a.c.V + row * Dp, voff[d]);
+        for (int d = 0; d < DTILES; ++d) vb[d] = load_at<u4>(block_bytes(a.c.V, unit, Dp), voff[d]);
     };
     // the wave's blocks, the first one in flight while the queries are read
-    RowTable table;
-    int blk = j.blk0 + wave, left = 0;
-    int64_t row = -1;
+    BlockTable table;
+    int blk = j.blk0 + wave;
+    unsigned left = 0;
+    uint32_t unit = 0;
+    bool there = false;
     if (blk < j.blk1) {
         table.load(a, j, blk, waves);
-        row = table.at(0);
-        load_k(row);
-        load_v(row);
+        unit = table.at(0);
+        there = table.there(0);
+        load_k(unit);
+        load_v(unit);
     }
 
     h8 q[DC][2][NS]; // 64-column chunk, k-step, term
@@ -490,12 +516,13 @@ __global__ __launch_bounds__(256, DC == 4 ? 1 : 2) void k_attn_stream(const Attn
         // this block's list: its first key, the keys there are, those a row sees
         const bool pre = blk < j.nbp;
         const int k0 = (pre ? blk : blk - j.nbp) * CACHE_BLOCK;
-        const int all = row < 0 ? 0 : (pre ? j.prefix : j.own), mine = row < 0 ? 0 : (pre ? j.prefix : lim);
-        const bool masked = row < 0 || k0 + CACHE_BLOCK > (pre ? j.prefix : lim_min);
+        const int all = there ? (pre ? j.prefix : j.own) : 0, mine = there ? (pre ? j.prefix : lim) : 0;
+        const bool masked = !there || k0 + CACHE_BLOCK > (pre ? j.prefix : lim_min);
         const bool next = blk + waves < j.blk1;
         if (next) {
             if (++left % 64 == 0) table.load(a, j, blk + waves, waves);
-            row = table.at(left % 64);
+            unit = table.at(left % 64);
+            there = table.there(left % 64);
         }
         f4 s[4];
 #pragma unroll
@@ -523,7 +550,7 @@ __global__ __launch_bounds__(256, DC == 4 ? 1 : 2) void k_attn_stream(const Attn
                 }
         }
         // the next block's keys, while this block's weights are formed
-        if (next) load_k(row);
+        if (next) load_k(unit);
         h8 p[2][NS];
         float sum = 0.0f, big, small;
 #pragma unroll
@@ -544,7 +571,7 @@ __global__ __launch_bounds__(256, DC == 4 ? 1 : 2) void k_attn_stream(const Attn
             for (int e = 0; e < 16; ++e)
                 small = s[e / 4][e % 4] > neg_inf() ? fminf(small, static_cast<float>(p[e / 8][0][e % 8])) : small;
         }
-        if (__any((!set && k0 < mine) || ref == 0.0f || !(big <= H_MAX) || !(sum <= SUM_MAX) || small < WR::LEAST)) {
+        if (__any(calls_for_general((!set && k0 < mine) || ref == 0.0f, big, sum, small < WR::LEAST))) {
             // the general form: references brought to this block's largest, small weights in rounds
             float vtop = 0.0f, grown = 1.0f;
 #pragma unroll
@@ -645,7 +672,7 @@ __global__ __launch_bounds__(256, DC == 4 ? 1 : 2) void k_attn_stream(const Attn
 #pragma unroll
                 for (int z = 0; z < NS; ++z) o[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vv, p[h][z], o[d], 0, 0, 0);
             }
-        if (next) load_v(row);
+        if (next) load_v(unit);
     }
 
     // add the waves: largest m of each row, every wave's sums brought to it
@@ -708,14 +735,17 @@ __global__ __launch_bounds__(256, DC == 4 ? 1 : 2) void k_attn_stream(const Attn
 // block n, beside the conversion of the next K and this V), and W(n), its weights.
 // P keeps the matrix cores busy and W the vector ALU, so with eight waves the
 // second four run one phase behind the first: of the two waves of a SIMD one is in
-// P while the other is in W (a barrier after every phase; measured without the
-// shift, both do the same phase and neither unit is busy half the time).  What P(n)
-// writes (K of n + 1, V of n, scales of n + 1) takes places that nothing has read
-// since the barrier before either half's P(n), and is read from the phase after
-// both halves' P(n) on.  With four waves the other workgroup of the CU fills in.
-// Operands are read from LDS some steps ahead; the bytes converted next are in
-// flight from memory in registers for a whole block.
-// Bound: vector ALU (weights, conversion) beside matrix cores.
+// P while the other is in W, with a barrier after every phase, and P has the higher
+// priority (8000 keys x 11264 rows: 82 us; without the shift 87, without the
+// priority 84).  What P(n) writes (K of n + 1, V of n, scales of n + 1) takes places
+// that nothing has read since the barrier before either half's P(n), and is read
+// from the phase after both halves' P(n) on.  With four waves the other workgroup
+// of the CU fills in.  Operands are read from LDS AHEAD of their use (4 to 8 measure
+// alike); the bytes converted next are in flight in registers for a whole block.
+// Bound: the phases' instruction streams.  11264 rows on 8000 keys of 8 heads of 128
+// (46 Gflop): 82 us, 560 Tflop/s; a block takes 5000 cycles of its CU where its
+// matrix instructions need 2048 and its vector instructions 2500.  One stream that
+// forms the next scores beside the weights, without phases, came to the same (91 us).
 // ---------------------------------------------------------------------------
 template <int DT, int DC, int NW>
 __global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(const AttnArgs a, const AttnPlan pl)
@@ -751,27 +781,28 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(const AttnArgs a, cons
     float ksr = 0.0f, vsr = 0.0f;
     int seen = 0; // keys of the fetched block that there are
     // A block's bytes into registers: K and the scales, and V.
-    auto fetch_k = [&](int blk, int64_t at) {
-        const int64_t row = at < 0 ? 0 : at;
+    auto fetch_k = [&](int blk, uint32_t unit, bool there) {
 #pragma unroll
-        for (int u = 0; u < UNITS; ++u) kreg[u] = load_at<u4>(a.c.K + row * Dp, koff[u]);
-        ksr = load_at<float>(a.c.Ks + row, 4 * lane);
-        vsr = load_at<float>(a.c.Vs + row, 4 * lane);
+        for (int u = 0; u < UNITS; ++u) kreg[u] = load_at<u4>(block_bytes(a.c.K, unit, Dp), koff[u]);
+        ksr = load_at<float>(block_scales(a.c.Ks, unit), 4 * lane);
+        vsr = load_at<float>(block_scales(a.c.Vs, unit), 4 * lane);
         // (applied where the scales are written: a use here would wait for the loads)
-        seen = at < 0 ? 0 : (blk < j.nbp ? j.prefix - blk * CACHE_BLOCK : j.own - (blk - j.nbp) * CACHE_BLOCK);
+        seen = there ? (blk < j.nbp ? j.prefix - blk * CACHE_BLOCK : j.own - (blk - j.nbp) * CACHE_BLOCK) : 0;
     };
-    auto fetch_v = [&](int64_t at) {
+    auto fetch_v = [&](uint32_t unit) {
 #pragma unroll
-        for (int u = 0; u < UNITS; ++u) vreg[u] = load_at<u4>(a.c.V + (at < 0 ? 0 : at) * Dp, voff[u]);
+        for (int u = 0; u < UNITS; ++u) vreg[u] = load_at<u4>(block_bytes(a.c.V, unit, Dp), voff[u]);
     };
-    // rows of block n and of block n + 1, whose K is in registers
-    RowTable table;
-    int64_t row0 = -1, row1 = -1;
+    // places of block n and of block n + 1, whose K is in registers
+    BlockTable table;
+    uint32_t unit0 = 0, unit1 = 0;
+    bool there0 = false, there1 = false;
     if (j.blk0 < j.blk1) { // (in flight while the queries are read)
         table.load(a, j, j.blk0, 1);
-        row0 = table.at(0);
-        fetch_k(j.blk0, row0);
-        fetch_v(row0);
+        unit0 = table.at(0);
+        there0 = table.there(0);
+        fetch_k(j.blk0, unit0, there0);
+        fetch_v(unit0);
     }
 
     // one power of two for all rows (what smaller rows lose is 2^-39 of the tile's largest score)
@@ -873,7 +904,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(const AttnArgs a, cons
     // Operands of P's products in the order of their use: SUM_OPS of the last block's V (16-key tile by
     // 16-key tile, 32 columns by 32), then SCORE_OPS of K (k-step by k-step, 32 keys by 32), read AHEAD
     // of their use.
-    constexpr int SUM_OPS = 4 * DT32, SCORE_OPS = 2 * KSTEPS, AHEAD = 8;
+    constexpr int SUM_OPS = 4 * DT32, SCORE_OPS = 2 * KSTEPS, AHEAD = 6;
     h8 ring[AHEAD];
     const h8 *pk = nullptr, *pv = nullptr;
     auto read_op = [&](int n) {
@@ -895,8 +926,9 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(const AttnArgs a, cons
         // (the first P adds zero weights of a block that is not there: its V must be finite)
         for (int n = tid; n < VBYTES / 16; n += 64 * NW) reinterpret_cast<u4 *>(v_at(1))[n] = u4{0, 0, 0, 0};
         if (j.blk0 + 1 < j.blk1) {
-            row1 = table.at(1);
-            fetch_k(j.blk0 + 1, row1);
+            unit1 = table.at(1);
+            there1 = table.there(1);
+            fetch_k(j.blk0 + 1, unit1, there1);
         }
     }
     __syncthreads();
@@ -907,9 +939,10 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(const AttnArgs a, cons
         const int snext = sbuf == 2 ? 0 : sbuf + 1;
         // this block's list: its first key and those a row sees
         const bool pre = blk < j.nbp;
-        const int k0 = (pre ? blk : blk - j.nbp) * CACHE_BLOCK, mine = row0 < 0 ? 0 : (pre ? j.prefix : lim);
-        const bool masked = row0 < 0 || k0 + CACHE_BLOCK > (pre ? j.prefix : lim_min);
+        const int k0 = (pre ? blk : blk - j.nbp) * CACHE_BLOCK, mine = there0 ? (pre ? j.prefix : lim) : 0;
+        const bool masked = !there0 || k0 + CACHE_BLOCK > (pre ? j.prefix : lim_min);
         // ---- P(blk) ----
+        __builtin_amdgcn_s_setprio(2); // (its products go before the other wave's vector instructions)
         pk = reinterpret_cast<const h8 *>(k_at(kbuf));
         pv = reinterpret_cast<const h8 *>(v_at(kbuf ^ 1));
         const float grown = grow; // asked for by this block's scales
@@ -942,15 +975,18 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(const AttnArgs a, cons
             }
             __builtin_amdgcn_sched_barrier(0);
         }
-        const int64_t this_row = row0;
-        row0 = row1;
-        if (blk + 1 < j.blk1) fetch_v(row1);
+        const uint32_t this_unit = unit0;
+        unit0 = unit1;
+        there0 = there1;
+        if (blk + 1 < j.blk1) fetch_v(unit1);
         if (blk + 2 < j.blk1) {
-            const int x = blk + 2 - j.blk0;
+            const unsigned x = blk + 2 - j.blk0;
             if (x % 64 == 0) table.load(a, j, blk + 2, 1);
-            row1 = table.at(x % 64);
-            fetch_k(blk + 2, row1);
+            unit1 = table.at(x % 64);
+            there1 = table.there(x % 64);
+            fetch_k(blk + 2, unit1, there1);
         }
+        __builtin_amdgcn_s_setprio(0);
         if constexpr (NW == 8) __syncthreads();
 
         // ---- W(blk) ----
@@ -971,7 +1007,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(const AttnArgs a, cons
                 kq[x % 3] = sc[2 * x + hf];
                 vq[x % 3] = sc[16 + 2 * x + hf];
             };
-            float sum = 0.0f;
+            float sums[2] = {0.0f, 0.0f}, big, small; // (two chains)
             read_scales(0);
             read_scales(1);
 #pragma unroll
@@ -983,7 +1019,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(const AttnArgs a, cons
                 for (int x = 0; x < 2; ++x) {
                     const float y =
                         __builtin_amdgcn_exp2f(__builtin_fmaf(score(t, e + x), kq[quad % 3][(e + x) % 4], -m));
-                    sum += y;
+                    sums[x] += y;
                     w[x] = y * vq[quad % 3][(e + x) % 4];
                 }
 #pragma unroll
@@ -992,9 +1028,11 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(const AttnArgs a, cons
                     p[t][0][e + x] = hi;
                     if constexpr (NS == 2) p[t][1][e + x] = static_cast<_Float16>(w[x] - static_cast<float>(hi));
                 }
+#pragma unroll
+                for (int x = 0; x < 2; ++x) pin(sums[x]);
                 if (n % 2 == 1) __builtin_amdgcn_sched_barrier(0);
             }
-            float big, small;
+            float sum = sums[0] + sums[1];
             weight_range(p, big, small);
             if (masked) { // (masked weights are 0 and call for nothing)
                 small = WR::LEAST;
@@ -1002,7 +1040,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(const AttnArgs a, cons
                 for (int e = 0; e < 32; ++e)
                     small = score(e / 8, e % 8) > neg_inf() ? fminf(small, static_cast<float>(p[e / 8][0][e % 8])) : small;
             }
-            if (grown != 1.0f || __any((!set && k0 < mine) || !(big <= H_MAX) || !(sum <= SUM_MAX) || small < WR::LEAST)) {
+            if (grown != 1.0f || __any(calls_for_general(!set && k0 < mine, big, sum, small < WR::LEAST))) {
                 // the general form: the references brought to the block's, small weights in rounds
                 int at = hf; // (the scales are read again, not kept)
                 asm volatile("" : "+v"(at));
@@ -1071,7 +1109,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(const AttnArgs a, cons
                     }
                 } else if (share(1.0f)) {
                     // rounds, with V's bytes from memory (another wave may not have written them to LDS yet)
-                    const uint8_t *v8 = reinterpret_cast<const uint8_t *>(a.c.V + (this_row < 0 ? 0 : this_row) * Dp);
+                    const uint8_t *v8 = reinterpret_cast<const uint8_t *>(block_bytes(a.c.V, this_unit, Dp));
                     uint32_t lane_d = i; // (opaque: addresses are formed here, not kept across the blocks)
                     asm volatile("" : "+v"(lane_d));
                     float down = 1.0f / WR::STEP;
@@ -1107,14 +1145,14 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(const AttnArgs a, cons
         sbuf = snext;
         __syncthreads();
     }
-    pk = nullptr;
     pv = reinterpret_cast<const h8 *>(v_at(kbuf ^ 1));
     if (j.blk0 < j.blk1) {
 #pragma unroll
         for (int n = 0; n < SUM_OPS; ++n) {
             if (n % AHEAD == 0) {
 #pragma unroll
-                for (int x = 0; x < AHEAD; ++x) read_op(n + x);
+                for (int x = 0; x < AHEAD; ++x)
+                    if (n + x < SUM_OPS) read_op(n + x);
             }
             sum_step(n);
         }

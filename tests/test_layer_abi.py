@@ -78,6 +78,11 @@ def test_cache_bytes():
         assert bl.bitlinear_cache_bytes(*bad) == -1, bad
 
 
+def test_cache_block_count():
+    assert bl.bitlinear_cache_bytes(1 << 26, 64, 31, 16) == (1 << 26) * 64 * 31 * 16
+    assert bl.bitlinear_cache_bytes(1 << 26, 64, 32, 16) == -1
+
+
 def cache(**kw):
     a = dict(K=A, K_scale=B, V=C, V_scale=D, pages=4, page_tokens=64, heads=2, head_dim=128)
     a.update(kw)
