@@ -427,7 +427,12 @@ __device__ __forceinline__ float max_abs8(const float (&v)[8])
 // operand order of O^T += V^T P^T: the weights never leave their lane.  The waves of
 // a workgroup (one, two or four) take the chunk's blocks in turn and add their sums
 // in LDS.
-// Bound: HBM (the bytes of the cache); no LDS and no barrier in the loop.
+// Bound: HBM (the bytes of the cache) for 16 rows, no LDS and no barrier in the loop:
+// 2 x 8 rows on 60001 keys of 8 heads of 128, 127 MB: 26 us, 4.9 TB/s.  With more row
+// tiles the conversion of each (5 x 8 rows: 54 us, 376 MB through L2); with 176
+// sequences' own keys of up to 512, 1408 jobs of unequal length, the longest one (32
+// us for 107 MB: a wave alone takes 3 us a block).  More rows a wave (two and three
+// tiles on one conversion) need registers past 256 and came to the same.
 // ---------------------------------------------------------------------------
 template <int DT, int DC>
 __global__ __launch_bounds__(256, DC == 4 ? 1 : 2) void k_attn_stream(const AttnArgs a, const AttnPlan pl)
@@ -1183,7 +1188,8 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(const AttnArgs a, cons
 // Joins the parts of every row.  LPR lanes of four columns each cover a row.  With
 // few parts (WIDE false) a group of LPR lanes takes a row and goes through its
 // parts four at a time; with many, a wave takes a row, its lanes reading the (m, l)
-// of 64 parts at once and 64 / LPR parts' sums side by side.
+// of 64 parts at once and 64 / LPR parts' sums side by side.  Bound: HBM / L2: 11264
+// rows of 128 from 6 parts, 38 MB: 8.6 us; 320 rows from 20 parts: 5 us.
 template <int DT, int LPR, bool WIDE>
 __global__ __launch_bounds__(256) void k_attn_join(const AttnArgs a, const AttnPlan pl, int64_t rows)
 {
@@ -1348,15 +1354,18 @@ AttnPlan attn_plan(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head
     p.rows_prefix = tile_rows(tokens * G, head_dim, dtype);
     p.rows_own = tile_rows(max_q * G, head_dim, dtype);
     p.tiles_own = static_cast<int>(div_up(max_q * G, p.rows_own));
-    // one pass over prefix and own keys where a sequence fills row tiles of its own anyway, or the
-    // prefix is short
+    // one pass over prefix and own keys where a sequence fills row tiles of its own anyway (4 x 400 query
+    // tokens x 8 rows on 2100 keys: 207 us, with a pass of its own for the prefix 222 + 25), or the prefix is
+    // short
     p.joint = nbp > 0 && (max_q * G >= 128 || 2 * prefix * kv_heads * dp * (seqs - 1) <= kJointBytes);
     const int64_t tp = p.joint || nbp == 0 ? 0 : div_up(tokens * G, p.rows_prefix);
+    // with the same kernel for both, one launch (5 x 8 rows on 60001 keys with 333 of their own: 54 us
+    // for both, 52 + 12 one after the other)
     p.together = tp > 0 && p.rows_prefix == 16;
     AttnCut cut{0, 0, 4};
     if (tp > 0)
-        cut = choose_cut(tp * kv_heads, nbp, p.rows_prefix, head_dim, 0, p.together && nbo > 0 ? seqs * p.tiles_own * kv_heads : 0,
-                         true);
+        cut = choose_cut(tp * kv_heads, nbp, p.rows_prefix, head_dim, 0,
+                         p.together && nbo > 0 ? seqs * p.tiles_own * kv_heads : 0, true);
     p.chunk_prefix = cut.chunk;
     p.splits_prefix = cut.splits;
     p.waves_prefix = cut.waves;

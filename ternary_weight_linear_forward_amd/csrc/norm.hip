@@ -11,6 +11,9 @@
 // binary64: a term h^2 is exact there, so rho does not depend on the order of
 // the sum to binary32's precision, and no h overflows it.
 // Bound: HBM for many rows; for few, the chain load - sum - maximum - store.
+// Measured (a copy of 1 GiB moves 4.78 TB/s, read and written): 8192 x 8192 bf16 with
+// residual and kept sum, 470 MB: 103 us, 4.6 TB/s; 176 x 8640 fp32: 7.0 us; 1 x 3200:
+// 3.8 us.  The same passes as separate reads of the row took 3.6 times as long.
 #include "common.h"
 #include "launch.h"
 #include "rows.h"
@@ -206,7 +209,7 @@ static void launch_norm(const NormArgs &a, hipStream_t stream)
     const int64_t need = tiled ? width / 8 : (a.K + 15) / 16 * 2; // pieces of a row
     const dim3 grid(static_cast<unsigned>(tiled ? (a.M + 15) / 16 * 16 : a.M));
     // many rows: workgroups of four waves, so that rows in different phases share a CU;
-    // few: one piece per thread as far as 1024 threads go
+    // few: one piece per thread as far as 1024 threads go, for the shorter chain
     const int64_t threads = a.M >= 1024 ? 256 : 1024;
     const int64_t ppt = need <= threads ? 1 : need <= 2 * threads ? 2 : need <= 4 * 1024 ? 4 : 0;
     const dim3 block(static_cast<unsigned>(ppt ? ((need + ppt - 1) / ppt + 63) / 64 * 64 : 1024));
@@ -229,7 +232,8 @@ hipError_t launch_norm_quantize(const NormArgs &a, hipStream_t stream)
     return hipGetLastError();
 }
 
-// V = q (beta / 127), a piece per thread, 'chunks' workgroups a row.
+// V = q (beta / 127), a piece per thread, 'chunks' workgroups a row.  Bound: HBM
+// (8192 x 8192 to bf16 behind the norm: 33 us, 6.0 TB/s, the bytes partly in cache).
 template <int DT>
 __global__ __launch_bounds__(256) void k_dequantize(const int8_t *Xq, int64_t ldq, const float *beta, int64_t K, void *V,
                                                     int64_t ldv, uint32_t chunks)
@@ -266,7 +270,9 @@ hipError_t launch_dequantize_act(const int8_t *Xq, int64_t ldq, const float *bet
 
 // ---- gradient ---------------------------------------------------------------
 // A workgroup takes rows p, p + parts, ... and keeps its share of dW, a row of K
-// sums, in registers; k_norm_bwd_sum adds the workgroups' rows in a fixed order.
+// sums, in registers; k_norm_bwd_sum adds the workgroups' rows in a fixed order, so
+// that no atomic's order reaches dW.  Bound: HBM.  2048 x 8640 bf16 with dH, 177 MB:
+// 39 us, 4.6 TB/s, and 4.7 us for the sum; 100 x 3200 fp32: 5.1 and 3.3 us.
 int64_t norm_bwd_parts(int64_t M, int64_t K)
 {
     const int64_t parts = K <= 4096 ? 512 : 256; // one or two for each CU
