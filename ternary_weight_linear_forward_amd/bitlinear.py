@@ -24,9 +24,9 @@ if not os.path.exists(LIB_PATH):
 # library's libamdhip64.so.7 dependency binds to that same runtime: two HIP
 # runtimes in one process would not share devices, streams or allocations.
 try:
-    import torch  # noqa: F401
+    import torch
 except ImportError:
-    pass
+    torch = None
 
 _lib = ctypes.CDLL(LIB_PATH)
 
@@ -340,18 +340,15 @@ def _torch():
 def _stream(stream=None) -> int:
     if stream is not None:
         return int(stream.cuda_stream)
-    torch = _torch()
-    # the current stream's handle without a Stream object around it (0.4 us instead of 3)
+    # the current stream's handle without a Stream object around it (0.3 us instead of 3)
     return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
-_CODES: dict = {}
+_CODES = {} if torch is None else {torch.float32: F32, torch.bfloat16: BF16, torch.int8: I8, torch.int32: I32}
+_FLOATS = {} if torch is None else {torch.float32: F32, torch.bfloat16: BF16}
 
 
 def _dtype_code(t) -> int:
-    if not _CODES:
-        torch = _torch()
-        _CODES.update({torch.float32: F32, torch.bfloat16: BF16, torch.int8: I8, torch.int32: I32})
     return _CODES[t.dtype]
 
 
@@ -575,10 +572,10 @@ def backward_dw(Xq, beta, dY, K: int, out=None, stream=None):
     return out
 
 
-def _row_stride(t, where: str, M: int, K: int, *dtypes) -> int:
-    """Row stride of a tensor [M x K] (at least K for a single row); refuses other
-    shapes, other dtypes and rows with gaps."""
-    if t.dtype not in dtypes or t.shape != (M, K):
+def _row_stride(t, where: str, M: int, K: int, dtype=None) -> int:
+    """Row stride of an fp32 or bf16 tensor [M x K] (at least K for a single row);
+    refuses other shapes, other dtypes and rows with gaps."""
+    if (t.dtype not in _FLOATS if dtype is None else t.dtype != dtype) or t.shape != (M, K):
         raise BitlinearError(ERR_INVALID_ARG, where)
     ld, step = t.stride()
     if step != 1 and K > 1:
@@ -587,12 +584,16 @@ def _row_stride(t, where: str, M: int, K: int, *dtypes) -> int:
 
 
 def _norm_weight(w, K: int, where: str) -> int | None:
-    torch = _torch()
     if w is None:
         return None
     if w.dtype != torch.float32 or w.shape != (K,) or (K > 1 and w.stride(0) != 1):
         raise BitlinearError(ERR_INVALID_ARG, where)
     return w.data_ptr()
+
+
+def _new_rows(like, ld: int, M: int, K: int):
+    """Rows [M x K] without gaps in the dtype of 'like', a tensor [M x K] of row stride ld."""
+    return torch.empty_like(like) if ld == K else like.new_empty((M, K))
 
 
 def norm_quantize(X, w=None, eps: float = 1e-5, residual=None, H=None, keep_h: bool = True, layout: int | None = None,
@@ -603,33 +604,34 @@ def norm_quantize(X, w=None, eps: float = 1e-5, residual=None, H=None, keep_h: b
     residual's dtype (X's without one; written to 'H' if given, which may be
     the residual; None with keep_h=False); Xq int8 [M x ldq], ldq = K rounded
     up to 16, or with a weight layout the 1-d tiled activations forward takes."""
-    torch = _torch()
     name = "norm_quantize"
     M, K = X.shape
-    device = X.device
-    ldx = _row_stride(X, name, M, K, torch.float32, torch.bfloat16)
-    ref, ldr = X, 0
-    if residual is not None:
-        ref, ldr = residual, _row_stride(residual, name, M, K, torch.float32, torch.bfloat16)
+    ldx = _row_stride(X, name, M, K)
+    if residual is None:
+        ref, ldref, rp, ldr = X, ldx, None, 0
+    else:
+        ldref = ldr = _row_stride(residual, name, M, K)
+        ref, rp = residual, residual.data_ptr()
     wp = _norm_weight(w, K, name)
-    ldh = 0
+    hp, ldh = None, 0
     if H is not None:
         ldh = _row_stride(H, name, M, K, ref.dtype)
+        hp = H.data_ptr()
     elif keep_h:
-        H, ldh = torch.empty((M, K), dtype=ref.dtype, device=device), K
+        H, ldh = _new_rows(ref, ldref, M, K), K
+        hp = H.data_ptr()
     if layout is None:
-        ldq = (K + 15) // 16 * 16
-        Xq = torch.empty((M, ldq), dtype=torch.int8, device=device)
+        ldq, qdt, lay = (K + 15) // 16 * 16, I8, LAYOUT_I2
+        Xq = X.new_empty((M, ldq), dtype=torch.int8)
     else:
-        ldq, nbytes = 0, bitlinear_act_tiled_bytes(M, K, layout)
+        ldq, qdt, lay, nbytes = 0, I8_TILED, layout, bitlinear_act_tiled_bytes(M, K, layout)
         if nbytes < 0:
             raise BitlinearError(ERR_INVALID_ARG, name)
-        Xq = torch.empty(nbytes, dtype=torch.int8, device=device)
-    beta = torch.empty(M, dtype=torch.float32, device=device)
-    _check(_lib.bitlinear_norm_quantize(
-        X.data_ptr(), _dtype_code(X), M, K, ldx, _ptr(residual), ldr, wp, eps, _ptr(H), _dtype_code(ref), ldh,
-        Xq.data_ptr(), I8 if layout is None else I8_TILED, ldq, LAYOUT_I2 if layout is None else layout,
-        beta.data_ptr(), _stream(stream)), "bitlinear_norm_quantize")
+        Xq = X.new_empty(nbytes, dtype=torch.int8)
+    beta = X.new_empty(M, dtype=torch.float32)
+    _check(_lib.bitlinear_norm_quantize(X.data_ptr(), _FLOATS[X.dtype], M, K, ldx, rp, ldr, wp, eps, hp,
+                                        _FLOATS[ref.dtype], ldh, Xq.data_ptr(), qdt, ldq, lay, beta.data_ptr(),
+                                        _stream(stream)), "bitlinear_norm_quantize")
     if stream is not None:
         _record(stream, H, Xq, beta)
     return H, Xq, beta
@@ -650,10 +652,9 @@ def _ld(t) -> int:
 
 def dequantize_act(Xq, beta, K: int, dtype=None, out=None, stream=None):
     """The values of int8 rows Xq [M x >=K] with beta [M]: q * (beta / 127), fp32 or bf16 [M x K]."""
-    torch = _torch()
     M, ldq = Xq.shape[0], _ld(Xq)
     if out is None:
-        out, ldv = torch.empty((M, K), dtype=dtype or torch.float32, device=Xq.device), K
+        out, ldv = beta.new_empty((M, K), dtype=dtype or torch.float32), K
     else:
         ldv = _ld(out)
     _check(_lib.bitlinear_dequantize_act(Xq.data_ptr(), ldq, beta.data_ptr(), M, K, out.data_ptr(), _dtype_code(out),
@@ -667,26 +668,25 @@ def norm_backward(dY, H, w=None, eps: float = 1e-5, dH=None, dX=None, want_dw: b
     """Gradient of the norm (bitlinear_norm_backward): dY fp32 [M x K], H the
     norm's kept sum, dH the gradient arriving through the residual stream (H's
     dtype, or None).  Returns (dX in H's dtype, dW fp32 [K] or None)."""
-    torch = _torch()
     name = "norm_backward"
     M, K = H.shape
     dtype = H.dtype
     lddy = _row_stride(dY, name, M, K, torch.float32)
-    ldh = _row_stride(H, name, M, K, torch.float32, torch.bfloat16)
+    ldh = _row_stride(H, name, M, K)
     lddh = 0 if dH is None else _row_stride(dH, name, M, K, dtype)
     if dX is None:
-        dX, lddx = torch.empty((M, K), dtype=dtype, device=H.device), K
+        dX, lddx = _new_rows(H, ldh, M, K), K
     else:
         lddx = _row_stride(dX, name, M, K, dtype)
     wp = _norm_weight(w, K, name)
-    dW = torch.empty(K, dtype=torch.float32, device=H.device) if want_dw else None
+    dW = dY.new_empty(K) if want_dw else None
     nws = _lib.bitlinear_norm_backward_workspace_bytes(M, K, 1 if want_dw else 0)
     if nws < 0:
         raise BitlinearError(ERR_INVALID_ARG, name)
     if nws > 0 and (ws is None or ws.numel() < nws):
         ws = torch.empty(nws, dtype=torch.uint8, device=H.device)
     _check(_lib.bitlinear_norm_backward(
-        dY.data_ptr(), lddy, H.data_ptr(), _dtype_code(H), ldh, wp, eps, _ptr(dH), lddh, M, K, dX.data_ptr(), lddx,
+        dY.data_ptr(), lddy, H.data_ptr(), _FLOATS[dtype], ldh, wp, eps, _ptr(dH), lddh, M, K, dX.data_ptr(), lddx,
         _ptr(dW), _ptr(ws) if nws > 0 else None, nws, _stream(stream)), "bitlinear_norm_backward")
     if stream is not None:
         _record(stream, dX, dW, ws)
@@ -700,7 +700,6 @@ class KVCache:
     up to 16.  KVCache.empty allocates one."""
 
     def __init__(self, k, v, k_scale, v_scale, head_dim: int):
-        torch = _torch()
         pages, heads, page_tokens, dp = k.shape
         scales = (pages, heads, page_tokens)
         if v.shape != (pages, heads, page_tokens // 64, dp, 64) or page_tokens % 64 or \
@@ -716,7 +715,6 @@ class KVCache:
 
     @classmethod
     def empty(cls, pages: int, heads: int, head_dim: int, page_tokens: int = 64, device="cuda"):
-        torch = _torch()
         if bitlinear_cache_bytes(pages, page_tokens, heads, head_dim) < 0:
             raise BitlinearError(ERR_INVALID_ARG, "KVCache")
         dp = (head_dim + 15) // 16 * 16
@@ -729,8 +727,7 @@ class KVCache:
 
 def _kv_strides(cache, t, tokens, where):
     """Token and head stride of a tensor [tokens x heads x head_dim] of the cache's heads."""
-    torch = _torch()
-    if (t.dtype != torch.bfloat16 and t.dtype != torch.float32) or t.shape != (tokens, cache.heads, cache.head_dim):
+    if t.dtype not in _FLOATS or t.shape != (tokens, cache.heads, cache.head_dim):
         raise BitlinearError(ERR_INVALID_ARG, where)
     lt, lh, step = t.stride()
     if step != 1 and cache.head_dim > 1:
@@ -741,7 +738,6 @@ def _kv_strides(cache, t, tokens, where):
 def cache_write(cache: KVCache, K, V, slots, stream=None) -> None:
     """Quantise K, V [tokens x heads x head_dim] (fp32/bf16) into the cache's
     slots (int64 [tokens]; a slot outside the cache is skipped)."""
-    torch = _torch()
     n = slots.numel()
     lkt, lkh = _kv_strides(cache, K, n, "cache_write")
     lvt, lvh = _kv_strides(cache, V, n, "cache_write")
@@ -753,7 +749,6 @@ def cache_write(cache: KVCache, K, V, slots, stream=None) -> None:
 
 def cache_read(cache: KVCache, slots, dtype=None, stream=None):
     """(K, V) [tokens x heads x head_dim] of the cache's slots (zeros for a slot outside it)."""
-    torch = _torch()
     n = slots.numel()
     if slots.dtype != torch.int64 or not slots.is_contiguous():
         raise BitlinearError(ERR_INVALID_ARG, "cache_read")
@@ -774,16 +769,16 @@ def attention(cache: KVCache, Q, own_pages, own_len, max_own: int, prefix_pages=
     own_len int32 [seqs] (at most max_own); prefix_pages int32; q_start int32
     [seqs + 1] or None (max_q tokens each); scale 1 / sqrt(head_dim) by
     default.  Returns O (Q's shape and dtype), or (O, lse fp32 [tokens x heads])."""
-    torch = _torch()
     name = "attention"
     tokens, heads, D = Q.shape
     seqs = own_len.numel()
     pt, i32 = cache.page_tokens, torch.int32
-    if (Q.dtype != torch.bfloat16 and Q.dtype != torch.float32) or D != cache.head_dim or own_pages.dim() != 2:
+    if Q.dtype not in _FLOATS or D != cache.head_dim or own_pages.dim() != 2:
         raise BitlinearError(ERR_INVALID_ARG, name)
     lqt, lqh, step = Q.stride()
     if out is None:
-        out, lot, loh, ostep = torch.empty((tokens, heads, D), dtype=Q.dtype, device=Q.device), heads * D, D, 1
+        out = torch.empty_like(Q) if Q.is_contiguous() else Q.new_empty((tokens, heads, D))
+        lot, loh, ostep = heads * D, D, 1
     else:
         if out.dtype != Q.dtype or out.shape != Q.shape:
             raise BitlinearError(ERR_INVALID_ARG, name)

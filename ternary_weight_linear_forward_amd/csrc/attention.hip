@@ -378,21 +378,33 @@ __device__ __forceinline__ float row_factor(float scale, int e2)
 }
 
 // NV times eight query values of a row, the n-th at column col(n), zeros past
-// head_dim.  With head_dim a multiple of 8 the loads are unconditional (a column
-// past the row reads its start), so that they go out together.
+// head_dim.  The loads are unconditional, so that they go out together: eight values
+// that reach past the row are its last eight, moved down afterwards.
 template <int DT, int NV, class Col>
 __device__ __forceinline__ void load_queries(const AttnArgs &a, int64_t off, const Col &col, float (&v)[NV][8])
 {
-    if (a.c.D % 8 == 0) {
+    const int D = a.c.D;
+    if (D >= 8) {
 #pragma unroll
-        for (int n = 0; n < NV; ++n) load8<DT>(a.Q, off + (col(n) < a.c.D ? col(n) : 0), 8, v[n]);
+        for (int n = 0; n < NV; ++n) load8<DT>(a.Q, off + min(col(n), D - 8), 8, v[n]);
 #pragma unroll
-        for (int n = 0; n < NV; ++n)
+        for (int n = 0; n < NV; ++n) {
+            if (D % 8 != 0) {
+                const int down = max(col(n) - (D - 8), 0);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[n][e] = col(n) < a.c.D ? v[n][e] : 0.0f;
+                for (int step = 4; step > 0; step >>= 1)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float next = e + step < 8 ? v[n][e + step < 8 ? e + step : 0] : 0.0f;
+                        v[n][e] = down & step ? next : v[n][e];
+                    }
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[n][e] = col(n) < D ? v[n][e] : 0.0f;
+        }
     } else {
 #pragma unroll
-        for (int n = 0; n < NV; ++n) load8<DT>(a.Q, off + col(n), a.c.D - col(n), v[n]);
+        for (int n = 0; n < NV; ++n) load8<DT>(a.Q, off + col(n), D - col(n), v[n]);
     }
 }
 
