@@ -378,33 +378,21 @@ __device__ __forceinline__ float row_factor(float scale, int e2)
 }
 
 // NV times eight query values of a row, the n-th at column col(n), zeros past
-// head_dim.  The loads are unconditional, so that they go out together: eight values
-// that reach past the row are its last eight, moved down afterwards.
+// head_dim.  With head_dim a multiple of 8 the loads are unconditional (a column
+// past the row reads its start), so that they go out together.
 template <int DT, int NV, class Col>
 __device__ __forceinline__ void load_queries(const AttnArgs &a, int64_t off, const Col &col, float (&v)[NV][8])
 {
-    const int D = a.c.D;
-    if (D >= 8) {
+    if (a.c.D % 8 == 0) {
 #pragma unroll
-        for (int n = 0; n < NV; ++n) load8<DT>(a.Q, off + min(col(n), D - 8), 8, v[n]);
+        for (int n = 0; n < NV; ++n) load8<DT>(a.Q, off + (col(n) < a.c.D ? col(n) : 0), 8, v[n]);
 #pragma unroll
-        for (int n = 0; n < NV; ++n) {
-            if (D % 8 != 0) {
-                const int down = max(col(n) - (D - 8), 0);
+        for (int n = 0; n < NV; ++n)
 #pragma unroll
-                for (int step = 4; step > 0; step >>= 1)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float next = e + step < 8 ? v[n][e + step < 8 ? e + step : 0] : 0.0f;
-                        v[n][e] = down & step ? next : v[n][e];
-                    }
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[n][e] = col(n) < D ? v[n][e] : 0.0f;
-        }
+            for (int e = 0; e < 8; ++e) v[n][e] = col(n) < a.c.D ? v[n][e] : 0.0f;
     } else {
 #pragma unroll
-        for (int n = 0; n < NV; ++n) load8<DT>(a.Q, off + col(n), D - col(n), v[n]);
+        for (int n = 0; n < NV; ++n) load8<DT>(a.Q, off + col(n), a.c.D - col(n), v[n]);
     }
 }
 
@@ -569,26 +557,31 @@ __global__ __launch_bounds__(256, DC == 4 ? 1 : 2) void k_attn_stream(const Attn
         // the next block's keys, while this block's weights are formed
         if (next) load_k(unit);
         h8 p[2][NS];
-        float sum = 0.0f, big, small;
+        float sum = 0.0f, big = __builtin_inff(), small = 0.0f;
+        // (before any V_scale was seen, a wave's first block as a rule, the general form is all there is)
+        bool rare = __builtin_amdgcn_readfirstlane(__float_as_int(ref)) == 0;
+        if (!rare) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            float w[8];
+            for (int h = 0; h < 2; ++h) {
+                float w[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float x = __builtin_amdgcn_exp2f(s[2 * h + e / 4][e % 4] - m);
-                sum += x;
-                w[e] = x * (vs[2 * h + e / 4][e % 4] * vscale);
+                for (int e = 0; e < 8; ++e) {
+                    const float x = __builtin_amdgcn_exp2f(s[2 * h + e / 4][e % 4] - m);
+                    sum += x;
+                    w[e] = x * (vs[2 * h + e / 4][e % 4] * vscale);
+                }
+                split_weights<NS>(w, p[h]);
             }
-            split_weights<NS>(w, p[h]);
-        }
-        weight_range(p, big, small);
-        if (masked) { // (masked weights are 0 and call for nothing)
-            small = WR::LEAST;
+            weight_range(p, big, small);
+            if (masked) { // (masked weights are 0 and call for nothing)
+                small = WR::LEAST;
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-                small = s[e / 4][e % 4] > neg_inf() ? fminf(small, static_cast<float>(p[e / 8][0][e % 8])) : small;
+                for (int e = 0; e < 16; ++e)
+                    small = s[e / 4][e % 4] > neg_inf() ? fminf(small, static_cast<float>(p[e / 8][0][e % 8])) : small;
+            }
+            rare = __any(calls_for_general(!set && k0 < mine, big, sum, small < WR::LEAST));
         }
-        if (__any(calls_for_general((!set && k0 < mine) || ref == 0.0f, big, sum, small < WR::LEAST))) {
+        if (rare) {
             // the general form: references brought to this block's largest, small weights in rounds
             float vtop = 0.0f, grown = 1.0f;
 #pragma unroll
