@@ -1317,11 +1317,11 @@ struct AttnCut {
 // The cut with the least time, in eighths of a block, of all rounds of the card: a
 // wave (of k_attn_stream, whose waves take blocks in turn) or workgroup (of
 // k_attn_tile) costs its blocks and about four more for its start and end; waves
-// that join their sums, and a split more whose sums go through memory, cost the
-// eighths given, and the join itself, where there would be none (joined), four
-// blocks.  waves: those of k_attn_stream, 0 for any; others: workgroups of the same
-// launch.
-AttnCut choose_cut(int64_t wgs, int64_t blocks, int rows, int64_t head_dim, int waves, int64_t others, bool joined)
+// that join their sums cost half a block, a part's sums on their way through memory
+// 'part', and the join itself, where there would be none (joined), four blocks.
+// waves: those of k_attn_stream, 0 for any; others: workgroups of the same launch.
+AttnCut choose_cut(int64_t wgs, int64_t blocks, int rows, int64_t head_dim, int waves, int64_t others, int64_t part,
+                   bool joined)
 {
     AttnCut best{0, 0, waves ? waves : 4};
     if (blocks == 0) return best;
@@ -1335,8 +1335,8 @@ AttnCut choose_cut(int64_t wgs, int64_t blocks, int rows, int64_t head_dim, int 
         for (int64_t s = 1; s <= 64 && (s == 1 || div_up(blocks, s) >= (stream ? w : 2)); ++s) {
             const int64_t c = div_up(blocks, s), n = div_up(blocks, c);
             const int64_t cost =
-                8 * div_up(wgs * n + others, slots) * ((stream ? div_up(c, w) : c) + 4) + n +
-                (stream && w > 1 ? 4 : 0) + (n > 1 && !joined ? 32 : 0);
+                8 * div_up(wgs * n + others, slots) * ((stream ? div_up(c, w) : c) + 4) +
+                (stream && w > 1 ? 4 : 0) + (n > 1 || joined ? n * part : 0) + (n > 1 && !joined ? 32 : 0);
             if (least < 0 || cost < least) {
                 least = cost;
                 best = AttnCut{static_cast<int>(c), static_cast<int>(n), w};
@@ -1367,16 +1367,21 @@ AttnPlan attn_plan(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head
     // with the same kernel for both, one launch (5 x 8 rows on 60001 keys with 333 of their own: 54 us
     // for both, 52 + 12 one after the other)
     p.together = tp > 0 && p.rows_prefix == 16;
+    // a part's sums, written and read at a copy's rate, in eighths of a block's 2.6 us
+    const int64_t part = 1 + tokens * heads * dp * 6 / 1000000;
+    // workgroups with rows at most: a sequence's last tile is its own.  With both, 2 x 300 query tokens x 64
+    // heads on 5000 keys are split (158 -> 135 us) and 4 x 400 on 2100 are not (204; split 222)
+    const int64_t busy = min(seqs * p.tiles_own, div_up(tokens * G, p.rows_own) + seqs) * kv_heads;
     AttnCut cut{0, 0, 4};
     if (tp > 0)
         cut = choose_cut(tp * kv_heads, nbp, p.rows_prefix, head_dim, 0,
-                         p.together && nbo > 0 ? seqs * p.tiles_own * kv_heads : 0, true);
+                         p.together && nbo > 0 ? busy : 0, part, true);
     p.chunk_prefix = cut.chunk;
     p.splits_prefix = cut.splits;
     p.waves_prefix = cut.waves;
     p.wgs_prefix = static_cast<int>(tp * kv_heads * p.splits_prefix);
-    cut = choose_cut(seqs * p.tiles_own * kv_heads, p.joint ? nbp + nbo : nbo, p.rows_own, head_dim,
-                     p.together ? p.waves_prefix : 0, p.together ? p.wgs_prefix : 0, tp > 0);
+    cut = choose_cut(busy, p.joint ? nbp + nbo : nbo, p.rows_own, head_dim,
+                     p.together ? p.waves_prefix : 0, p.together ? p.wgs_prefix : 0, part, tp > 0);
     p.chunk_own = cut.chunk;
     p.splits_own = cut.splits;
     p.waves_own = cut.waves;
