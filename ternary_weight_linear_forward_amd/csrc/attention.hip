@@ -1297,8 +1297,8 @@ int64_t div_up(int64_t x, int64_t y) { return (x + y - 1) / y; }
 // and of k_attn_tile: 60001 x 24: 48, 81; x 64: 69, 82; x 96: 95, 86; 12000 x 96: 37,
 // 50; x 128: 40, 52; x 256: 62, 59; x 1024: 187, 108.  With the registers of fp32
 // queries (two terms) and head_dim past 64, or of head_dim past 128, k_attn_stream
-// won at every size (400 query tokens x 4 on 2100 keys, heads of 256, bf16: 716, 838;
-// of 128, fp32: 758, 1109).  Eight waves share a conversion of the keys and need
+// won at every size (400 query tokens x 4 on 2100 keys, heads of 256, bf16: 738, 838;
+// of 128, fp32: 813, 1109).  Eight waves share a conversion of the keys and need
 // registers for two waves a SIMD (fp32 queries do not leave them).
 constexpr int64_t kStreamRows = 96;
 
