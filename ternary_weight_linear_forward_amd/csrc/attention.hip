@@ -26,12 +26,15 @@
 //    2^-21 of the reference's): blocks form no maximum unless one of that happens.
 //    Weights that are too small even then are multiplied in further rounds, brought
 //    up by STEP each, into sums of their own.  l sums the unrounded p.
+#include "attn_plan.h"
 #include "cache_core.h"
 #include "common.h"
 #include "launch.h"
 #include "rows.h"
 
 namespace bl {
+
+static_assert(ATTN_BLOCK == CACHE_BLOCK, "the plan counts blocks of the cache");
 
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
@@ -1289,115 +1292,12 @@ __global__ __launch_bounds__(256) void k_attn_join(const AttnArgs a, const AttnP
 // ---- host -------------------------------------------------------------------
 namespace {
 
-int64_t div_up(int64_t x, int64_t y) { return (x + y - 1) / y; }
-
-// Rows a workgroup takes: 16 with k_attn_stream, 128 or 256 (four or eight waves)
-// with k_attn_tile.  Row tiles that read the cache again from L2 cost less than a
-// mostly empty tile of 128: bf16, 8 kv heads of 128, keys x rows, us of k_attn_stream
-// and of k_attn_tile: 60001 x 24: 48, 81; x 64: 69, 82; x 96: 95, 86; 12000 x 96: 37,
-// 50; x 128: 40, 52; x 256: 62, 59; x 1024: 187, 108.  With the registers of fp32
-// queries (two terms) and head_dim past 64, or of head_dim past 128, k_attn_stream
-// won at every size (400 query tokens x 4 on 2100 keys, heads of 256, bf16: 738, 838;
-// of 128, fp32: 813, 1109).  Eight waves share a conversion of the keys and need
-// registers for two waves a SIMD (fp32 queries do not leave them).
-constexpr int64_t kStreamRows = 96;
-
-int tile_rows(int64_t rows, int64_t head_dim, int dtype)
-{
-    if (rows <= kStreamRows || head_dim > 128 || (dtype == DT_F32 && head_dim > 64)) return 16;
-    return rows <= 128 || head_dim <= 64 ? 128 : 256;
-}
-
-// How 'wgs' workgroups' passes over 'blocks' key blocks are split: blocks of a
-// part, parts, waves of a workgroup.
-struct AttnCut {
-    int chunk, splits, waves;
-};
-
-// The cut with the least time, in eighths of a block, of all rounds of the card: a
-// wave (of k_attn_stream, whose waves take blocks in turn) or workgroup (of
-// k_attn_tile) costs its blocks and about four more for its start and end; waves
-// that join their sums cost half a block, a part's sums on their way through memory
-// 'part', and the join itself, where there would be none (joined), four blocks.
-// waves: those of k_attn_stream, 0 for any; others: workgroups of the same launch.
-AttnCut choose_cut(int64_t wgs, int64_t blocks, int rows, int64_t head_dim, int waves, int64_t others, int64_t part,
-                   bool joined)
-{
-    AttnCut best{0, 0, waves ? waves : 4};
-    if (blocks == 0) return best;
-    const int dc = head_dim <= 64 ? 1 : head_dim <= 128 ? 2 : 4;
-    const bool stream = rows == 16;
-    int64_t least = -1;
-    for (int w = 1; w <= 8; w *= 2) {
-        if (stream ? w > 4 || (waves && w != waves) : w != rows / 32) continue;
-        const bool alone = stream ? dc == 4 : rows == 256; // one wave a SIMD, one workgroup a CU; or two
-        const int64_t slots = stream ? 256 * (4 / w) * (alone ? 1 : 2) : 256 * (alone ? 1 : 2);
-        for (int64_t s = 1; s <= 64 && (s == 1 || div_up(blocks, s) >= (stream ? w : 2)); ++s) {
-            const int64_t c = div_up(blocks, s), n = div_up(blocks, c);
-            const int64_t cost =
-                8 * div_up(wgs * n + others, slots) * ((stream ? div_up(c, w) : c) + 4) +
-                (stream && w > 1 ? 4 : 0) + (n > 1 || joined ? n * part : 0) + (n > 1 && !joined ? 32 : 0);
-            if (least < 0 || cost < least) {
-                least = cost;
-                best = AttnCut{static_cast<int>(c), static_cast<int>(n), w};
-            }
-        }
-    }
-    return best;
-}
-
-// Reading the prefix again for each sequence costs less than a launch and a join
-// of their own up to about this many bytes (a launch and its join are near 8 us).
-constexpr int64_t kJointBytes = int64_t(16) << 20;
-
-AttnPlan attn_plan(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t seqs, int64_t max_q,
-                   int64_t max_own, int64_t prefix, int dtype)
-{
-    AttnPlan p;
-    const int64_t G = heads / kv_heads, dp = div_up(head_dim, 16) * 16;
-    const int64_t nbp = div_up(prefix, CACHE_BLOCK), nbo = div_up(max_own, CACHE_BLOCK);
-    p.rows_prefix = tile_rows(tokens * G, head_dim, dtype);
-    p.rows_own = tile_rows(max_q * G, head_dim, dtype);
-    p.tiles_own = static_cast<int>(div_up(max_q * G, p.rows_own));
-    // one pass over prefix and own keys where a sequence fills row tiles of its own anyway (4 x 400 query
-    // tokens x 8 rows on 2100 keys: 207 us, with a pass of its own for the prefix 222 + 25), or the prefix is
-    // short
-    p.joint = nbp > 0 && (max_q * G >= 128 || 2 * prefix * kv_heads * dp * (seqs - 1) <= kJointBytes);
-    const int64_t tp = p.joint || nbp == 0 ? 0 : div_up(tokens * G, p.rows_prefix);
-    // with the same kernel for both, one launch (5 x 8 rows on 60001 keys with 333 of their own: 54 us
-    // for both, 52 + 12 one after the other)
-    p.together = tp > 0 && p.rows_prefix == 16;
-    // a part's sums, written and read at a copy's rate, in eighths of a block's 2.6 us
-    const int64_t part = 1 + tokens * heads * dp * 6 / 1000000;
-    // workgroups with rows at most: a sequence's last tile is its own.  With both, 2 x 300 query tokens x 64
-    // heads on 5000 keys are split (158 -> 135 us) and 4 x 400 on 2100 are not (204; split 222)
-    const int64_t busy = min(seqs * p.tiles_own, div_up(tokens * G, p.rows_own) + seqs) * kv_heads;
-    AttnCut cut{0, 0, 4};
-    if (tp > 0)
-        cut = choose_cut(tp * kv_heads, nbp, p.rows_prefix, head_dim, 0,
-                         p.together && nbo > 0 ? busy : 0, part, true);
-    p.chunk_prefix = cut.chunk;
-    p.splits_prefix = cut.splits;
-    p.waves_prefix = cut.waves;
-    p.wgs_prefix = static_cast<int>(tp * kv_heads * p.splits_prefix);
-    cut = choose_cut(busy, p.joint ? nbp + nbo : nbo, p.rows_own, head_dim,
-                     p.together ? p.waves_prefix : 0, p.together ? p.wgs_prefix : 0, part, tp > 0);
-    p.chunk_own = cut.chunk;
-    p.splits_own = cut.splits;
-    p.waves_own = cut.waves;
-    p.wgs_own = static_cast<int>(seqs * p.tiles_own * kv_heads * p.splits_own);
-    p.wg0 = 0;
-    const int64_t parts = p.splits_prefix + p.splits_own;
-    p.direct = parts == 1 && p.splits_own == 1;
-    p.ml_off = p.direct ? 0 : parts * tokens * heads * dp;
-    return p;
-}
-
 template <int DT>
-hipError_t launch_part(const AttnArgs &a, AttnPlan pl, int rows, int waves, int wg0, int wgs, hipStream_t st)
+hipError_t launch_part(const AttnArgs &a, AttnPlan pl, const AttnLaunch &l, hipStream_t st)
 {
+    const int rows = l.rows, waves = l.waves, wgs = l.wgs;
     if (wgs == 0) return hipSuccess;
-    pl.wg0 = wg0;
+    pl.wg0 = l.first;
     const int dc = a.c.Dp <= 64 ? 1 : a.c.Dp <= 128 ? 2 : 4;
     const dim3 grid(static_cast<unsigned>(wgs)), block(64 * waves);
     const size_t lds = (waves * 16 * (64 * dc + 2) + 16) * sizeof(float);
@@ -1421,14 +1321,12 @@ hipError_t launch_part(const AttnArgs &a, AttnPlan pl, int rows, int waves, int 
 template <int DT>
 hipError_t launch_attn(const AttnArgs &a, const AttnPlan &pl, hipStream_t st)
 {
-    hipError_t e = hipSuccess;
-    if (pl.together) {
-        e = launch_part<DT>(a, pl, pl.rows_own, pl.waves_own, 0, pl.wgs_prefix + pl.wgs_own, st);
-    } else {
-        e = launch_part<DT>(a, pl, pl.rows_prefix, pl.waves_prefix, 0, pl.wgs_prefix, st);
-        if (e == hipSuccess) e = launch_part<DT>(a, pl, pl.rows_own, pl.waves_own, pl.wgs_prefix, pl.wgs_own, st);
+    AttnLaunch l[2];
+    const int n = attn_launches(pl, l);
+    for (int x = 0; x < n; ++x) {
+        const hipError_t e = launch_part<DT>(a, pl, l[x], st);
+        if (e != hipSuccess) return e;
     }
-    if (e != hipSuccess) return e;
     if (pl.direct) return hipSuccess;
     const int64_t rows = static_cast<int64_t>(a.seqs) * a.max_q * a.heads;
     const bool wide = pl.splits_prefix + pl.splits_own > 12;
@@ -1456,7 +1354,7 @@ int64_t attn_workspace_bytes(int64_t tokens, int64_t heads, int64_t kv_heads, in
 {
     int64_t most = 0;
     for (const int dtype : {DT_F32, DT_BF16}) {
-        const AttnPlan p = attn_plan(tokens, heads, kv_heads, head_dim, seqs, max_q, max_own, prefix, dtype);
+        const AttnPlan p = attn_plan(tokens, heads, kv_heads, head_dim, seqs, max_q, max_own, prefix, dtype == DT_F32);
         const int64_t need = p.direct ? 0 : (p.ml_off + 2 * (p.splits_prefix + p.splits_own) * tokens * heads) * 4;
         most = need > most ? need : most;
     }
@@ -1466,7 +1364,7 @@ int64_t attn_workspace_bytes(int64_t tokens, int64_t heads, int64_t kv_heads, in
 hipError_t launch_attention(const AttnArgs &a, hipStream_t stream)
 {
     const AttnPlan p =
-        attn_plan(a.tokens, a.heads, a.c.heads, a.c.D, a.seqs, a.max_q, a.max_own, a.prefix, a.dtype);
+        attn_plan(a.tokens, a.heads, a.c.heads, a.c.D, a.seqs, a.max_q, a.max_own, a.prefix, a.dtype == DT_F32);
     return a.dtype == DT_F32 ? launch_attn<DT_F32>(a, p, stream) : launch_attn<DT_BF16>(a, p, stream);
 }
 

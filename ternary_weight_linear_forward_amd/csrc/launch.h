@@ -227,20 +227,6 @@ struct AttnArgs {
     float scale;
     float *ws;
 };
-// How a call is cut: the prefix's workgroups (row tiles x kv heads x splits of
-// chunk_prefix blocks of 64 keys), then the sequences'.
-struct AttnPlan {
-    int rows_prefix, rows_own;   // rows of a workgroup (16: k_attn_stream, 128, 256: k_attn_tile)
-    int waves_prefix, waves_own; // and its waves
-    int tiles_own;               // row tiles of a sequence
-    int chunk_prefix, splits_prefix, chunk_own, splits_own;
-    int wgs_prefix, wgs_own;
-    int wg0;        // first workgroup of the launch
-    bool joint;     // the sequences' workgroups go over the prefix too (none of its own)
-    bool together;  // prefix and sequences in one launch
-    bool direct;    // one part in all: the workgroups write the result
-    int64_t ml_off; // floats of o sums before the (m, l) pairs
-};
 int64_t attn_workspace_bytes(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t seqs,
                              int64_t max_q, int64_t max_own, int64_t prefix);
 hipError_t launch_attention(const AttnArgs &a, hipStream_t stream);
