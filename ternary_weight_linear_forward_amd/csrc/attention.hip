@@ -256,6 +256,7 @@ __device__ __forceinline__ bool attn_job(const AttnArgs &a, const AttnPlan &pl, 
         j.n = a.tokens;
         j.row0 = tile * tile_rows;
         j.rows = min(tile_rows, a.tokens * G - j.row0);
+        if (j.rows <= 0) return false; // (no plan has such a tile; its queries would lie past Q)
         j.nbp = nbp;
         j.own = 0;
         j.own_pages = nullptr;

@@ -91,6 +91,9 @@ inline AttnPlan attn_plan(int64_t tokens, int64_t heads, int64_t kv_heads, int64
     AttnPlan p;
     const int64_t G = heads / kv_heads, dp = div_up(head_dim, 16) * 16;
     const int64_t nbp = div_up(prefix, ATTN_BLOCK), nbo = div_up(max_own, ATTN_BLOCK);
+    // (max_q is a bound, which a captured call keeps from its largest batch: a sequence has no more
+    // query tokens than the call, so its tiles are never larger than the prefix's)
+    max_q = std::min(max_q, tokens);
     p.rows_prefix = tile_rows(tokens * G, head_dim, f32);
     p.rows_own = tile_rows(max_q * G, head_dim, f32);
     p.tiles_own = static_cast<int>(div_up(max_q * G, p.rows_own));
@@ -101,7 +104,7 @@ inline AttnPlan attn_plan(int64_t tokens, int64_t heads, int64_t kv_heads, int64
     const int64_t tp = p.joint || nbp == 0 ? 0 : div_up(tokens * G, p.rows_prefix);
     // with the same kernel for both, one launch (5 x 8 rows on 60001 keys with 333 of their own: 54 us
     // for both, 52 + 12 one after the other)
-    p.together = tp > 0 && p.rows_prefix == 16;
+    p.together = tp > 0 && p.rows_prefix == 16 && p.rows_own == 16;
     // a part's sums, written and read at a copy's rate, in eighths of a block's 2.6 us
     const int64_t part = 1 + tokens * heads * dp * 6 / 1000000;
     // workgroups with rows at most: a sequence's last tile is its own.  With both, 2 x 300 query tokens x 64
