@@ -13,8 +13,9 @@
 // Arithmetic.  int8 bytes are exact in binary16, so both products run on the
 // f16 matrix cores with fp32 accumulation, and no scale touches the operands:
 //  - a query row is multiplied by a power of two that brings its largest value
-//    into [2^13, 2^14) and rounded to binary16: bf16 queries keep their 8 bits
-//    down to 2^-24 of the row's size; fp32 queries are two binary16 terms (22
+//    into [2^13, 2^14), or up to 2^4 below (rows that share k_attn_tile's power),
+//    and rounded to binary16: bf16 queries keep their 8 bits down to 2^-24 of the
+//    row's size; fp32 queries are two binary16 terms (22
 //    bits).  Scores are then t = <q', k> * K_scale and softmax runs in base 2 on
 //    c t with c = scale log2(e) 2^-e per row.
 //  - weights p = 2^(c t - m) are multiplied by V_scale / ref * PSCALE, ref a
@@ -819,9 +820,15 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(const AttnArgs a, cons
         fetch_v(unit0);
     }
 
-    // one power of two for all rows (what smaller rows lose is 2^-39 of the tile's largest score)
+    // One power of two for all rows whose largest value is within ALIKE binades of the tile's, so that
+    // their scores take one factor, held beside the K_scales (it costs such a row what lies below 2^-34
+    // of its largest value: half of binary16's least step of 2^-24 against 2^9).  A smaller row has a
+    // power of its own, whose difference, shift, comes out of its scores; a row that is not finite takes
+    // no part in the choice.  Whatever one row holds, the others keep theirs.
+    constexpr int ALIKE = 4;
     h8 q[KSTEPS][NS];
     float c;
+    int shift = 0;
     {
         const int rr = rho < j.rows ? j.row0 + rho : j.row0;
         const int64_t off = (j.tok0 + static_cast<int64_t>(rr / G)) * a.ldq_t + (j.kvh * G + rr % G) * a.ldq_h;
@@ -829,18 +836,23 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(const AttnArgs a, cons
         load_queries<DT>(a, off, [&](int n) { return 16 * n + 8 * hf; }, v);
 #pragma unroll
         for (int k = 0; k < KSTEPS; ++k) top = fmaxf(top, max_abs8(v[k]));
-        top = wave_max_nonneg(top);
+        const float row = max_across32(top);
+        const bool sized = row > 0.0f && row < __builtin_inff();
+        top = wave_max_nonneg(sized ? row : 0.0f);
         float *tops = reinterpret_cast<float *>(smem);
         if (lane == 0) tops[wave] = top;
         __syncthreads();
 #pragma unroll
         for (int w = 0; w < NW; ++w) top = fmaxf(top, tops[w]);
         __syncthreads();
-        const int e2 = row_exponent(top);
+        const int tile_e2 = row_exponent(top), e2 = sized ? row_exponent(row) : tile_e2;
+        shift = min(tile_e2 - e2, 0);
+        shift = shift < -ALIKE ? shift : 0;
 #pragma unroll
-        for (int k = 0; k < KSTEPS; ++k) query_terms<NS>(v[k], e2, a.scale, q[k]);
-        c = row_factor(a.scale, e2);
+        for (int k = 0; k < KSTEPS; ++k) query_terms<NS>(v[k], tile_e2 - shift, a.scale, q[k]);
+        c = row_factor(a.scale, tile_e2);
     }
+    const bool shifted = __any(shift != 0);
     // own keys the lane's row sees, and the least of the wave's rows: below it nothing is masked
     const int lim = row_limit(j, G, rho);
     int lim_min = rho < j.rows ? lim : 0x7fffffff;
@@ -1006,6 +1018,12 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(const AttnArgs a, cons
         // ---- W(blk) ----
         {
             const f4 *sc = reinterpret_cast<const f4 *>(scales_at(sbuf));
+            if (shifted) {
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) s[t][r] = __builtin_ldexpf(s[t][r], shift);
+            }
             if (masked) {
 #pragma unroll
                 for (int t = 0; t < 2; ++t)

@@ -37,3 +37,33 @@ def test_max_q_above_the_tokens(heads, kvh, D, prefix, nq, max_q, dtype):
         want, bound, wl, wb = reference(st, q, nq, D ** -0.5, dtype)
         check(o, want, bound)
         assert np.all(np.abs(to_host(lse) - wl) <= wb)
+
+
+@pytest.mark.parametrize("heads,kvh,D,nq,prefix,dtype", [
+    (8, 1, 128, [1] * 28, 6500, "bf16"), (8, 1, 100, [1] * 14, 6500, "bf16"), (8, 2, 64, [1] * 38, 6500, "f32"),
+    (8, 1, 128, [40, 3], 70, "bf16"), (8, 2, 128, [2] * 3, 70, "bf16"), (4, 1, 50, [50], 0, "f32")])
+@pytest.mark.parametrize("stray", [1e38, float("inf"), float("nan")])
+def test_rows_do_not_touch_one_another(heads, kvh, D, nq, prefix, dtype, stray):
+    """Rows of one tile belong to different tokens, those of the prefix also to different sequences: queries of very
+    different sizes, and tokens of no sequence (the first and the last) that hold anything, leave every other row
+    within its own bound."""
+    tokens = sum(nq) + 2
+    print("attention stray", heads, kvh, D, tokens, prefix, dtype, stray, flush=True)
+    own = [n + 5 * b % 70 for b, n in enumerate(nq)]
+    st = Setup(kvh, D, 64, prefix, own, seed=D + tokens)
+    qt, q = queries(tokens, heads, D, 13, dtype)
+    sizes = np.array([1.0, 2.0 ** -30, 8.0, 2.0 ** -9, 2.0 ** 7, 2.0 ** -7, 2.0 ** -100])[np.arange(tokens) % 7]
+    q = q * sizes[:, None, None].astype(np.float32)  # (powers of two: exact)
+    qt = qt * torch.tensor(sizes, dtype=qt.dtype, device="cuda")[:, None, None]
+    qt[0], qt[-1] = stray, -stray
+    qt[-1, :, ::3] = 1.0
+    start = to_dev((1 + np.concatenate([[0], np.cumsum(nq)])).astype(np.int32))
+    out = torch.full((tokens, heads, D), -9.0, dtype=qt.dtype, device="cuda")
+    _, lse = bl.attention(st.cache(), qt, to_dev(st.table), to_dev(np.array(own, np.int32)), max(own),
+                          prefix_pages=to_dev(st.prefix_pages), prefix_len=prefix, q_start=start, max_q=max(nq),
+                          out=out, return_lse=True)
+    torch.cuda.synchronize()
+    want, bound, wl, wb = reference(st, q[1:-1], nq, D ** -0.5, dtype)
+    check(out[1:-1], want, bound)
+    assert np.all(np.abs(to_host(lse)[1:-1] - wl) <= wb)
+    assert bool((out[0] == -9).all()) and bool((out[-1] == -9).all())
