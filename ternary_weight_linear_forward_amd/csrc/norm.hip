@@ -73,9 +73,10 @@ __device__ __forceinline__ void fill8(float (&v)[8], float x)
     for (int e = 0; e < 8; ++e) v[e] = x;
 }
 
-// One workgroup per row, PPT pieces per thread.  'pieces' covers the output
-// row's bytes: those past K are written with 0, and so are whole rows past M
-// (tiled layout).  A thread reads an element of x and r before it writes that
+// One workgroup per row, PPT pieces per thread.  'pieces' covers the row up to a
+// multiple of 16 (tiled: the layout's padding): bytes past K are written with 0,
+// and so are a wide stride's bytes past the pieces and whole rows past M (tiled
+// layout).  A thread reads an element of x and r before it writes that
 // element of H, so H may be either.
 template <int XDT, int HDT, int PPT>
 __global__ __launch_bounds__(1024) void k_norm_rows(const NormArgs a, int pieces, int nsteps)
@@ -145,7 +146,7 @@ __global__ __launch_bounds__(1024) void k_norm_rows(const NormArgs a, int pieces
     }
     // (int8 rows with a wide stride: the rest of the padding)
     if (a.layout < 0)
-        for (int64_t k = 8 * (static_cast<int64_t>(blockDim.x) * PPT + threadIdx.x); k < a.ldq; k += 8 * blockDim.x)
+        for (int64_t k = 8 * (static_cast<int64_t>(pieces) + threadIdx.x); k < a.ldq; k += 8 * blockDim.x)
             *reinterpret_cast<uint2 *>(a.Xq + m * a.ldq + k) = make_uint2(0u, 0u);
     if (threadIdx.x == 0 && live) a.beta[m] = b;
 }
