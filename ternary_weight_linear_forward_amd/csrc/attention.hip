@@ -1218,14 +1218,15 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(const AttnArgs a, cons
 // of 64 parts at once and 64 / LPR parts' sums side by side.  Bound: HBM / L2: 11264
 // rows of 128 from 6 parts, 38 MB: 8.6 us; 320 rows from 20 parts: 5 us.
 template <int DT, int LPR, bool WIDE>
-__global__ __launch_bounds__(256) void k_attn_join(const AttnArgs a, const AttnPlan pl, int64_t rows)
+__global__ __launch_bounds__(256) void k_attn_join(const AttnArgs a, const AttnPlan pl, int64_t row0, int64_t rows)
 {
     constexpr int PER = WIDE ? 64 : LPR; // lanes a row
-    const int64_t r = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / PER;
+    const int64_t r = row0 + (blockIdx.x * (256 / PER) + threadIdx.x / PER);
     if (r >= rows) return;
     const int head = static_cast<int>(r % a.heads), lane = lane_id();
     const int64_t bi = r / a.heads;
-    const int b = static_cast<int>(bi / a.max_q), i = static_cast<int>(bi % a.max_q);
+    const int most = min(a.max_q, a.tokens); // query tokens of a sequence
+    const int b = static_cast<int>(bi / most), i = static_cast<int>(bi % most);
     int first = b * a.max_q, n = a.max_q;
     if (a.q_start) {
         first = a.q_start[b];
@@ -1312,11 +1313,9 @@ __global__ __launch_bounds__(256) void k_attn_join(const AttnArgs a, const AttnP
 namespace {
 
 template <int DT>
-hipError_t launch_part(const AttnArgs &a, AttnPlan pl, const AttnLaunch &l, hipStream_t st)
+hipError_t launch_part(const AttnArgs &a, AttnPlan pl, int rows, int waves, int64_t first, int64_t wgs, hipStream_t st)
 {
-    const int rows = l.rows, waves = l.waves, wgs = l.wgs;
-    if (wgs == 0) return hipSuccess;
-    pl.wg0 = l.first;
+    pl.wg0 = static_cast<int>(first);
     const int dc = a.c.Dp <= 64 ? 1 : a.c.Dp <= 128 ? 2 : 4;
     const dim3 grid(static_cast<unsigned>(wgs)), block(64 * waves);
     const size_t lds = (waves * 16 * (64 * dc + 2) + 16) * sizeof(float);
@@ -1343,26 +1342,31 @@ hipError_t launch_attn(const AttnArgs &a, const AttnPlan &pl, hipStream_t st)
     AttnLaunch l[2];
     const int n = attn_launches(pl, l);
     for (int x = 0; x < n; ++x) {
-        const hipError_t e = launch_part<DT>(a, pl, l[x], st);
+        const hipError_t e = attn_pieces(l[x].wgs, hipSuccess, [&](int64_t at, int64_t wgs) {
+            return launch_part<DT>(a, pl, l[x].rows, l[x].waves, l[x].first + at, wgs, st);
+        });
         if (e != hipSuccess) return e;
     }
     if (pl.direct) return hipSuccess;
-    const int64_t rows = static_cast<int64_t>(a.seqs) * a.max_q * a.heads;
+    const int64_t rows = attn_join_rows(a.tokens, a.heads, a.seqs, a.max_q);
     const bool wide = pl.splits_prefix + pl.splits_own > 12;
-    const int lpr = a.c.Dp <= 64 ? 16 : a.c.Dp <= 128 ? 32 : 64;
-    const dim3 grid(static_cast<unsigned>(div_up(rows * (wide ? 64 : lpr), 256))), block(256);
-#define BL_JOIN(LPR, WIDE) hipLaunchKernelGGL((k_attn_join<DT, LPR, WIDE>), grid, block, 0, st, a, pl, rows)
-    if (wide) {
-        if (lpr == 16) BL_JOIN(16, true);
-        else if (lpr == 32) BL_JOIN(32, true);
-        else BL_JOIN(64, true);
-    } else {
-        if (lpr == 16) BL_JOIN(16, false);
-        else if (lpr == 32) BL_JOIN(32, false);
-        else BL_JOIN(64, false);
-    }
+    const int lpr = a.c.Dp <= 64 ? 16 : a.c.Dp <= 128 ? 32 : 64, rows_wg = 256 / (wide ? 64 : lpr);
+    return attn_pieces(div_up(rows, rows_wg), hipSuccess, [&](int64_t at, int64_t wgs) {
+        const dim3 grid(static_cast<unsigned>(wgs)), block(256);
+        const int64_t row0 = at * rows_wg;
+#define BL_JOIN(LPR, WIDE) hipLaunchKernelGGL((k_attn_join<DT, LPR, WIDE>), grid, block, 0, st, a, pl, row0, rows)
+        if (wide) {
+            if (lpr == 16) BL_JOIN(16, true);
+            else if (lpr == 32) BL_JOIN(32, true);
+            else BL_JOIN(64, true);
+        } else {
+            if (lpr == 16) BL_JOIN(16, false);
+            else if (lpr == 32) BL_JOIN(32, false);
+            else BL_JOIN(64, false);
+        }
 #undef BL_JOIN
-    return hipGetLastError();
+        return hipGetLastError();
+    });
 }
 
 } // namespace

@@ -55,6 +55,8 @@ struct AttnCut {
 // that join their sums cost half a block, a part's sums on their way through memory
 // 'part', and the join itself, where there would be none (joined), four blocks.
 // waves: those of k_attn_stream, 0 for any; others: workgroups of the same launch.
+// 2^20 workgroups are a thousand rounds of the card, which no split makes shorter: no
+// more parts than that asks for, so that workgroups are numbered in 31 bits.
 inline AttnCut choose_cut(int64_t wgs, int64_t blocks, int rows, int64_t head_dim, int waves, int64_t others,
                           int64_t part, bool joined)
 {
@@ -62,12 +64,13 @@ inline AttnCut choose_cut(int64_t wgs, int64_t blocks, int rows, int64_t head_di
     if (blocks == 0) return best;
     const int dc = head_dim <= 64 ? 1 : head_dim <= 128 ? 2 : 4;
     const bool stream = rows == 16;
+    const int64_t most = std::max<int64_t>(1, std::min<int64_t>(64, (int64_t(1) << 20) / wgs));
     int64_t least = -1;
     for (int w = 1; w <= 8; w *= 2) {
         if (stream ? w > 4 || (waves && w != waves) : w != rows / 32) continue;
         const bool alone = stream ? dc == 4 : rows == 256; // one wave a SIMD, one workgroup a CU; or two
         const int64_t slots = stream ? 256 * (4 / w) * (alone ? 1 : 2) : 256 * (alone ? 1 : 2);
-        for (int64_t s = 1; s <= 64 && (s == 1 || div_up(blocks, s) >= (stream ? w : 2)); ++s) {
+        for (int64_t s = 1; s <= most && (s == 1 || div_up(blocks, s) >= (stream ? w : 2)); ++s) {
             const int64_t c = div_up(blocks, s), n = div_up(blocks, c);
             const int64_t cost =
                 8 * div_up(wgs * n + others, slots) * ((stream ? div_up(c, w) : c) + 4) +
@@ -134,18 +137,40 @@ inline AttnPlan attn_plan(int64_t tokens, int64_t heads, int64_t kv_heads, int64
 // The launches of a plan's parts, in order: workgroups first .. first + wgs - 1 in
 // tiles of 'rows' rows by 'waves' waves.  Returns how many (some may be of no workgroup).
 struct AttnLaunch {
-    int rows, waves, first, wgs;
+    int rows, waves;
+    int64_t first, wgs;
 };
 
 inline int attn_launches(const AttnPlan &p, AttnLaunch (&l)[2])
 {
     if (p.together) {
-        l[0] = {p.rows_own, p.waves_own, 0, p.wgs_prefix + p.wgs_own};
+        l[0] = {p.rows_own, p.waves_own, 0, int64_t(p.wgs_prefix) + p.wgs_own};
         return 1;
     }
     l[0] = {p.rows_prefix, p.waves_prefix, 0, p.wgs_prefix};
     l[1] = {p.rows_own, p.waves_own, p.wgs_prefix, p.wgs_own};
     return 2;
+}
+
+// Rows the join goes through: every query a sequence may have.
+inline int64_t attn_join_rows(int64_t tokens, int64_t heads, int64_t seqs, int64_t max_q)
+{
+    return seqs * std::min(max_q, tokens) * heads;
+}
+
+// A launch holds fewer than 2^32 threads, workgroups here at most 512: larger ones go
+// out in pieces of 2^22 workgroups, f(first, workgroups) each, until f gives something
+// other than 'ok'.
+constexpr int64_t kMaxWorkgroups = int64_t(1) << 22;
+
+template <class R, class F>
+R attn_pieces(int64_t wgs, R ok, const F &f)
+{
+    for (int64_t at = 0; at < wgs; at += kMaxWorkgroups) {
+        const R r = f(at, std::min(wgs - at, kMaxWorkgroups));
+        if (r != ok) return r;
+    }
+    return ok;
 }
 
 } // namespace bl

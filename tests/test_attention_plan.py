@@ -25,19 +25,34 @@ extern "C" int cut(const int64_t *x, int64_t *out)
     for (int k = 0; k < 10; ++k) out[8 + k] = v[k];
     return n;
 }
+extern "C" int64_t pieces(int64_t wgs, int64_t *out)
+{
+    int64_t n = 0;
+    bl::attn_pieces(wgs, 0, [&](int64_t first, int64_t count) { out[2 * n] = first; out[2 * n++ + 1] = count; return 0; });
+    return n;
+}
+extern "C" int64_t join_rows(int64_t tokens, int64_t heads, int64_t seqs, int64_t max_q)
+{
+    return bl::attn_join_rows(tokens, heads, seqs, max_q);
+}
 """
 NAMES = ("tiles_own", "chunk_prefix", "splits_prefix", "chunk_own", "splits_own", "wgs_prefix", "wgs_own", "joint",
          "direct", "ml_off")
 
 
 @pytest.fixture(scope="module")
-def cut(tmp_path_factory):
+def lib(tmp_path_factory):
     d = tmp_path_factory.mktemp("plan")
-    src, lib = str(d / "cut.cpp"), str(d / "cut.so")
+    src, out = str(d / "cut.cpp"), str(d / "cut.so")
     with open(src, "w") as f:
         f.write(SHIM)
-    subprocess.run(["g++", "-O1", "-std=c++17", "-Wall", "-Werror", "-shared", "-fPIC", "-I", CSRC, src, "-o", lib], check=True)
-    fn = ctypes.CDLL(lib).cut
+    subprocess.run(["g++", "-O1", "-std=c++17", "-Wall", "-Werror", "-shared", "-fPIC", "-I", CSRC, src, "-o", out], check=True)
+    return ctypes.CDLL(out)
+
+
+@pytest.fixture(scope="module")
+def cut(lib):
+    fn = lib.cut
 
     def call(*sizes):
         out = (ctypes.c_int64 * 18)()
@@ -80,7 +95,7 @@ def check(cut, tokens, heads, kvh, D, seqs, max_q, max_own, prefix, f32):
             assert (p["tiles_own"] - 1) * rows < most * G <= p["tiles_own"] * rows, what
             blocks = nbo + (nbp if p["joint"] else 0)
             assert p["splits_own"] * p["chunk_own"] >= blocks > (p["splits_own"] - 1) * p["chunk_own"], what
-    assert at == p["wgs_prefix"] + p["wgs_own"], what
+    assert at == p["wgs_prefix"] + p["wgs_own"] < 1 << 31, what
     assert (p["wgs_prefix"] > 0) == (prefix > 0 and not p["joint"]), what
     if p["direct"]:
         assert p["wgs_prefix"] == 0 and p["splits_own"] == 1, what
@@ -107,3 +122,32 @@ def test_the_bound_of_a_captured_call(cut):
         check(cut, 12, 64, 8, 128, 4, 13, own, 60001, False)
         check(cut, 96, 32, 32, 128, 4, 100, own, 4000, False)
         check(cut, 60, 32, 32, 64, 4, 100, own, 8000, True)
+
+
+def test_launches_hold_fewer_than_2_32_threads(cut, lib):
+    """At the largest sizes the header allows, and around a piece's size: the pieces are one after the other, hold
+    every workgroup once, and none has 2^32 threads."""
+    wgs = {1, (1 << 22) - 1, 1 << 22, (1 << 22) + 1, 3 << 22, (1 << 30) + 5}
+    for heads, kvh in ((256, 256), (256, 4), (4096, 4096), (17, 1), (34, 2), (1, 1)):
+        for seqs, max_q, tokens in ((1 << 20, 1, 64), (1 << 20, 1, 1 << 20), (1 << 10, 1 << 10, 1 << 20), (1, 1 << 20, 1 << 20),
+                                    (1 << 20, 1 << 20, 1), (256, 8192, 8192), (1 << 16, 1 << 20, 1 << 12)):
+            if max(seqs * max_q, tokens) * heads > 1 << 28:
+                continue
+            for D, f32 in ((16, False), (128, False), (128, True), (256, False)):
+                for prefix, own in ((0, 64), (100, 64), (1 << 30, 1 << 30), (60000, 0)):
+                    check(cut, tokens, heads, kvh, D, seqs, max_q, own, prefix, f32)
+                    launches, p = cut(tokens, heads, kvh, D, seqs, max_q, own, prefix, f32)
+                    wgs |= {x[3] for x in launches if x[3]}
+                    lib.join_rows.restype = ctypes.c_int64
+                    rows = lib.join_rows(*(ctypes.c_int64(v) for v in (tokens, heads, seqs, max_q)))
+                    assert rows == seqs * min(max_q, tokens) * heads <= 1 << 28
+                    wgs |= {up(rows, 256 // lanes) for lanes in (16, 32, 64)}
+    lib.pieces.restype = ctypes.c_int64
+    for n in wgs:
+        out = (ctypes.c_int64 * 1024)()
+        k = lib.pieces(ctypes.c_int64(n), out)
+        at = 0
+        for i in range(k):
+            assert out[2 * i] == at and 0 < out[2 * i + 1] * 512 < 1 << 32
+            at += out[2 * i + 1]
+        assert at == n

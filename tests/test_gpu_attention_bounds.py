@@ -67,3 +67,27 @@ def test_rows_do_not_touch_one_another(heads, kvh, D, nq, prefix, dtype, stray):
     check(out[1:-1], want, bound)
     assert np.all(np.abs(to_host(lse)[1:-1] - wl) <= wb)
     assert bool((out[0] == -9).all()) and bool((out[-1] == -9).all())
+
+
+def test_a_million_places_in_the_batch():
+    """2^20 sequences of 256 heads, 64 of them with a token: workgroups and join rows past 2^32 threads."""
+    print("attention 2^20 sequences", flush=True)
+    seqs, heads, kvh, D, prefix = 1 << 20, 256, 4, 16, 100
+    lens = [(7 * b) % 64 for b in range(64)]
+    st = Setup(kvh, D, 64, prefix, lens, seed=3)
+    qt, q = queries(64, heads, D, 14, "bf16")
+    where = np.sort(np.random.default_rng(5).permutation(seqs)[:64])  # the sequences that have their one token
+    where[0], where[-1] = 0, seqs - 1
+    has = np.zeros(seqs, np.int64)
+    has[where] = 1
+    start = to_dev(np.concatenate([[0], np.cumsum(has)]).astype(np.int32))
+    own = np.full(seqs, 64, np.int32)
+    own[where] = lens
+    table = np.full((seqs, 1), -1, np.int32)
+    table[where] = st.table[:, :1]
+    o, lse = bl.attention(st.cache(), qt, to_dev(table), to_dev(own), 64, prefix_pages=to_dev(st.prefix_pages),
+                          prefix_len=prefix, q_start=start, max_q=1, return_lse=True)
+    torch.cuda.synchronize()
+    want, bound, wl, wb = reference(st, q, [1] * 64, D ** -0.5, "bf16")
+    check(o, want, bound)
+    assert np.all(np.abs(to_host(lse) - wl) <= wb)
