@@ -314,7 +314,6 @@ int bitlinear_attention(const bitlinear_cache_t *cache, const void *Q, int dtype
         return BITLINEAR_ERR_INVALID_ARG;
     const int64_t need =
         bl::attn_workspace_bytes(tokens, heads, a.c.heads, a.c.D, seqs, max_q, max_own, prefix_len);
-    if (need < 0) return BITLINEAR_ERR_UNSUPPORTED;
     if (need > 0 && (!ws || ws_bytes < need)) return BITLINEAR_ERR_WORKSPACE;
     if (need > 0 && !aligned16(ws)) return BITLINEAR_ERR_INVALID_ARG;
     const Span so = rows_span(O, tokens, heads, ldo_token, ldo_head, a.c.D, es),
