@@ -645,20 +645,27 @@ def _record(stream, *tensors) -> None:
             t.record_stream(stream)
 
 
-def _ld(t) -> int:
-    """Row stride of a 2-d tensor (the row length where there is one row)."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
-
-
 def dequantize_act(Xq, beta, K: int, dtype=None, out=None, stream=None):
-    """The values of int8 rows Xq [M x >=K] with beta [M]: q * (beta / 127), fp32 or bf16 [M x K]."""
-    M, ldq = Xq.shape[0], _ld(Xq)
+    """The values of int8 rows Xq [M x >=K] with beta fp32 [M]: q * (beta / 127), [M x K] of 'dtype' (fp32 or bf16;
+    fp32 by default) or written to 'out'."""
+    name = "dequantize_act"
+    if Xq.dim() != 2 or Xq.dtype != torch.int8 or beta.dtype != torch.float32:
+        raise BitlinearError(ERR_INVALID_ARG, name)
+    (M, width), (ldq, step) = Xq.shape, Xq.stride()
+    if width < K or (step != 1 and K > 1) or beta.shape != (M,) or (M > 1 and beta.stride(0) != 1):
+        raise BitlinearError(ERR_INVALID_ARG, name)
+    if M == 1:
+        ldq = max(ldq, width)
     if out is None:
-        out, ldv = beta.new_empty((M, K), dtype=dtype or torch.float32), K
+        if dtype is None:
+            dtype = torch.float32
+        elif dtype not in _FLOATS:
+            raise BitlinearError(ERR_INVALID_ARG, name)
+        out, ldv = beta.new_empty((M, K), dtype=dtype), K
     else:
-        ldv = _ld(out)
-    _check(_lib.bitlinear_dequantize_act(Xq.data_ptr(), ldq, beta.data_ptr(), M, K, out.data_ptr(), _dtype_code(out),
-                                         ldv, _stream(stream)), "bitlinear_dequantize_act")
+        ldv, dtype = _row_stride(out, name, M, K), out.dtype
+    _check(_lib.bitlinear_dequantize_act(Xq.data_ptr(), ldq, beta.data_ptr(), M, K, out.data_ptr(), _FLOATS[dtype], ldv,
+                                         _stream(stream)), "bitlinear_dequantize_act")
     if stream is not None:
         _record(stream, out)
     return out
