@@ -604,6 +604,8 @@ def norm_quantize(X, w=None, eps: float = 1e-5, residual=None, H=None, keep_h: b
     residual's dtype (X's without one; written to 'H' if given, which may be
     the residual; None with keep_h=False); Xq int8 [M x ldq], ldq = K rounded
     up to 16, or with a weight layout the 1-d tiled activations forward takes."""
+    if stream is not None:
+        return _on(stream, norm_quantize, X, w, eps, residual, H, keep_h, layout)
     name = "norm_quantize"
     M, K = X.shape
     ldx = _row_stride(X, name, M, K)
@@ -631,23 +633,31 @@ def norm_quantize(X, w=None, eps: float = 1e-5, residual=None, H=None, keep_h: b
     beta = X.new_empty(M, dtype=torch.float32)
     _check(_lib.bitlinear_norm_quantize(X.data_ptr(), _FLOATS[X.dtype], M, K, ldx, rp, ldr, wp, eps, hp,
                                         _FLOATS[ref.dtype], ldh, Xq.data_ptr(), qdt, ldq, lay, beta.data_ptr(),
-                                        _stream(stream)), "bitlinear_norm_quantize")
-    if stream is not None:
-        _record(stream, H, Xq, beta)
+                                        _stream()), "bitlinear_norm_quantize")
     return H, Xq, beta
 
 
-def _record(stream, *tensors) -> None:
-    """Tensors allocated here and used on another stream than the current one
-    must not be handed out again before that stream is done with them."""
-    for t in tensors:
-        if t is not None:
+def _on(stream, call, *args):
+    """call(*args) with 'stream' as the current one.  What it allocates belongs to that stream: memory that the
+    caller's stream freed, and may still be writing, is not taken for it.  The caller's tensors are not handed out
+    again before 'stream' is done with them, nor the results before the caller's stream is."""
+    caller = torch.cuda.current_stream()
+    with torch.cuda.stream(stream):
+        out = call(*args)
+    for t in args:
+        if isinstance(t, torch.Tensor):
             t.record_stream(stream)
+    for t in out if isinstance(out, tuple) else (out,):
+        if t is not None:
+            t.record_stream(caller)
+    return out
 
 
 def dequantize_act(Xq, beta, K: int, dtype=None, out=None, stream=None):
     """The values of int8 rows Xq [M x >=K] with beta fp32 [M]: q * (beta / 127), [M x K] of 'dtype' (fp32 or bf16;
     fp32 by default) or written to 'out'."""
+    if stream is not None:
+        return _on(stream, dequantize_act, Xq, beta, K, dtype, out)
     name = "dequantize_act"
     if Xq.dim() != 2 or Xq.dtype != torch.int8 or beta.dtype != torch.float32:
         raise BitlinearError(ERR_INVALID_ARG, name)
@@ -665,9 +675,7 @@ def dequantize_act(Xq, beta, K: int, dtype=None, out=None, stream=None):
     else:
         ldv, dtype = _row_stride(out, name, M, K), out.dtype
     _check(_lib.bitlinear_dequantize_act(Xq.data_ptr(), ldq, beta.data_ptr(), M, K, out.data_ptr(), _FLOATS[dtype], ldv,
-                                         _stream(stream)), "bitlinear_dequantize_act")
-    if stream is not None:
-        _record(stream, out)
+                                         _stream()), "bitlinear_dequantize_act")
     return out
 
 
@@ -675,6 +683,8 @@ def norm_backward(dY, H, w=None, eps: float = 1e-5, dH=None, dX=None, want_dw: b
     """Gradient of the norm (bitlinear_norm_backward): dY fp32 [M x K], H the
     norm's kept sum, dH the gradient arriving through the residual stream (H's
     dtype, or None).  Returns (dX in H's dtype, dW fp32 [K] or None)."""
+    if stream is not None:
+        return _on(stream, norm_backward, dY, H, w, eps, dH, dX, want_dw, ws)
     name = "norm_backward"
     M, K = H.shape
     dtype = H.dtype
@@ -694,9 +704,7 @@ def norm_backward(dY, H, w=None, eps: float = 1e-5, dH=None, dX=None, want_dw: b
         ws = torch.empty(nws, dtype=torch.uint8, device=H.device)
     _check(_lib.bitlinear_norm_backward(
         dY.data_ptr(), lddy, H.data_ptr(), _FLOATS[dtype], ldh, wp, eps, _ptr(dH), lddh, M, K, dX.data_ptr(), lddx,
-        _ptr(dW), _ptr(ws) if nws > 0 else None, nws, _stream(stream)), "bitlinear_norm_backward")
-    if stream is not None:
-        _record(stream, dX, dW, ws)
+        _ptr(dW), _ptr(ws) if nws > 0 else None, nws, _stream()), "bitlinear_norm_backward")
     return dX, dW
 
 
@@ -745,17 +753,21 @@ def _kv_strides(cache, t, tokens, where):
 def cache_write(cache: KVCache, K, V, slots, stream=None) -> None:
     """Quantise K, V [tokens x heads x head_dim] (fp32/bf16) into the cache's
     slots (int64 [tokens]; a slot outside the cache is skipped)."""
+    if stream is not None:
+        return _on(stream, cache_write, cache, K, V, slots)
     n = slots.numel()
     lkt, lkh = _kv_strides(cache, K, n, "cache_write")
     lvt, lvh = _kv_strides(cache, V, n, "cache_write")
     if K.dtype != V.dtype or slots.dtype != torch.int64 or not slots.is_contiguous():
         raise BitlinearError(ERR_INVALID_ARG, "cache_write")
     _check(_lib.bitlinear_cache_write(cache.desc, K.data_ptr(), lkt, lkh, V.data_ptr(), lvt, lvh, _dtype_code(K), n,
-                                      slots.data_ptr(), _stream(stream)), "bitlinear_cache_write")
+                                      slots.data_ptr(), _stream()), "bitlinear_cache_write")
 
 
 def cache_read(cache: KVCache, slots, dtype=None, stream=None):
     """(K, V) [tokens x heads x head_dim] of the cache's slots (zeros for a slot outside it)."""
+    if stream is not None:
+        return _on(stream, cache_read, cache, slots, dtype)
     n = slots.numel()
     if slots.dtype != torch.int64 or not slots.is_contiguous():
         raise BitlinearError(ERR_INVALID_ARG, "cache_read")
@@ -763,9 +775,7 @@ def cache_read(cache: KVCache, slots, dtype=None, stream=None):
     K = torch.empty((n, H, D), dtype=dtype or torch.bfloat16, device=slots.device)
     V = torch.empty_like(K)
     _check(_lib.bitlinear_cache_read(cache.desc, slots.data_ptr(), n, K.data_ptr(), H * D, D, V.data_ptr(), H * D, D,
-                                     _dtype_code(K), _stream(stream)), "bitlinear_cache_read")
-    if stream is not None:
-        _record(stream, K, V)
+                                     _dtype_code(K), _stream()), "bitlinear_cache_read")
     return K, V
 
 
@@ -776,6 +786,9 @@ def attention(cache: KVCache, Q, own_pages, own_len, max_own: int, prefix_pages=
     own_len int32 [seqs] (at most max_own); prefix_pages int32; q_start int32
     [seqs + 1] or None (max_q tokens each); scale 1 / sqrt(head_dim) by
     default.  Returns O (Q's shape and dtype), or (O, lse fp32 [tokens x heads])."""
+    if stream is not None:
+        return _on(stream, attention, cache, Q, own_pages, own_len, max_own, prefix_pages, prefix_len, q_start, max_q, scale,
+                   out, return_lse, ws)
     name = "attention"
     tokens, heads, D = Q.shape
     seqs = own_len.numel()
@@ -810,7 +823,5 @@ def attention(cache: KVCache, Q, own_pages, own_len, max_own: int, prefix_pages=
         cache.desc, Q.data_ptr(), _dtype_code(Q), tokens, heads, lqt, lqh, seqs, _ptr(q_start), max_q,
         own_pages.data_ptr(), ldp if rows > 1 else max(ldp, cols), own_len.data_ptr(), max_own, _ptr(prefix_pages),
         prefix_len, D ** -0.5 if scale is None else scale, out.data_ptr(), lot, loh, _ptr(lse),
-        _ptr(ws) if nws > 0 else None, nws, _stream(stream)), "bitlinear_attention")
-    if stream is not None:
-        _record(stream, out, lse, ws)
+        _ptr(ws) if nws > 0 else None, nws, _stream()), "bitlinear_attention")
     return (out, lse) if return_lse else out
