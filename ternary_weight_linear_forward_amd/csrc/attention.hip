@@ -517,16 +517,17 @@ __global__ __launch_bounds__(256, DC == 4 ? 1 : 2) void k_attn_stream(const Attn
 
     f4 o[DTILES];
     // m: the row's reference in base 2 (0 until it is set), have: its largest weight so far
-    // (what this lane saw of it), ref: the V_scales' power of two
+    // (what this lane saw of it), ref: the power of two of the V_scales that the row sees (a row sees
+    // what the rows before it see: where the first one's is set, all are)
     float m = 0.0f, l = 0.0f, have = 0.0f, ref = 0.0f, vscale = 0.0f;
     bool set = false;
 #pragma unroll
     for (int d = 0; d < DTILES; ++d) o[d] = f4{0.0f, 0.0f, 0.0f, 0.0f};
     for (; blk < j.blk1; blk += waves) {
-        // this block's list: its first key, the keys there are, those a row sees
+        // this block's list: its first key and those the lane's row sees
         const bool pre = blk < j.nbp;
         const int k0 = (pre ? blk : blk - j.nbp) * CACHE_BLOCK;
-        const int all = there ? (pre ? j.prefix : j.own) : 0, mine = there ? (pre ? j.prefix : lim) : 0;
+        const int mine = there ? (pre ? j.prefix : lim) : 0;
         const bool masked = !there || k0 + CACHE_BLOCK > (pre ? j.prefix : lim_min);
         const bool next = blk + waves < j.blk1;
         if (next) {
@@ -556,7 +557,7 @@ __global__ __launch_bounds__(256, DC == 4 ? 1 : 2) void k_attn_stream(const Attn
                 for (int e = 0; e < 4; ++e) {
                     const int key = k0 + 16 * t + 4 * g + e;
                     s[t][e] = key < mine ? s[t][e] : neg_inf();
-                    vs[t][e] = key < all ? vs[t][e] : 0.0f;
+                    vs[t][e] = key < mine ? vs[t][e] : 0.0f; // (a hidden one may be anything)
                 }
         }
         // the next block's keys, while this block's weights are formed
@@ -884,15 +885,17 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(const AttnArgs a, cons
         grow = 1.0f;
         ksr = lane < seen ? ksr : 0.0f;
         vsr = lane < seen ? vsr : 0.0f;
+        // A V_scale that is not finite leaves the reference as it is and counts as the largest number: its
+        // key's weight overflows where a row sees it and is 0 where it is hidden.
         if (__any(vsr > ref)) {
-            const float ref2 = pow2_above(wave_max_nonneg(vsr));
+            const float ref2 = fmaxf(pow2_above(wave_max_nonneg(vsr < __builtin_inff() ? vsr : 0.0f)), ref);
             grow = ref / ref2;
             ref = ref2;
             vscale = WR::PSCALE / ref;
         }
         if (wave == 0) {
             to[lane] = fmaxf(ksr * c, 1.17549435e-38f); // (a masked score is -inf: never times 0)
-            to[64 + lane] = vsr * vscale;
+            to[64 + lane] = fminf(vsr * vscale, 3.402823466e38f);
         }
     };
     constexpr int STAGE_STEPS = 4 * UNITS + 1;

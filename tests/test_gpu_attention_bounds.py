@@ -91,3 +91,26 @@ def test_a_million_places_in_the_batch():
     want, bound, wl, wb = reference(st, q, [1] * 64, D ** -0.5, "bf16")
     check(o, want, bound)
     assert np.all(np.abs(to_host(lse) - wl) <= wb)
+
+
+@pytest.mark.parametrize("heads,kvh,D,prefix,own,nq,at,dtype", [
+    (8, 1, 128, 70, 300, 90, 260, "bf16"), (8, 1, 128, 0, 64, 64, 33, "bf16"), (2, 2, 128, 200, 70, 40, 40, "f32"),
+    (8, 2, 64, 10, 130, 100, 127, "f32"), (4, 4, 100, 0, 90, 20, 75, "bf16"), (8, 1, 256, 30, 50, 50, 20, "bf16")])
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+def test_hidden_keys_may_hold_anything(heads, kvh, D, prefix, own, nq, at, dtype, bad):
+    """A prompt's token whose key and value are not finite: the queries before it, which do not see it, are as if it
+    were not there."""
+    print("attention hidden", heads, kvh, D, prefix, own, nq, at, dtype, bad, flush=True)
+    st = Setup(kvh, D, 64, prefix, [own], seed=D + at)
+    qt, q = queries(nq, heads, D, 15, dtype)
+    page = st.lists[1][at // 64]
+    cache = st.cache()
+    cache.k_scale[page, :, at % 64] = bad
+    cache.v_scale[page, :, at % 64] = bad
+    o, lse = bl.attention(cache, qt, to_dev(st.table), to_dev(np.array([own], np.int32)), own,
+                          prefix_pages=to_dev(st.prefix_pages), prefix_len=prefix, max_q=nq, return_lse=True)
+    torch.cuda.synchronize()
+    want, bound, wl, wb = reference(st, q, [nq], D ** -0.5, dtype)
+    free = at - (own - nq)  # queries 0 .. free - 1 see keys 0 .. own - nq + free - 1 = at - 1 at most
+    check(o[:free], want[:free], bound[:free])
+    assert np.all(np.abs(to_host(lse)[:free] - wl[:free]) <= wb[:free])
