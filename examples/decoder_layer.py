@@ -45,7 +45,7 @@ class AttentionBlock:
     def __init__(self, wq, wk, wv, wo, norm, heads, kv_heads, seqs, max_own, max_prefix, page_tokens=64):
         self.q, self.k, self.v, self.o = (Linear(w) for w in (wq, wk, wv, wo))
         self.norm, self.heads, self.kv_heads, self.page = norm, heads, kv_heads, page_tokens
-        self.D, self.max_own = wq.shape[0] // heads, max_own
+        self.D, self.max_own, self.max_prefix = wq.shape[0] // heads, max_own, max_prefix
         need = lambda n: (n + page_tokens - 1) // page_tokens  # noqa: E731
         dev = norm.device
         self.cache = bl.KVCache.empty(need(max_prefix) + seqs * need(max_own), kv_heads, self.D, page_tokens, dev)
@@ -53,6 +53,7 @@ class AttentionBlock:
         self.own_pages = (need(max_prefix) + torch.arange(seqs * need(max_own), dtype=torch.int32, device=dev)
                           ).reshape(seqs, need(max_own))
         self.own_len = torch.zeros(seqs, dtype=torch.int32, device=dev)
+        self.held = [0] * seqs  # own_len as the host knows it
         self.prefix_len = 0
 
     def _slots(self, pages, positions):
@@ -73,6 +74,8 @@ class AttentionBlock:
     def load_prefix(self, hidden, residual):
         """The shared beginning, once: its tokens see one another and go to the prefix's pages."""
         n = hidden.shape[0]
+        if n > self.max_prefix:
+            raise ValueError(f"a prefix of {n} tokens in a block for {self.max_prefix}")
         at = torch.arange(n, device=hidden.device)
         pages = self.prefix_pages[None]
         out = self._attend(hidden, residual, self._slots(pages.expand(n, -1), at), pages,
@@ -83,6 +86,11 @@ class AttentionBlock:
     def step(self, hidden, residual, counts):
         """New tokens of every sequence, 'counts' of them each (hidden and residual hold them one sequence after
         the other): (the block's output, the sum that its norm kept) for the rest of the layer."""
+        held = [n + c for n, c in zip(self.held, counts)]
+        if len(counts) != len(self.held) or min(counts) < 0 or sum(counts) != hidden.shape[0] or max(held) > self.max_own:
+            raise ValueError(f"{hidden.shape[0]} new tokens, counts {counts}: {len(self.held)} sequences hold "
+                             f"{self.held} of {self.max_own}")
+        self.held = held
         dev = hidden.device
         count = torch.tensor(counts, dtype=torch.int32, device=dev)
         start = torch.zeros(len(counts) + 1, dtype=torch.int32, device=dev)
