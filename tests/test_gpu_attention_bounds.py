@@ -114,3 +114,32 @@ def test_hidden_keys_may_hold_anything(heads, kvh, D, prefix, own, nq, at, dtype
     free = at - (own - nq)  # queries 0 .. free - 1 see keys 0 .. own - nq + free - 1 = at - 1 at most
     check(o[:free], want[:free], bound[:free])
     assert np.all(np.abs(to_host(lse)[:free] - wl[:free]) <= wb[:free])
+
+
+@pytest.mark.parametrize("heads,kvh,D,nq,dtype", [(4, 2, 64, 1, "f32"), (8, 1, 128, 1, "bf16"), (8, 1, 128, 40, "bf16")])
+def test_lengths_are_cut_to_their_bound(heads, kvh, D, nq, dtype):
+    """own_len past max_own counts as max_own, also inside keys that are there, and below 0 as 0."""
+    print("attention cut", heads, kvh, D, nq, dtype, flush=True)
+    st = Setup(kvh, D, 64, 40, [300, 90, 300], seed=D + nq)
+    qt, q = queries(3 * nq, heads, D, 16, dtype)
+    o = bl.attention(st.cache(), qt, to_dev(st.table), to_dev(np.array([1 << 30, -(1 << 31), 151], np.int32)), 150,
+                     prefix_pages=to_dev(st.prefix_pages), prefix_len=40, max_q=nq)
+    torch.cuda.synchronize()
+    st.own = [150, 0, 150]
+    want, bound, _, _ = reference(st, q, [nq] * 3, D ** -0.5, dtype)
+    check(o, want, bound)
+
+
+@pytest.mark.parametrize("heads,kvh,D,n,prefix,dtype", [(2, 1, 128, 2048, 0, "bf16"), (2, 2, 64, 1100, 0, "f32"),
+                                                        (2, 1, 128, 900, 300, "f32"), (1, 1, 256, 800, 0, "bf16")])
+def test_a_prompt_into_an_empty_cache(heads, kvh, D, n, prefix, dtype):
+    """Every token of a sequence is a query: the first sees one key of its own, the last all of them."""
+    print("attention causal", heads, kvh, D, n, prefix, dtype, flush=True)
+    st = Setup(kvh, D, 64, prefix, [n], seed=D + n)
+    qt, q = queries(n, heads, D, 17, dtype)
+    o, lse = bl.attention(st.cache(), qt, to_dev(st.table), to_dev(np.array([n], np.int32)), n,
+                          prefix_pages=to_dev(st.prefix_pages), prefix_len=prefix, max_q=n, return_lse=True)
+    torch.cuda.synchronize()
+    want, bound, wl, wb = reference(st, q, [n], D ** -0.5, dtype)
+    check(o, want, bound)
+    assert np.all(np.abs(to_host(lse) - wl) <= wb)
