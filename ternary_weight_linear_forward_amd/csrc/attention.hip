@@ -27,6 +27,9 @@
 //    2^-21 of the reference's): blocks form no maximum unless one of that happens.
 //    Weights that are too small even then are multiplied in further rounds, brought
 //    up by STEP each, into sums of their own.  l sums the unrounded p.
+//    This form costs where scores spread: at a standard deviation of 1.6, 3 and 5 nats
+//    11264 rows on 8000 keys of 8 heads of 128 take 84, 324 and 418 us (k_attn_tile,
+//    bf16), 5 x 8 rows on 60001 keys 54, 98 and 114 us (k_attn_stream).
 #include "attn_plan.h"
 #include "cache_core.h"
 #include "common.h"
@@ -434,8 +437,8 @@ __device__ __forceinline__ float max_abs8(const float (&v)[8])
 // in LDS.
 // Bound: HBM (the bytes of the cache) for 16 rows, no LDS and no barrier in the loop:
 // 2 x 8 rows on 60001 keys of 8 heads of 128, 127 MB: 26 us, 4.9 TB/s.  With more row
-// tiles the conversion of each (5 x 8 rows: 54 us, 376 MB through L2); with 176
-// sequences' own keys of up to 512, 1408 jobs of unequal length, the longest one (32
+// tiles the conversion of each (5 x 8 rows: 53 us, 376 MB through L2); with 176
+// sequences' own keys of up to 512, 1408 jobs of unequal length, the longest one (31
 // us for 107 MB: a wave alone takes 3 us a block).  More rows a wave (two and three
 // tiles on one conversion) need registers past 256 and came to the same.
 // ---------------------------------------------------------------------------
@@ -759,7 +762,8 @@ __global__ __launch_bounds__(256, DC == 4 ? 1 : 2) void k_attn_stream(const Attn
 // of the CU fills in.  Operands are read from LDS AHEAD of their use (4 to 8 measure
 // alike); the bytes converted next are in flight in registers for a whole block.
 // Bound: the phases' instruction streams.  11264 rows on 8000 keys of 8 heads of 128
-// (46 Gflop): 82 us, 560 Tflop/s; a block takes 5000 cycles of its CU where its
+// (46 Gflop): 78 us sustained, 590 Tflop/s (82 in the first launches after an idle
+// time, as the figures above); a block takes 5000 cycles of its CU where its
 // matrix instructions need 2048 and its vector instructions 2500.  One stream that
 // forms the next scores beside the weights, without phases, came to the same (91 us).
 // ---------------------------------------------------------------------------
@@ -1219,7 +1223,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(const AttnArgs a, cons
 // few parts (WIDE false) a group of LPR lanes takes a row and goes through its
 // parts four at a time; with many, a wave takes a row, its lanes reading the (m, l)
 // of 64 parts at once and 64 / LPR parts' sums side by side.  Bound: HBM / L2: 11264
-// rows of 128 from 6 parts, 38 MB: 8.6 us; 320 rows from 20 parts: 5 us.
+// rows of 128 from 6 parts, 38 MB: 8.5 us; 320 rows from 20 parts: 5 us.
 template <int DT, int LPR, bool WIDE>
 __global__ __launch_bounds__(256) void k_attn_join(const AttnArgs a, const AttnPlan pl, int64_t row0, int64_t rows)
 {

@@ -26,6 +26,9 @@ struct AttnPlan {
 
 inline int64_t div_up(int64_t x, int64_t y) { return (x + y - 1) / y; }
 
+// (Times in this file are of kernels in their first launches after an idle time, both
+// sides alike; sustained ones are up to an eighth lower.)
+
 // Rows a workgroup takes: 16 with k_attn_stream, 128 or 256 (four or eight waves)
 // with k_attn_tile.  Row tiles that read the cache again from L2 cost less than a
 // mostly empty tile of 128: bf16, 8 kv heads of 128, keys x rows, us of k_attn_stream

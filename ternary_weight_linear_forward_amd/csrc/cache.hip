@@ -9,9 +9,10 @@
 // v_perm_b32) and move as 8 words; the four T of a g are 16 neighbouring bytes.
 // A quad whose slots are not four consecutive, 4-aligned ones moves by bytes.
 // Bound: HBM for prompts, latency for a decode step's few tokens.
-// Measured: 16000 tokens x 8 heads x 128 bf16, 98 MB a direction: write 25 us (3.9
-// TB/s), read 20 us (4.8 TB/s); 1999 x 32 x 100 fp32, 64 MB: 15 and 18 us; 16 x 8 x
-// 128: 5.7 and 4.6 us.  Tokens one by one, without tiles, took 3.6 times as long.
+// Measured: 16000 tokens x 8 heads x 128 bf16, 98 MB a direction: write 26 us (3.8
+// TB/s), read 21 us (4.7 TB/s); 1999 x 32 x 100 fp32, 64 MB: 15 and 17 us; 16 x 8 x
+// 128: 5.6 and 4.7 us; 2000 x 8 x 128 from slot 0: 6.2 and 5.8 us, from slot 333, where
+// no quad is a run, 10.4 and 8.3 us.  Tokens one by one, without tiles, took 3.6 times as long.
 #include "cache_core.h"
 #include "common.h"
 #include "launch.h"

@@ -12,8 +12,9 @@
 // the sum to binary32's precision, and no h overflows it.
 // Bound: HBM for many rows; for few, the chain load - sum - maximum - store.
 // Measured (a copy of 1 GiB moves 4.78 TB/s, read and written): 8192 x 8192 bf16 with
-// residual and kept sum, 470 MB: 103 us, 4.6 TB/s; 176 x 8640 fp32: 7.0 us; 1 x 3200:
-// 3.8 us.  The same passes as separate reads of the row took 3.6 times as long.
+// residual and kept sum, 470 MB: 102 us, 4.6 TB/s (tiled rows: 128, 16-byte pieces 1 KB
+// apart); 176 x 8640 fp32: 7.1 us, a workgroup a row on 176 of 256 CUs; 1 x 3200: 3.9 us.
+// The same passes as separate reads of the row took 3.6 times as long.
 #include "common.h"
 #include "launch.h"
 #include "rows.h"
@@ -273,7 +274,8 @@ hipError_t launch_dequantize_act(const int8_t *Xq, int64_t ldq, const float *bet
 // A workgroup takes rows p, p + parts, ... and keeps its share of dW, a row of K
 // sums, in registers; k_norm_bwd_sum adds the workgroups' rows in a fixed order, so
 // that no atomic's order reaches dW.  Bound: HBM.  2048 x 8640 bf16 with dH, 177 MB:
-// 39 us, 4.6 TB/s, and 4.7 us for the sum; 100 x 3200 fp32: 5.1 and 3.3 us.
+// 38 us, 4.6 TB/s, and 4.8 us for the sum; 100 x 3200 fp32: 5.2 and 3.2 us; rows past
+// the registers (k_norm_bwd_loop), 2048 x 28672 bf16, 587 MB: 218 and 6.5 us.
 int64_t norm_bwd_parts(int64_t M, int64_t K)
 {
     const int64_t parts = K <= 4096 ? 512 : 256; // one or two for each CU
