@@ -60,16 +60,27 @@ struct WeightRange<2> { // the second term of 2^-3 still has a full 2^-24 of its
     static constexpr float PSCALE = 0x1p14f, LEAST = 0x1p-3f, STEP = 0x1p18f;
 };
 
-// Weights to NS binary16 terms.
+// A weight to NS binary16 terms.  With two the weight is a binary32 number before it
+// is split: the compiler may otherwise form a product's first term twice, once from
+// the product rounded to binary32 and once (v_fma_mixlo_f16) from the exact one, which
+// differ by a step of binary16 where the first rounding meets a middle, and the second
+// term would be that of the other.
+template <int NS>
+__device__ __forceinline__ void split_weight(float w, h8 (&p)[NS], int e)
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+    if constexpr (NS == 2) asm("" : "+v"(w));
+#endif
+    const _Float16 hi = static_cast<_Float16>(w);
+    p[0][e] = hi;
+    if constexpr (NS == 2) p[1][e] = static_cast<_Float16>(w - static_cast<float>(hi));
+}
+
 template <int NS>
 __device__ __forceinline__ void split_weights(const float (&w)[8], h8 (&p)[NS])
 {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const _Float16 hi = static_cast<_Float16>(w[e]);
-        p[0][e] = hi;
-        if constexpr (NS == 2) p[1][e] = static_cast<_Float16>(w[e] - static_cast<float>(hi));
-    }
+    for (int e = 0; e < 8; ++e) split_weight<NS>(w[e], p, e);
 }
 
 // A weight's share of a round: brought up by 'up' = STEP, STEP^2, .. into [LEAST,
@@ -1062,11 +1073,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(const AttnArgs a, cons
                     w[x] = y * vq[quad % 3][(e + x) % 4];
                 }
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const _Float16 hi = static_cast<_Float16>(w[x]);
-                    p[t][0][e + x] = hi;
-                    if constexpr (NS == 2) p[t][1][e + x] = static_cast<_Float16>(w[x] - static_cast<float>(hi));
-                }
+                for (int x = 0; x < 2; ++x) split_weight<NS>(w[x], p[t], e + x);
 #pragma unroll
                 for (int x = 0; x < 2; ++x) pin(sums[x]);
                 if (n % 2 == 1) __builtin_amdgcn_sched_barrier(0);

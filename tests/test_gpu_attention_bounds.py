@@ -9,7 +9,7 @@ torch = pytest.importorskip("torch")
 from ternary_weight_linear_forward_amd import bitlinear as bl  # noqa: E402
 
 from gpu_helpers import to_dev, to_host  # noqa: E402
-from test_gpu_attention import Setup, check, queries, reference  # noqa: E402
+from test_gpu_attention import U, Setup, check, queries, reference  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -143,3 +143,32 @@ def test_a_prompt_into_an_empty_cache(heads, kvh, D, n, prefix, dtype):
     want, bound, wl, wb = reference(st, q, [n], D ** -0.5, dtype)
     check(o, want, bound)
     assert np.all(np.abs(to_host(lse) - wl) <= wb)
+
+
+@pytest.mark.parametrize("heads,kvh,D,tokens", [(64, 8, 160, 400), (64, 8, 64, 1500), (64, 8, 64, 12), (32, 32, 100, 700)])
+def test_every_weight_of_fp32_queries_has_22_bits(heads, kvh, D, tokens):
+    """Rows of seven keys with values (and 63 of value 0 before them), so that a single weight off by a step of its
+    first term shows: among hundreds of thousands of weights some lie at the middle between two binary16 numbers,
+    where both terms have to agree on the first."""
+    print("attention terms", heads, kvh, D, tokens, flush=True)
+    n, G = 70, heads // kvh
+    worst = 0.0
+    for seed in range(4):
+        st = Setup(kvh, D, 64, n, [0], seed=100 + seed)
+        st.vs[st.lists[0][0], :, 1:] = 0.0
+        qt, q = queries(tokens, heads, D, 20 + seed, "f32")
+        o = bl.attention(st.cache(), qt, to_dev(st.table), to_dev(np.array([0], np.int32)), 0,
+                         prefix_pages=to_dev(st.prefix_pages), prefix_len=n, max_q=tokens)
+        torch.cuda.synchronize()
+        k, v = st.rows(st.lists[0], n)
+        qq = q.astype(np.float64).reshape(tokens, kvh, G, D)
+        s = D ** -0.5 * np.einsum("thgd,nhd->thgn", qq, k)
+        A = D ** -0.5 * np.einsum("thgd,nhd->thgn", np.abs(qq), np.abs(k)).max(-1)
+        p = np.exp(s - s.max(-1, keepdims=True))
+        p /= p.sum(-1, keepdims=True)
+        want, size = np.einsum("thgn,nhd->thgd", p, v), np.einsum("thgn,nhd->thgd", p, np.abs(v))
+        e = (D + 16) * U * A + 2.0 ** -21 * A + 8 * U * (A + np.abs(s).max(-1))
+        bound = (2 * e + (n + 16) * U + 2.0 ** -21)[..., None] * size + U * np.abs(want)
+        err = np.abs(to_host(o).astype(np.float64).reshape(want.shape) - want)
+        worst = max(worst, (err / bound).max())
+    assert worst <= 1.0
