@@ -684,6 +684,108 @@ int bitlinear_attention(const bitlinear_cache_t *cache, const void *Q, int dtype
                         const int32_t *prefix_pages, int64_t prefix_len, float scale, void *O, int64_t ldo_token,
                         int64_t ldo_head, float *lse, void *ws, int64_t ws_bytes, void *stream);
 
+/*
+ * Attention as bitlinear_attention's with a sliding window: of the keys that a query
+ * sees there (the prefix's at positions 0 .. prefix_len - 1, the sequence's own
+ * after them), it keeps the last 'window', its own among them, and the first 'sinks'
+ * positions of the sequence.
+ *   window  in [1, 2^31]; prefix_len + max_own or more keeps every key, and the call
+ *           is then bitlinear_attention.
+ *   sinks   in [0, 2^30].
+ * Pages (of either list) whose keys no query sees are not read, nor are their
+ * entries: such entries may hold anything.  Each sequence reads what it sees of the
+ * prefix by itself.  The other arguments, their bounds and the results are those of
+ * bitlinear_attention, ws of bitlinear_attention_window_workspace_bytes bytes.
+ */
+int64_t bitlinear_attention_window_workspace_bytes(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim,
+                                                   int64_t seqs, int64_t max_q, int64_t max_own, int64_t prefix_len,
+                                                   int64_t window, int64_t sinks);
+
+int bitlinear_attention_window(const bitlinear_cache_t *cache, const void *Q, int dtype, int64_t tokens, int64_t heads,
+                               int64_t ldq_token, int64_t ldq_head, int64_t seqs, const int32_t *q_start, int64_t max_q,
+                               const int32_t *own_pages, int64_t ld_pages, const int32_t *own_len, int64_t max_own,
+                               const int32_t *prefix_pages, int64_t prefix_len, int64_t window, int64_t sinks,
+                               float scale, void *O, int64_t ldo_token, int64_t ldo_head, float *lse, void *ws,
+                               int64_t ws_bytes, void *stream);
+
+/*
+ * Attention as bitlinear_attention's for trees of drafted tokens: the n_b query
+ * tokens of sequence b are the tree's, their keys the last n_b of its own.  Query
+ * token i sees the prefix, the own keys before the tree's (0 .. own_len[b] - n_b - 1),
+ * and the key of query token j of its sequence where its row of 'tree' has bit j:
+ * its ancestors and itself, as a rule, but any bits are taken.
+ *   tree    uint64 [tokens x ld_tree] (device): bit j % 64 of word j / 64 of a token's
+ *           row; ld_tree >= ceil(min(max_q, tokens) / 64).  Bits n_b and up are ignored.
+ *           8-byte aligned.
+ * With own_len[b] < n_b the first n_b - own_len[b] query tokens have no key.  The
+ * other arguments, their bounds, the workspace (bitlinear_attention_workspace_bytes)
+ * and the results are those of bitlinear_attention.
+ */
+int bitlinear_attention_tree(const bitlinear_cache_t *cache, const void *Q, int dtype, int64_t tokens, int64_t heads,
+                             int64_t ldq_token, int64_t ldq_head, int64_t seqs, const int32_t *q_start, int64_t max_q,
+                             const int32_t *own_pages, int64_t ld_pages, const int32_t *own_len, int64_t max_own,
+                             const int32_t *prefix_pages, int64_t prefix_len, const uint64_t *tree, int64_t ld_tree,
+                             float scale, void *O, int64_t ldo_token, int64_t ldo_head, float *lse, void *ws,
+                             int64_t ws_bytes, void *stream);
+
+/*
+ * Places of a step's new tokens: lengths, block tables and slots from the number of
+ * new tokens of every sequence, all on the device.  Sequence b holds held[b] own
+ * tokens (cut to [0, max_own]) in the pages own_pages[b][0 .. ceil(held[b] /
+ * page_tokens) - 1] and asks for count[b]:
+ *   count[b] >= 0: so many new tokens behind its own, in pages taken from the free
+ *           list where its last one ends.  A sequence whose pages the list does not
+ *           cover, that would pass max_own, or whose tokens would pass 'tokens', gets
+ *           nothing: its length stays, its tokens have no slots and first[b] = -1.
+ *           Pages go to the sequences in order until one asks for more than are left;
+ *           it and all later ones that ask for pages get none.
+ *   count[b] < 0: its last -count[b] tokens are given up (all, if it holds fewer), and
+ *           the pages that hold none of the others go back to the free list.
+ * The free list is a stack: pages given back are put on top in the order of the
+ * sequences and of their pages, then pages are taken from the top, one after the
+ * other, in the same order.
+ *   own_pages int32 [seqs x ld_pages] (read, new entries written),
+ *           ld_pages >= ceil(max_own / page_tokens).
+ *   free_pages int32 [max_free] (read, pages given back written; a page for which it
+ *           has no room is lost); free_count int32 [1]: pages it holds, cut to
+ *           [0, max_free].  May be NULL where max_free = 0.
+ *   free_left int32 [1] (written): pages it holds afterwards; may be free_count.
+ *   own_len int32 [seqs] (written): lengths afterwards; may be held.
+ *   first   int32 [seqs] (written): own position of the sequence's first new token
+ *           (own_len where there is none), or -1 where it got nothing.
+ *   q_start int32 [seqs + 1] (written): sums of the positive counts, cut to 'tokens':
+ *           what the attention entries take.
+ *   slots   int64 [tokens] (written): slot of each token in that order, -1 for those
+ *           without a place and for tokens of no sequence.  What bitlinear_cache_write
+ *           takes.
+ *   positions int32 [tokens] (written) or NULL: prefix_len + own position, -1 where
+ *           the slot is -1.
+ * seqs in [1, 65536], tokens in [0, 2^24], page_tokens a multiple of 64 up to 2^20,
+ * max_own and prefix_len in [0, 2^30], max_free in [0, 2^31 - 1].  Entries of the
+ * tables and of the list are not checked: the cache's entries skip pages outside it.
+ * Deterministic.  No output may overlap anything but as named.
+ */
+int bitlinear_cache_assign(int64_t seqs, int64_t page_tokens, const int32_t *held, const int32_t *count,
+                           int64_t max_own, int32_t *own_pages, int64_t ld_pages, int32_t *free_pages, int64_t max_free,
+                           const int32_t *free_count, int32_t *free_left, int32_t *own_len, int32_t *first,
+                           int32_t *q_start, int64_t *slots, int32_t *positions, int64_t tokens, int64_t prefix_len,
+                           void *stream);
+
+/*
+ * Move keys and values from slot to slot, bytes and scales as they are (the drafted
+ * tokens that were accepted, next to one another).
+ *   src, dst int64 [groups x width] (device): move j of group g takes slot
+ *           src[g * width + j] to dst[g * width + j].  The moves of a group happen at
+ *           once: all slots are read before one is written, so that they may overlap;
+ *           of several moves of a group to one slot the last counts.  A move from or to
+ *           a slot outside the cache is skipped.  A slot that one group writes and
+ *           another reads or writes races.
+ * groups in [0, 2^20], 0 does nothing; width in [1, BITLINEAR_MAX_MOVES].
+ */
+#define BITLINEAR_MAX_MOVES 64
+int bitlinear_cache_move(const bitlinear_cache_t *cache, const int64_t *src, const int64_t *dst, int64_t groups,
+                         int64_t width, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

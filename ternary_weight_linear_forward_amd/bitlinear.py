@@ -72,6 +72,7 @@ class Cache(ctypes.Structure):
 
 
 MAX_HEAD_DIM = 256
+MAX_MOVES = 64
 _CACHE = ctypes.POINTER(Cache)
 _F32 = ctypes.c_float
 
@@ -124,6 +125,14 @@ _SIGNATURES = {
     "bitlinear_attention_workspace_bytes": ([_I64] * 8, _I64),
     "bitlinear_attention": ([_CACHE, _P, _INT, _I64, _I64, _I64, _I64, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64,
                              _F32, _P, _I64, _I64, _P, _P, _I64, _P], _INT),
+    "bitlinear_attention_window_workspace_bytes": ([_I64] * 10, _I64),
+    "bitlinear_attention_window": ([_CACHE, _P, _INT, _I64, _I64, _I64, _I64, _I64, _P, _I64, _P, _I64, _P, _I64, _P,
+                                    _I64, _I64, _I64, _F32, _P, _I64, _I64, _P, _P, _I64, _P], _INT),
+    "bitlinear_attention_tree": ([_CACHE, _P, _INT, _I64, _I64, _I64, _I64, _I64, _P, _I64, _P, _I64, _P, _I64, _P,
+                                  _I64, _P, _I64, _F32, _P, _I64, _I64, _P, _P, _I64, _P], _INT),
+    "bitlinear_cache_assign": ([_I64, _I64, _P, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _P],
+                               _INT),
+    "bitlinear_cache_move": ([_CACHE, _P, _P, _I64, _I64, _P], _INT),
 }
 EXPORTED = tuple(_SIGNATURES)
 
@@ -331,6 +340,39 @@ def bitlinear_attention(cache, Q, dtype, tokens, heads, ldq_token, ldq_head, seq
                                     ldo_token, ldo_head, lse, ws, ws_bytes, stream)
 
 
+def bitlinear_attention_window_workspace_bytes(tokens, heads, kv_heads, head_dim, seqs, max_q, max_own, prefix_len,
+                                               window, sinks) -> int:
+    return _lib.bitlinear_attention_window_workspace_bytes(tokens, heads, kv_heads, head_dim, seqs, max_q, max_own,
+                                                           prefix_len, window, sinks)
+
+
+def bitlinear_attention_window(cache, Q, dtype, tokens, heads, ldq_token, ldq_head, seqs, q_start, max_q, own_pages,
+                               ld_pages, own_len, max_own, prefix_pages, prefix_len, window, sinks, scale, O, ldo_token,
+                               ldo_head, lse, ws, ws_bytes, stream) -> int:
+    return _lib.bitlinear_attention_window(cache, Q, dtype, tokens, heads, ldq_token, ldq_head, seqs, q_start, max_q,
+                                           own_pages, ld_pages, own_len, max_own, prefix_pages, prefix_len, window,
+                                           sinks, scale, O, ldo_token, ldo_head, lse, ws, ws_bytes, stream)
+
+
+def bitlinear_attention_tree(cache, Q, dtype, tokens, heads, ldq_token, ldq_head, seqs, q_start, max_q, own_pages,
+                             ld_pages, own_len, max_own, prefix_pages, prefix_len, tree, ld_tree, scale, O, ldo_token,
+                             ldo_head, lse, ws, ws_bytes, stream) -> int:
+    return _lib.bitlinear_attention_tree(cache, Q, dtype, tokens, heads, ldq_token, ldq_head, seqs, q_start, max_q,
+                                         own_pages, ld_pages, own_len, max_own, prefix_pages, prefix_len, tree, ld_tree,
+                                         scale, O, ldo_token, ldo_head, lse, ws, ws_bytes, stream)
+
+
+def bitlinear_cache_assign(seqs, page_tokens, held, count, max_own, own_pages, ld_pages, free_pages, max_free, free_count,
+                           free_left, own_len, first, q_start, slots, positions, tokens, prefix_len, stream) -> int:
+    return _lib.bitlinear_cache_assign(seqs, page_tokens, held, count, max_own, own_pages, ld_pages, free_pages, max_free,
+                                       free_count, free_left, own_len, first, q_start, slots, positions, tokens,
+                                       prefix_len, stream)
+
+
+def bitlinear_cache_move(cache, src, dst, groups, width, stream) -> int:
+    return _lib.bitlinear_cache_move(cache, src, dst, groups, width, stream)
+
+
 # --- torch-tensor helpers (allocation + marshalling) ------------------------
 def _torch():
     import torch
@@ -346,6 +388,7 @@ def _stream(stream=None) -> int:
 
 _CODES = {} if torch is None else {torch.float32: F32, torch.bfloat16: BF16, torch.int8: I8, torch.int32: I32}
 _FLOATS = {} if torch is None else {torch.float32: F32, torch.bfloat16: BF16}
+_WORDS = () if torch is None else (torch.int64, torch.uint64)
 
 
 def _dtype_code(t) -> int:
@@ -647,6 +690,9 @@ def _on(stream, call, *args):
     for t in args:
         if isinstance(t, torch.Tensor):
             t.record_stream(stream)
+        elif isinstance(t, KVCache):
+            for part in (t.k, t.v, t.k_scale, t.v_scale):
+                part.record_stream(stream)
     for t in out if isinstance(out, tuple) else (out,):
         if t is not None:
             t.record_stream(caller)
@@ -779,17 +825,75 @@ def cache_read(cache: KVCache, slots, dtype=None, stream=None):
     return K, V
 
 
-def attention(cache: KVCache, Q, own_pages, own_len, max_own: int, prefix_pages=None, prefix_len: int = 0, q_start=None,
-              max_q: int = 1, scale: float | None = None, out=None, return_lse: bool = False, ws=None, stream=None):
-    """Attention of sequences that share a prefix (bitlinear_attention).
-    Q [tokens x heads x head_dim] fp32/bf16; own_pages int32 [seqs x pages],
-    own_len int32 [seqs] (at most max_own); prefix_pages int32; q_start int32
-    [seqs + 1] or None (max_q tokens each); scale 1 / sqrt(head_dim) by
-    default.  Returns O (Q's shape and dtype), or (O, lse fp32 [tokens x heads])."""
+def _here(where: str, *tensors) -> None:
+    """Refuses tensors that are not on the current device, whose kernels would follow their addresses."""
+    for t in tensors:
+        if t is not None and not (t.is_cuda and t.get_device() == torch.cuda.current_device()):
+            raise BitlinearError(ERR_INVALID_ARG, where)
+
+
+def cache_assign(held, count, own_pages, free_pages, free_count, tokens: int, page_tokens: int, max_own: int | None = None,
+                 prefix_len: int = 0, own_len=None, free_left=None, stream=None):
+    """Places of a step's new tokens (bitlinear_cache_assign): held, count int32 [seqs] (a negative count gives tokens
+    back); own_pages int32 [seqs x pages] and the free list free_pages int32 [any], free_count int32 [1], both written;
+    'tokens' new tokens at most, own lengths of at most max_own (by default what own_pages has room for).
+    Returns (own_len int32 [seqs], first int32 [seqs], q_start int32 [seqs + 1], slots int64 [tokens], positions int32
+    [tokens], free_left int32 [1]); own_len may be given as 'held', free_left as 'free_count'."""
     if stream is not None:
-        return _on(stream, attention, cache, Q, own_pages, own_len, max_own, prefix_pages, prefix_len, q_start, max_q, scale,
-                   out, return_lse, ws)
-    name = "attention"
+        return _on(stream, cache_assign, held, count, own_pages, free_pages, free_count, tokens, page_tokens, max_own,
+                   prefix_len, own_len, free_left)
+    name, i32 = "cache_assign", torch.int32
+    seqs = held.numel()
+    if own_pages.dim() != 2 or page_tokens < 1:
+        raise BitlinearError(ERR_INVALID_ARG, name)
+    rows, cols = own_pages.shape
+    ldp, step = own_pages.stride()
+    if max_own is None:
+        max_own = cols * page_tokens
+    vectors = [(held, seqs), (count, seqs), (free_pages, free_pages.numel()), (free_count, 1)]
+    vectors += [(own_len, seqs)] if own_len is not None else []
+    vectors += [(free_left, 1)] if free_left is not None else []
+    if own_pages.dtype != i32 or rows != seqs or (cols > 1 and step != 1) or (rows > 1 and ldp < cols) or \
+            cols * page_tokens < max_own or tokens < 0 or \
+            any(t.dtype != i32 or t.dim() != 1 or t.numel() != n or not t.is_contiguous() for t, n in vectors):
+        raise BitlinearError(ERR_INVALID_ARG, name)
+    _here(name, held, count, own_pages, free_pages, free_count, own_len, free_left)
+    # one allocation: lengths, first positions, starts, positions, list
+    n = (0, 0 if own_len is not None else seqs, seqs, seqs + 1, tokens, 0 if free_left is not None else 1)
+    parts = held.new_empty(sum(n)).split(n[1:])
+    own_len = parts[0] if own_len is None else own_len
+    free_left = parts[4] if free_left is None else free_left
+    first, q_start, positions = parts[1], parts[2], parts[3]
+    slots = held.new_empty(tokens, dtype=torch.int64)
+    _check(_lib.bitlinear_cache_assign(
+        seqs, page_tokens, held.data_ptr(), count.data_ptr(), max_own, own_pages.data_ptr(), ldp if rows > 1 else max(ldp, cols),
+        free_pages.data_ptr(), free_pages.numel(), free_count.data_ptr(), free_left.data_ptr(), own_len.data_ptr(),
+        first.data_ptr(), q_start.data_ptr(), slots.data_ptr(), positions.data_ptr(), tokens, prefix_len, _stream()),
+        "bitlinear_cache_assign")
+    return own_len, first, q_start, slots, positions, free_left
+
+
+def cache_move(cache: KVCache, src, dst, stream=None) -> None:
+    """Move keys and values from slots src to slots dst, int64 [groups x width] or [width <= 64] (bitlinear_cache_move): a
+    row's moves happen at once; moves from or to slots outside the cache are skipped."""
+    if stream is not None:
+        return _on(stream, cache_move, cache, src, dst)
+    name = "cache_move"
+    if src.dim() not in (1, 2) or src.shape != dst.shape or src.dtype != torch.int64 or dst.dtype != torch.int64 or \
+            not (src.is_contiguous() and dst.is_contiguous()):
+        raise BitlinearError(ERR_INVALID_ARG, name)
+    groups, width = src.shape if src.dim() == 2 else (1, src.shape[0])
+    if width == 0:
+        return None
+    _here(name, src, dst, cache.k, cache.v, cache.k_scale, cache.v_scale)
+    _check(_lib.bitlinear_cache_move(cache.desc, src.data_ptr(), dst.data_ptr(), groups, width, _stream()),
+           "bitlinear_cache_move")
+
+
+def _attention(name, entry, need, extra, cache, Q, own_pages, own_len, max_own, prefix_pages, prefix_len, q_start, max_q,
+               scale, out, return_lse, ws):
+    """An attention entry on checked tensors: need(sizes ..) gives its workspace's bytes, 'extra' are its arguments
+    between prefix_len and scale."""
     tokens, heads, D = Q.shape
     seqs = own_len.numel()
     pt, i32 = cache.page_tokens, torch.int32
@@ -813,15 +917,66 @@ def attention(cache: KVCache, Q, own_pages, own_len, max_own: int, prefix_pages=
             (prefix_len > 0 and (prefix_pages is None or prefix_pages.numel() * pt < prefix_len or
                                  not prefix_pages.is_contiguous())):
         raise BitlinearError(ERR_INVALID_ARG, name)
-    nws = _lib.bitlinear_attention_workspace_bytes(tokens, heads, cache.heads, D, seqs, max_q, max_own, prefix_len)
+    nws = need(tokens, heads, cache.heads, D, seqs, max_q, max_own, prefix_len)
     if nws < 0:
         raise BitlinearError(ERR_INVALID_ARG, name)
     if nws > 0 and (ws is None or ws.numel() < nws):
         ws = torch.empty(nws, dtype=torch.uint8, device=Q.device)
     lse = torch.empty((tokens, heads), dtype=torch.float32, device=Q.device) if return_lse else None
-    _check(_lib.bitlinear_attention(
+    _check(entry(
         cache.desc, Q.data_ptr(), _dtype_code(Q), tokens, heads, lqt, lqh, seqs, _ptr(q_start), max_q,
         own_pages.data_ptr(), ldp if rows > 1 else max(ldp, cols), own_len.data_ptr(), max_own, _ptr(prefix_pages),
-        prefix_len, D ** -0.5 if scale is None else scale, out.data_ptr(), lot, loh, _ptr(lse),
-        _ptr(ws) if nws > 0 else None, nws, _stream()), "bitlinear_attention")
+        prefix_len, *extra, D ** -0.5 if scale is None else scale, out.data_ptr(), lot, loh, _ptr(lse),
+        _ptr(ws) if nws > 0 else None, nws, _stream()), "bitlinear_" + name)
     return (out, lse) if return_lse else out
+
+
+def attention(cache: KVCache, Q, own_pages, own_len, max_own: int, prefix_pages=None, prefix_len: int = 0, q_start=None,
+              max_q: int = 1, scale: float | None = None, out=None, return_lse: bool = False, ws=None, stream=None):
+    """Attention of sequences that share a prefix (bitlinear_attention).
+    Q [tokens x heads x head_dim] fp32/bf16; own_pages int32 [seqs x pages],
+    own_len int32 [seqs] (at most max_own); prefix_pages int32; q_start int32
+    [seqs + 1] or None (max_q tokens each); scale 1 / sqrt(head_dim) by
+    default.  Returns O (Q's shape and dtype), or (O, lse fp32 [tokens x heads])."""
+    if stream is not None:
+        return _on(stream, attention, cache, Q, own_pages, own_len, max_own, prefix_pages, prefix_len, q_start, max_q, scale,
+                   out, return_lse, ws)
+    return _attention("attention", _lib.bitlinear_attention, _lib.bitlinear_attention_workspace_bytes, (), cache, Q, own_pages,
+                      own_len, max_own, prefix_pages, prefix_len, q_start, max_q, scale, out, return_lse, ws)
+
+
+def attention_window(cache: KVCache, Q, own_pages, own_len, max_own: int, window: int, sinks: int = 0, prefix_pages=None,
+                     prefix_len: int = 0, q_start=None, max_q: int = 1, scale: float | None = None, out=None,
+                     return_lse: bool = False, ws=None, stream=None):
+    """attention in which a query sees the last 'window' of its keys and the sequence's first 'sinks' ones
+    (bitlinear_attention_window).  The other arguments and the result as for attention."""
+    if stream is not None:
+        return _on(stream, attention_window, cache, Q, own_pages, own_len, max_own, window, sinks, prefix_pages, prefix_len,
+                   q_start, max_q, scale, out, return_lse, ws)
+    name = "attention_window"
+    _here(name, Q, own_pages, own_len, prefix_pages, q_start, out, ws, cache.k, cache.v, cache.k_scale, cache.v_scale)
+    need = _lib.bitlinear_attention_window_workspace_bytes
+    return _attention(name, _lib.bitlinear_attention_window, lambda *sizes: need(*sizes, window, sinks), (window, sinks),
+                      cache, Q, own_pages, own_len, max_own, prefix_pages, prefix_len, q_start, max_q, scale, out, return_lse,
+                      ws)
+
+
+def attention_tree(cache: KVCache, Q, own_pages, own_len, max_own: int, tree, prefix_pages=None, prefix_len: int = 0,
+                   q_start=None, max_q: int = 1, scale: float | None = None, out=None, return_lse: bool = False, ws=None,
+                   stream=None):
+    """attention in which the query tokens of a sequence are a tree of drafts (bitlinear_attention_tree): tree int64
+    [tokens x words], whose bit j % 64 of word j / 64 lets a token see the key of its sequence's query token j.  The other
+    arguments and the result as for attention."""
+    if stream is not None:
+        return _on(stream, attention_tree, cache, Q, own_pages, own_len, max_own, tree, prefix_pages, prefix_len, q_start,
+                   max_q, scale, out, return_lse, ws)
+    name = "attention_tree"
+    if tree.dim() != 2 or tree.dtype not in _WORDS or tree.shape[0] != Q.shape[0] or tree.shape[1] * 64 < min(max_q, Q.shape[0]) or \
+            (tree.shape[1] > 1 and tree.stride(1) != 1):
+        raise BitlinearError(ERR_INVALID_ARG, name)
+    rows, words = tree.shape
+    ldt = tree.stride(0) if rows > 1 else words
+    _here(name, Q, own_pages, own_len, prefix_pages, q_start, out, ws, tree, cache.k, cache.v, cache.k_scale, cache.v_scale)
+    return _attention(name, _lib.bitlinear_attention_tree, _lib.bitlinear_attention_workspace_bytes, (tree.data_ptr(), ldt),
+                      cache, Q, own_pages, own_len, max_own, prefix_pages, prefix_len, q_start, max_q, scale, out, return_lse,
+                      ws)

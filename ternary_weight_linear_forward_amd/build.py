@@ -22,7 +22,7 @@ INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libbitlinear.so")
 SOURCES = ["api.cpp", "api_layer.cpp", "weights.hip", "act.hip", "gemv.hip", "group.hip", "gemm.hip", "backward.hip",
-           "norm.hip", "cache.hip", "attention.hip"]
+           "norm.hip", "cache.hip", "assign.hip", "attention.hip", "attn_masked.hip"]
 
 
 def hipcc() -> str:

@@ -4,6 +4,7 @@
 // when validation fails.  No allocation, no synchronisation, no state.
 #include "bitlinear.h"
 
+#include <algorithm>
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -88,6 +89,92 @@ bool attn_sizes_ok(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head
            prefix_len >= 0 && prefix_len <= kMaxKeys && seqs * max_q <= kMaxRows / heads &&
            tokens <= kMaxRows / heads;
 }
+
+constexpr int64_t kMaxAssign = 65536;                    // sequences of one assignment
+
+// (prefix_len + max_own reach 2^31)
+bool window_ok(int64_t window, int64_t sinks)
+{
+    return window >= 1 && window <= (int64_t(1) << 31) && sinks >= 0 && sinks <= kMaxKeys;
+}
+
+// Which keys a row sees beside the causal limit: a window, or a tree.
+struct Sight {
+    int64_t window = 0, sinks = 0;
+    const uint64_t *tree = nullptr;
+    int64_t ld_tree = 0;
+};
+
+int attention_call(const Sight &sight, const bitlinear_cache_t *cache, const void *Q, int dtype, int64_t tokens,
+                   int64_t heads, int64_t ldq_token, int64_t ldq_head, int64_t seqs, const int32_t *q_start,
+                   int64_t max_q, const int32_t *own_pages, int64_t ld_pages, const int32_t *own_len, int64_t max_own,
+                   const int32_t *prefix_pages, int64_t prefix_len, float scale, void *O, int64_t ldo_token,
+                   int64_t ldo_head, float *lse, void *ws, int64_t ws_bytes, void *stream)
+{
+    bl::AttnArgs a;
+    CacheSpans cs;
+    const int st = check_cache(cache, &a.c, &cs);
+    if (st != BITLINEAR_OK) return st;
+    if (!Q || !O || !own_len || !float_dtype(dtype) || !isfinite(scale) ||
+        !attn_sizes_ok(tokens, heads, a.c.heads, a.c.D, seqs, max_q, max_own, prefix_len))
+        return BITLINEAR_ERR_INVALID_ARG;
+    if (!q_start && tokens != seqs * max_q) return BITLINEAR_ERR_INVALID_ARG;
+    const int64_t np = (prefix_len + a.c.page_tokens - 1) / a.c.page_tokens,
+                  no = (max_own + a.c.page_tokens - 1) / a.c.page_tokens;
+    if ((np > 0 && !prefix_pages) || (no > 0 && !own_pages) || ld_pages < no || !stride_ok(seqs, ld_pages + 1))
+        return BITLINEAR_ERR_INVALID_ARG;
+    const int es = dtype_size(dtype);
+    if (!aligned_to(Q, es) || !aligned_to(O, es) || !aligned_to(q_start, 4) || !aligned_to(own_pages, 4) ||
+        !aligned_to(own_len, 4) || !aligned_to(prefix_pages, 4) || !aligned_to(lse, 4) ||
+        !rows_ok(tokens, heads, ldq_token, ldq_head, a.c.D, false) ||
+        !rows_ok(tokens, heads, ldo_token, ldo_head, a.c.D, true))
+        return BITLINEAR_ERR_INVALID_ARG;
+    const int64_t need = bl::attn_workspace_bytes(tokens, heads, a.c.heads, a.c.D, seqs, max_q, max_own, prefix_len, sight.window,
+                                 sight.sinks);
+    if (need > 0 && (!ws || ws_bytes < need)) return BITLINEAR_ERR_WORKSPACE;
+    if (need > 0 && !aligned16(ws)) return BITLINEAR_ERR_INVALID_ARG;
+    const Span so = rows_span(O, tokens, heads, ldo_token, ldo_head, a.c.D, es),
+               sl = lse ? span_of(lse, 1, tokens * heads, tokens * heads, 4) : Span{0, 0},
+               sw = need > 0 ? span_of(ws, 1, need, need, 1) : Span{0, 0};
+    const Span in[] = {rows_span(Q, tokens, heads, ldq_token, ldq_head, a.c.D, es),
+                       q_start ? span_of(q_start, 1, seqs + 1, seqs + 1, 4) : Span{0, 0},
+                       no > 0 ? span_of(own_pages, seqs, ld_pages, no, 4) : Span{0, 0},
+                       span_of(own_len, 1, seqs, seqs, 4),
+                       np > 0 ? span_of(prefix_pages, 1, np, np, 4) : Span{0, 0},
+                       sight.tree ? span_of(sight.tree, tokens, sight.ld_tree, sight.ld_tree, 8) : Span{0, 0},
+                       cs.s[0], cs.s[1], cs.s[2], cs.s[3]};
+    for (const Span &s : in)
+        if (overlap(so, s) || overlap(sl, s) || overlap(sw, s)) return BITLINEAR_ERR_INVALID_ARG;
+    if (overlap(so, sl) || overlap(so, sw) || overlap(sl, sw)) return BITLINEAR_ERR_INVALID_ARG;
+    a.Q = Q;
+    a.O = O;
+    a.lse = lse;
+    a.q_start = q_start;
+    a.own_pages = own_pages;
+    a.own_len = own_len;
+    a.prefix_pages = prefix_pages;
+    a.ldq_t = ldq_token;
+    a.ldq_h = ldq_head;
+    a.ldo_t = ldo_token;
+    a.ldo_h = ldo_head;
+    a.ld_pages = ld_pages;
+    a.dtype = dtype;
+    a.tokens = static_cast<int>(tokens);
+    a.heads = static_cast<int>(heads);
+    a.seqs = static_cast<int>(seqs);
+    a.max_q = static_cast<int>(max_q);
+    a.max_own = static_cast<int>(max_own);
+    a.prefix = static_cast<int>(prefix_len);
+    a.scale = scale;
+    a.ws = static_cast<float *>(ws);
+    a.window = sight.window;
+    a.sinks = static_cast<int>(sight.sinks);
+    a.tree = sight.tree;
+    a.ld_tree = sight.ld_tree;
+    (void)hipGetLastError();
+    return status_of(bl::launch_attention(a, as_stream(stream)));
+}
+
 
 } // namespace
 
@@ -294,63 +381,130 @@ int bitlinear_attention(const bitlinear_cache_t *cache, const void *Q, int dtype
                         const int32_t *prefix_pages, int64_t prefix_len, float scale, void *O, int64_t ldo_token,
                         int64_t ldo_head, float *lse, void *ws, int64_t ws_bytes, void *stream)
 {
-    bl::AttnArgs a;
-    CacheSpans cs;
-    const int st = check_cache(cache, &a.c, &cs);
-    if (st != BITLINEAR_OK) return st;
-    if (!Q || !O || !own_len || !float_dtype(dtype) || !isfinite(scale) ||
-        !attn_sizes_ok(tokens, heads, a.c.heads, a.c.D, seqs, max_q, max_own, prefix_len))
+    return attention_call(Sight(), cache, Q, dtype, tokens, heads, ldq_token, ldq_head, seqs, q_start, max_q, own_pages,
+                          ld_pages, own_len, max_own, prefix_pages, prefix_len, scale, O, ldo_token, ldo_head, lse, ws,
+                          ws_bytes, stream);
+}
+
+int64_t bitlinear_attention_window_workspace_bytes(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim,
+                                                   int64_t seqs, int64_t max_q, int64_t max_own, int64_t prefix_len,
+                                                   int64_t window, int64_t sinks)
+{
+    if (!attn_sizes_ok(tokens, heads, kv_heads, head_dim, seqs, max_q, max_own, prefix_len) || !window_ok(window, sinks))
+        return -1;
+    return bl::attn_workspace_bytes(tokens, heads, kv_heads, head_dim, seqs, max_q, max_own, prefix_len, window, sinks);
+}
+
+int bitlinear_attention_window(const bitlinear_cache_t *cache, const void *Q, int dtype, int64_t tokens, int64_t heads,
+                               int64_t ldq_token, int64_t ldq_head, int64_t seqs, const int32_t *q_start, int64_t max_q,
+                               const int32_t *own_pages, int64_t ld_pages, const int32_t *own_len, int64_t max_own,
+                               const int32_t *prefix_pages, int64_t prefix_len, int64_t window, int64_t sinks,
+                               float scale, void *O, int64_t ldo_token, int64_t ldo_head, float *lse, void *ws,
+                               int64_t ws_bytes, void *stream)
+{
+    if (!window_ok(window, sinks)) return BITLINEAR_ERR_INVALID_ARG;
+    Sight s;
+    s.window = window;
+    s.sinks = sinks;
+    return attention_call(s, cache, Q, dtype, tokens, heads, ldq_token, ldq_head, seqs, q_start, max_q, own_pages,
+                          ld_pages, own_len, max_own, prefix_pages, prefix_len, scale, O, ldo_token, ldo_head, lse, ws,
+                          ws_bytes, stream);
+}
+
+int bitlinear_attention_tree(const bitlinear_cache_t *cache, const void *Q, int dtype, int64_t tokens, int64_t heads,
+                             int64_t ldq_token, int64_t ldq_head, int64_t seqs, const int32_t *q_start, int64_t max_q,
+                             const int32_t *own_pages, int64_t ld_pages, const int32_t *own_len, int64_t max_own,
+                             const int32_t *prefix_pages, int64_t prefix_len, const uint64_t *tree, int64_t ld_tree,
+                             float scale, void *O, int64_t ldo_token, int64_t ldo_head, float *lse, void *ws,
+                             int64_t ws_bytes, void *stream)
+{
+    if (!tree || !aligned_to(tree, 8) || tokens < 1 || tokens > kMaxQueries || max_q < 1 || ld_tree < 1 ||
+        ld_tree < (std::min(max_q, tokens) + 63) / 64 || !stride_ok(tokens, ld_tree))
         return BITLINEAR_ERR_INVALID_ARG;
-    if (!q_start && tokens != seqs * max_q) return BITLINEAR_ERR_INVALID_ARG;
-    const int64_t np = (prefix_len + a.c.page_tokens - 1) / a.c.page_tokens,
-                  no = (max_own + a.c.page_tokens - 1) / a.c.page_tokens;
-    if ((np > 0 && !prefix_pages) || (no > 0 && !own_pages) || ld_pages < no || !stride_ok(seqs, ld_pages + 1))
+    Sight s;
+    s.tree = tree;
+    s.ld_tree = ld_tree;
+    return attention_call(s, cache, Q, dtype, tokens, heads, ldq_token, ldq_head, seqs, q_start, max_q, own_pages,
+                          ld_pages, own_len, max_own, prefix_pages, prefix_len, scale, O, ldo_token, ldo_head, lse, ws,
+                          ws_bytes, stream);
+}
+
+int bitlinear_cache_assign(int64_t seqs, int64_t page_tokens, const int32_t *held, const int32_t *count,
+                           int64_t max_own, int32_t *own_pages, int64_t ld_pages, int32_t *free_pages, int64_t max_free,
+                           const int32_t *free_count, int32_t *free_left, int32_t *own_len, int32_t *first,
+                           int32_t *q_start, int64_t *slots, int32_t *positions, int64_t tokens, int64_t prefix_len,
+                           void *stream)
+{
+    if (seqs < 1 || seqs > kMaxAssign || page_tokens < 64 || page_tokens % 64 || page_tokens > (int64_t(1) << 20) ||
+        max_own < 0 || max_own > kMaxKeys || prefix_len < 0 || prefix_len > kMaxKeys || max_free < 0 ||
+        max_free > INT32_MAX || tokens < 0 || tokens > kMaxCacheTokens)
         return BITLINEAR_ERR_INVALID_ARG;
-    const int es = dtype_size(dtype);
-    if (!aligned_to(Q, es) || !aligned_to(O, es) || !aligned_to(q_start, 4) || !aligned_to(own_pages, 4) ||
-        !aligned_to(own_len, 4) || !aligned_to(prefix_pages, 4) || !aligned_to(lse, 4) ||
-        !rows_ok(tokens, heads, ldq_token, ldq_head, a.c.D, false) ||
-        !rows_ok(tokens, heads, ldo_token, ldo_head, a.c.D, true))
+    const int64_t cols = (max_own + page_tokens - 1) / page_tokens;
+    if (!held || !count || !own_len || !first || !q_start || !free_left || (cols > 0 && !own_pages) ||
+        (tokens > 0 && !slots) || (max_free > 0 && (!free_pages || !free_count)) || ld_pages < cols ||
+        !stride_ok(seqs, ld_pages + 1))
         return BITLINEAR_ERR_INVALID_ARG;
-    const int64_t need =
-        bl::attn_workspace_bytes(tokens, heads, a.c.heads, a.c.D, seqs, max_q, max_own, prefix_len);
-    if (need > 0 && (!ws || ws_bytes < need)) return BITLINEAR_ERR_WORKSPACE;
-    if (need > 0 && !aligned16(ws)) return BITLINEAR_ERR_INVALID_ARG;
-    const Span so = rows_span(O, tokens, heads, ldo_token, ldo_head, a.c.D, es),
-               sl = lse ? span_of(lse, 1, tokens * heads, tokens * heads, 4) : Span{0, 0},
-               sw = need > 0 ? span_of(ws, 1, need, need, 1) : Span{0, 0};
-    const Span in[] = {rows_span(Q, tokens, heads, ldq_token, ldq_head, a.c.D, es),
-                       q_start ? span_of(q_start, 1, seqs + 1, seqs + 1, 4) : Span{0, 0},
-                       no > 0 ? span_of(own_pages, seqs, ld_pages, no, 4) : Span{0, 0},
-                       span_of(own_len, 1, seqs, seqs, 4),
-                       np > 0 ? span_of(prefix_pages, 1, np, np, 4) : Span{0, 0},
-                       cs.s[0], cs.s[1], cs.s[2], cs.s[3]};
-    for (const Span &s : in)
-        if (overlap(so, s) || overlap(sl, s) || overlap(sw, s)) return BITLINEAR_ERR_INVALID_ARG;
-    if (overlap(so, sl) || overlap(so, sw) || overlap(sl, sw)) return BITLINEAR_ERR_INVALID_ARG;
-    a.Q = Q;
-    a.O = O;
-    a.lse = lse;
-    a.q_start = q_start;
+    if (!aligned_to(held, 4) || !aligned_to(count, 4) || !aligned_to(own_pages, 4) || !aligned_to(free_pages, 4) ||
+        !aligned_to(free_count, 4) || !aligned_to(free_left, 4) || !aligned_to(own_len, 4) || !aligned_to(first, 4) ||
+        !aligned_to(q_start, 4) || !aligned_to(slots, 8) || !aligned_to(positions, 4))
+        return BITLINEAR_ERR_INVALID_ARG;
+    const Span none = {0, 0};
+    // what is written, then what is only read: nothing written may overlap anything, but own_len may be held
+    // and free_left free_count
+    const Span out[] = {span_of(own_len, 1, seqs, seqs, 4),
+                        span_of(free_left, 1, 1, 1, 4),
+                        span_of(first, 1, seqs, seqs, 4),
+                        span_of(q_start, 1, seqs + 1, seqs + 1, 4),
+                        tokens > 0 ? span_of(slots, 1, tokens, tokens, 8) : none,
+                        positions && tokens > 0 ? span_of(positions, 1, tokens, tokens, 4) : none,
+                        cols > 0 ? span_of(own_pages, seqs, ld_pages, cols, 4) : none,
+                        max_free > 0 ? span_of(free_pages, 1, max_free, max_free, 4) : none};
+    const Span in[] = {span_of(held, 1, seqs, seqs, 4), max_free > 0 ? span_of(free_count, 1, 1, 1, 4) : none,
+                       span_of(count, 1, seqs, seqs, 4)};
+    for (int i = 0; i < 8; ++i) {
+        for (int k = 0; k < i; ++k)
+            if (overlap(out[i], out[k])) return BITLINEAR_ERR_INVALID_ARG;
+        for (int k = 0; k < 3; ++k)
+            if (overlap(out[i], in[k]) && !(i == k && out[i].lo == in[k].lo)) return BITLINEAR_ERR_INVALID_ARG;
+    }
+    bl::AssignArgs a;
+    a.held = held;
+    a.count = count;
+    a.free_count = max_free > 0 ? free_count : nullptr;
     a.own_pages = own_pages;
+    a.free_pages = free_pages;
+    a.free_left = free_left;
     a.own_len = own_len;
-    a.prefix_pages = prefix_pages;
-    a.ldq_t = ldq_token;
-    a.ldq_h = ldq_head;
-    a.ldo_t = ldo_token;
-    a.ldo_h = ldo_head;
+    a.first = first;
+    a.q_start = q_start;
+    a.slots = slots;
+    a.positions = positions;
     a.ld_pages = ld_pages;
-    a.dtype = dtype;
     a.tokens = static_cast<int>(tokens);
-    a.heads = static_cast<int>(heads);
     a.seqs = static_cast<int>(seqs);
-    a.max_q = static_cast<int>(max_q);
+    a.page_tokens = static_cast<int>(page_tokens);
     a.max_own = static_cast<int>(max_own);
+    a.max_free = static_cast<int>(max_free);
     a.prefix = static_cast<int>(prefix_len);
-    a.scale = scale;
-    a.ws = static_cast<float *>(ws);
     (void)hipGetLastError();
-    return status_of(bl::launch_attention(a, as_stream(stream)));
+    return status_of(bl::launch_cache_assign(a, as_stream(stream)));
+}
+
+int bitlinear_cache_move(const bitlinear_cache_t *cache, const int64_t *src, const int64_t *dst, int64_t groups,
+                         int64_t width, void *stream)
+{
+    bl::CacheView c;
+    CacheSpans cs;
+    const int st = check_cache(cache, &c, &cs);
+    if (st != BITLINEAR_OK) return st;
+    if (groups < 0 || groups > kMaxQueries || width < 1 || width > BITLINEAR_MAX_MOVES) return BITLINEAR_ERR_INVALID_ARG;
+    if (groups == 0) return BITLINEAR_OK;
+    const int64_t n = groups * width;
+    if (!src || !dst || !aligned_to(src, 8) || !aligned_to(dst, 8) || hits(cs, span_of(src, 1, n, n, 8)) ||
+        hits(cs, span_of(dst, 1, n, n, 8)))
+        return BITLINEAR_ERR_INVALID_ARG;
+    (void)hipGetLastError();
+    return status_of(bl::launch_cache_move(c, src, dst, groups, static_cast<int>(width), as_stream(stream)));
 }
 
 } // extern "C"

@@ -91,8 +91,23 @@ inline AttnCut choose_cut(int64_t wgs, int64_t blocks, int rows, int64_t head_di
 // of their own up to about this many bytes (a launch and its join are near 8 us).
 constexpr int64_t kJointBytes = int64_t(16) << 20;
 
+// Blocks of 64 keys that a tile of 'queries' query tokens of one sequence meets at most
+// with a window of 'window' keys and 'sinks' first tokens: those of the first tokens,
+// and a run of window + queries - 1 positions that starts and ends inside blocks and may
+// go from the prefix's last block, partly filled, to the first own one.
+inline int64_t attn_window_blocks(int64_t prefix, int64_t max_own, int64_t queries, int64_t window, int64_t sinks)
+{
+    const int64_t nbp = div_up(prefix, ATTN_BLOCK), nbo = div_up(max_own, ATTN_BLOCK);
+    const int64_t head = sinks <= prefix ? div_up(sinks, ATTN_BLOCK) : nbp + div_up(sinks - prefix, ATTN_BLOCK);
+    return std::min(nbp + nbo, head + div_up(window + queries - 1, ATTN_BLOCK) + 2);
+}
+
+// window > 0: with a sliding window and 'sinks' first tokens.  A sequence's own
+// workgroups then go over what they see of the prefix (its keys lie in at most a window,
+// and in another place for every sequence).
 inline AttnPlan attn_plan(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t seqs,
-                          int64_t max_q, int64_t max_own, int64_t prefix, bool f32)
+                          int64_t max_q, int64_t max_own, int64_t prefix, bool f32, int64_t window = 0,
+                          int64_t sinks = 0)
 {
     AttnPlan p;
     const int64_t G = heads / kv_heads, dp = div_up(head_dim, 16) * 16;
@@ -106,7 +121,7 @@ inline AttnPlan attn_plan(int64_t tokens, int64_t heads, int64_t kv_heads, int64
     // one pass over prefix and own keys where a sequence fills row tiles of its own anyway (4 x 400 query
     // tokens x 8 rows on 2100 keys: 207 us, with a pass of its own for the prefix 222 + 25), or the prefix is
     // short
-    p.joint = nbp > 0 && (max_q * G >= 128 || 2 * prefix * kv_heads * dp * (seqs - 1) <= kJointBytes);
+    p.joint = nbp > 0 && (window > 0 || max_q * G >= 128 || 2 * prefix * kv_heads * dp * (seqs - 1) <= kJointBytes);
     const int64_t tp = p.joint || nbp == 0 ? 0 : div_up(tokens * G, p.rows_prefix);
     // with the same kernel for both, one launch (5 x 8 rows on 60001 keys with 333 of their own: 54 us
     // for both, 52 + 12 one after the other)
@@ -124,7 +139,10 @@ inline AttnPlan attn_plan(int64_t tokens, int64_t heads, int64_t kv_heads, int64
     p.splits_prefix = cut.splits;
     p.waves_prefix = cut.waves;
     p.wgs_prefix = static_cast<int>(tp * kv_heads * p.splits_prefix);
-    cut = choose_cut(busy, p.joint ? nbp + nbo : nbo, p.rows_own, head_dim,
+    const int64_t blocks_own =
+        window > 0 ? attn_window_blocks(prefix, max_own, std::min(max_q, (p.rows_own + G - 2) / G + 1), window, sinks)
+                   : (p.joint ? nbp : 0) + nbo;
+    cut = choose_cut(busy, blocks_own, p.rows_own, head_dim,
                      p.together ? p.waves_prefix : 0, p.together ? p.wgs_prefix : 0, part, tp > 0);
     p.chunk_own = cut.chunk;
     p.splits_own = cut.splits;

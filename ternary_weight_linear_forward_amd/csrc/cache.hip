@@ -201,6 +201,74 @@ __global__ __launch_bounds__(256) void k_cache_read(const CacheView c, const Cac
     }
 }
 
+// Moves of one group (grid x) and head (grid y): every byte and scale is read before
+// the barrier and written after it.  A token's K is one run of bytes; its V is a byte
+// of each of Dp rows of 64, where neighbouring lanes take the group's moves, whose
+// tokens lie in one or two blocks as a rule.  Only a move's own bytes are written: the
+// others of a row may be another group's.  Bound: latency for a few drafts, then the
+// rows of V that single bytes are taken from.
+__global__ __launch_bounds__(256) void k_cache_move(const CacheView c, const int64_t *src, const int64_t *dst, int width)
+{
+    __shared__ int64_t at_src[MAX_MOVES], at_dst[MAX_MOVES]; // rows of the head's K; at_dst -1: no move
+    __shared__ __attribute__((aligned(16))) uint8_t k[MAX_MOVES * 256], v[MAX_MOVES * 256];
+    __shared__ float ks[MAX_MOVES], vs[MAX_MOVES];
+    const int64_t g0 = static_cast<int64_t>(blockIdx.x) * width;
+    const int head = blockIdx.y, tid = threadIdx.x;
+    if (tid < 64) { // (one wave)
+        const int64_t s = tid < width ? src[g0 + tid] : -1, d = tid < width ? dst[g0 + tid] : -1;
+        bool ok = s >= 0 && s < c.slots && d >= 0 && d < c.slots;
+        const int64_t target = ok ? d : -1;
+        for (int x = 1; x < width; ++x) { // a later move to the same slot counts instead
+            const int64_t other = __shfl(target, x);
+            ok = ok && !(x > tid && other == d);
+        }
+        auto row = [&](int64_t slot) {
+            const int64_t page = slot / c.page_tokens;
+            return cache_row0(c, page, head) + (slot - page * c.page_tokens);
+        };
+        const int64_t rs = ok ? row(s) : 0, rd = ok ? row(d) : -1;
+        at_src[tid] = rs;
+        at_dst[tid] = rd;
+        if (ok) {
+            ks[tid] = c.Ks[rs];
+            vs[tid] = c.Vs[rs];
+        }
+    }
+    __syncthreads();
+    const int units = c.Dp / 16;
+    for (int n = tid; n < width * units; n += 256) {
+        const int m = n / units, u = n % units;
+        if (at_dst[m] >= 0)
+            reinterpret_cast<uint4 *>(k)[n] = *reinterpret_cast<const uint4 *>(c.K + at_src[m] * c.Dp + 16 * u);
+    }
+    for (int n = tid; n < width * c.Dp; n += 256) {
+        const int d = n / width, m = n % width;
+        if (at_dst[m] >= 0) v[n] = c.V[v_at(c, at_src[m], d)];
+    }
+    __syncthreads();
+    for (int n = tid; n < width * units; n += 256) {
+        const int m = n / units, u = n % units;
+        if (at_dst[m] >= 0)
+            *reinterpret_cast<uint4 *>(c.K + at_dst[m] * c.Dp + 16 * u) = reinterpret_cast<const uint4 *>(k)[n];
+    }
+    for (int n = tid; n < width * c.Dp; n += 256) {
+        const int d = n / width, m = n % width;
+        if (at_dst[m] >= 0) c.V[v_at(c, at_dst[m], d)] = static_cast<int8_t>(v[n]);
+    }
+    if (tid < width && at_dst[tid] >= 0) {
+        c.Ks[at_dst[tid]] = ks[tid];
+        c.Vs[at_dst[tid]] = vs[tid];
+    }
+}
+
+hipError_t launch_cache_move(const CacheView &c, const int64_t *src, const int64_t *dst, int64_t groups, int width,
+                             hipStream_t stream)
+{
+    hipLaunchKernelGGL(k_cache_move, dim3(static_cast<unsigned>(groups), static_cast<unsigned>(c.heads)), dim3(256), 0,
+                       stream, c, src, dst, width);
+    return hipGetLastError();
+}
+
 // Threads a row (8 columns each).
 template <class F>
 static void by_lanes(int Dp, const F &f)

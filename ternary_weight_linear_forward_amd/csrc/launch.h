@@ -216,6 +216,22 @@ hipError_t launch_cache_write(const CacheView &c, const CacheRows &r, int dtype,
 hipError_t launch_cache_read(const CacheView &c, const CacheRows &r, int dtype, int64_t tokens, const int64_t *slots,
                              hipStream_t stream);
 
+// Moves of groups of 'width' (at most MAX_MOVES) slots.
+constexpr int MAX_MOVES = 64;
+hipError_t launch_cache_move(const CacheView &c, const int64_t *src, const int64_t *dst, int64_t groups, int width,
+                             hipStream_t stream);
+
+// Places of a step's new tokens (assign.hip; names as in bitlinear_cache_assign).
+struct AssignArgs {
+    const int32_t *held, *count, *free_count; // free_count: null for an empty list
+    int32_t *own_pages, *free_pages, *free_left, *own_len, *first, *q_start;
+    int64_t *slots;
+    int32_t *positions; // or null
+    int64_t ld_pages;
+    int tokens, seqs, page_tokens, max_own, max_free, prefix;
+};
+hipError_t launch_cache_assign(const AssignArgs &a, hipStream_t stream);
+
 struct AttnArgs {
     CacheView c;
     const void *Q;
@@ -226,9 +242,16 @@ struct AttnArgs {
     int dtype, tokens, heads, seqs, max_q, max_own, prefix;
     float scale;
     float *ws;
+    int64_t window = 0; // keys of a sliding window, 0: none
+    int sinks = 0;      // and the first tokens that stay visible
+    const uint64_t *tree = nullptr; // who sees which drafted token, rows of ld_tree words, or null
+    int64_t ld_tree = 0;
 };
+// Which keys a row sees: its sequence's first ones, with a window over them, or with
+// a tree over the last.
+enum { ATTN_CAUSAL = 0, ATTN_WINDOW = 1, ATTN_TREE = 2 };
 int64_t attn_workspace_bytes(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t seqs,
-                             int64_t max_q, int64_t max_own, int64_t prefix);
+                             int64_t max_q, int64_t max_own, int64_t prefix, int64_t window = 0, int64_t sinks = 0);
 hipError_t launch_attention(const AttnArgs &a, hipStream_t stream);
 
 // Names (as profilers print them, without the argument list) of the kernel a
