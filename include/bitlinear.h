@@ -718,9 +718,12 @@ int bitlinear_attention_window(const bitlinear_cache_t *cache, const void *Q, in
  *           row; ld_tree >= ceil(min(max_q, tokens) / 64).  Bits n_b and up are ignored.
  *           8-byte aligned.
  * With own_len[b] < n_b the first n_b - own_len[b] query tokens have no key.  The
- * other arguments, their bounds, the workspace (bitlinear_attention_workspace_bytes)
- * and the results are those of bitlinear_attention.
+ * other arguments, their bounds and the results are those of bitlinear_attention, ws
+ * of bitlinear_attention_tree_workspace_bytes bytes.
  */
+int64_t bitlinear_attention_tree_workspace_bytes(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim,
+                                                 int64_t seqs, int64_t max_q, int64_t max_own, int64_t prefix_len);
+
 int bitlinear_attention_tree(const bitlinear_cache_t *cache, const void *Q, int dtype, int64_t tokens, int64_t heads,
                              int64_t ldq_token, int64_t ldq_head, int64_t seqs, const int32_t *q_start, int64_t max_q,
                              const int32_t *own_pages, int64_t ld_pages, const int32_t *own_len, int64_t max_own,

@@ -128,6 +128,7 @@ _SIGNATURES = {
     "bitlinear_attention_window_workspace_bytes": ([_I64] * 10, _I64),
     "bitlinear_attention_window": ([_CACHE, _P, _INT, _I64, _I64, _I64, _I64, _I64, _P, _I64, _P, _I64, _P, _I64, _P,
                                     _I64, _I64, _I64, _F32, _P, _I64, _I64, _P, _P, _I64, _P], _INT),
+    "bitlinear_attention_tree_workspace_bytes": ([_I64] * 8, _I64),
     "bitlinear_attention_tree": ([_CACHE, _P, _INT, _I64, _I64, _I64, _I64, _I64, _P, _I64, _P, _I64, _P, _I64, _P,
                                   _I64, _P, _I64, _F32, _P, _I64, _I64, _P, _P, _I64, _P], _INT),
     "bitlinear_cache_assign": ([_I64, _I64, _P, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _P],
@@ -352,6 +353,10 @@ def bitlinear_attention_window(cache, Q, dtype, tokens, heads, ldq_token, ldq_he
     return _lib.bitlinear_attention_window(cache, Q, dtype, tokens, heads, ldq_token, ldq_head, seqs, q_start, max_q,
                                            own_pages, ld_pages, own_len, max_own, prefix_pages, prefix_len, window,
                                            sinks, scale, O, ldo_token, ldo_head, lse, ws, ws_bytes, stream)
+
+
+def bitlinear_attention_tree_workspace_bytes(tokens, heads, kv_heads, head_dim, seqs, max_q, max_own, prefix_len) -> int:
+    return _lib.bitlinear_attention_tree_workspace_bytes(tokens, heads, kv_heads, head_dim, seqs, max_q, max_own, prefix_len)
 
 
 def bitlinear_attention_tree(cache, Q, dtype, tokens, heads, ldq_token, ldq_head, seqs, q_start, max_q, own_pages,
@@ -977,6 +982,6 @@ def attention_tree(cache: KVCache, Q, own_pages, own_len, max_own: int, tree, pr
     rows, words = tree.shape
     ldt = tree.stride(0) if rows > 1 else words
     _here(name, Q, own_pages, own_len, prefix_pages, q_start, out, ws, tree, cache.k, cache.v, cache.k_scale, cache.v_scale)
-    return _attention(name, _lib.bitlinear_attention_tree, _lib.bitlinear_attention_workspace_bytes, (tree.data_ptr(), ldt),
+    return _attention(name, _lib.bitlinear_attention_tree, _lib.bitlinear_attention_tree_workspace_bytes, (tree.data_ptr(), ldt),
                       cache, Q, own_pages, own_len, max_own, prefix_pages, prefix_len, q_start, max_q, scale, out, return_lse,
                       ws)

@@ -130,7 +130,7 @@ int attention_call(const Sight &sight, const bitlinear_cache_t *cache, const voi
         !rows_ok(tokens, heads, ldo_token, ldo_head, a.c.D, true))
         return BITLINEAR_ERR_INVALID_ARG;
     const int64_t need = bl::attn_workspace_bytes(tokens, heads, a.c.heads, a.c.D, seqs, max_q, max_own, prefix_len, sight.window,
-                                 sight.sinks);
+                                                  sight.sinks, sight.tree != nullptr);
     if (need > 0 && (!ws || ws_bytes < need)) return BITLINEAR_ERR_WORKSPACE;
     if (need > 0 && !aligned16(ws)) return BITLINEAR_ERR_INVALID_ARG;
     const Span so = rows_span(O, tokens, heads, ldo_token, ldo_head, a.c.D, es),
@@ -409,6 +409,13 @@ int bitlinear_attention_window(const bitlinear_cache_t *cache, const void *Q, in
     return attention_call(s, cache, Q, dtype, tokens, heads, ldq_token, ldq_head, seqs, q_start, max_q, own_pages,
                           ld_pages, own_len, max_own, prefix_pages, prefix_len, scale, O, ldo_token, ldo_head, lse, ws,
                           ws_bytes, stream);
+}
+
+int64_t bitlinear_attention_tree_workspace_bytes(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim,
+                                                 int64_t seqs, int64_t max_q, int64_t max_own, int64_t prefix_len)
+{
+    if (!attn_sizes_ok(tokens, heads, kv_heads, head_dim, seqs, max_q, max_own, prefix_len)) return -1;
+    return bl::attn_workspace_bytes(tokens, heads, kv_heads, head_dim, seqs, max_q, max_own, prefix_len, 0, 0, true);
 }
 
 int bitlinear_attention_tree(const bitlinear_cache_t *cache, const void *Q, int dtype, int64_t tokens, int64_t heads,

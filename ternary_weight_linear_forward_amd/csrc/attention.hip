@@ -105,6 +105,23 @@ __global__ __launch_bounds__(256) void k_attn_join(const AttnArgs a, const AttnP
 namespace {
 
 template <int DT>
+hipError_t launch_causal(const AttnArgs &a, AttnPlan pl, int rows, int waves, int64_t first, int64_t wgs, hipStream_t st)
+{
+    if (rows == 16) return launch_attn_stream<DT, ATTN_CAUSAL>(a, pl, waves, first, wgs, st);
+    pl.wg0 = static_cast<int>(first);
+    const dim3 grid(static_cast<unsigned>(wgs)), block(64 * waves);
+#define BL_TILE(DC, NW) hipLaunchKernelGGL((k_attn_tile<DT, DC, NW>), grid, block, 0, st, a, pl)
+    if (a.c.Dp <= 64) {
+        BL_TILE(1, 4);
+    } else if constexpr (DT == DT_BF16) {
+        if (rows == 128) BL_TILE(2, 4);
+        else BL_TILE(2, 8);
+    }
+#undef BL_TILE
+    return hipGetLastError();
+}
+
+template <int DT>
 hipError_t launch_join(const AttnArgs &a, const AttnPlan &pl, hipStream_t st)
 {
     const int64_t rows = attn_join_rows(a.tokens, a.heads, a.seqs, a.max_q);
@@ -128,20 +145,23 @@ hipError_t launch_join(const AttnArgs &a, const AttnPlan &pl, hipStream_t st)
     });
 }
 
-
-// A window over every key there may be is none.
-AttnPlan plan_of(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t seqs, int64_t max_q,
-                 int64_t max_own, int64_t prefix, bool f32, int64_t window, int64_t sinks)
+// How a call sees its keys: a window over every key there may be is none.
+int mask_of(int64_t prefix, int64_t max_own, int64_t window, bool tree)
 {
-    return attn_plan(tokens, heads, kv_heads, head_dim, seqs, max_q, max_own, prefix, f32,
-                     window < prefix + max_own ? window : 0, sinks);
+    return tree ? ATTN_TREE : window > 0 && window < prefix + max_own ? ATTN_WINDOW : ATTN_CAUSAL;
 }
 
 template <int DT>
-hipError_t launch_attn(const AttnArgs &a, const AttnPlan &pl, hipStream_t st)
+hipError_t launch_attn(const AttnArgs &a, hipStream_t st)
 {
-    const int mask = a.tree ? ATTN_TREE : a.window > 0 && a.window < int64_t(a.prefix) + a.max_own ? ATTN_WINDOW : ATTN_CAUSAL;
-    const hipError_t e = mask == ATTN_CAUSAL ? launch_attn_parts<DT, ATTN_CAUSAL>(a, pl, st) : launch_attn_masked(a, pl, mask, st);
+    const int mask = mask_of(a.prefix, a.max_own, a.window, a.tree != nullptr);
+    const AttnPlan pl = attn_plan(a.tokens, a.heads, a.c.heads, a.c.D, a.seqs, a.max_q, a.max_own, a.prefix, DT == DT_F32,
+                                  mask != ATTN_CAUSAL, mask == ATTN_WINDOW ? a.window : 0, a.sinks);
+    const hipError_t e = mask != ATTN_CAUSAL
+                             ? launch_attn_masked(a, pl, mask, st)
+                             : launch_attn_parts(pl, [&](int rows, int waves, int64_t first, int64_t wgs) {
+                                   return launch_causal<DT>(a, pl, rows, waves, first, wgs, st);
+                               });
     return e != hipSuccess || pl.direct ? e : launch_join<DT>(a, pl, st);
 }
 
@@ -149,11 +169,13 @@ hipError_t launch_attn(const AttnArgs &a, const AttnPlan &pl, hipStream_t st)
 
 // Room for either type's plan.
 int64_t attn_workspace_bytes(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t seqs,
-                             int64_t max_q, int64_t max_own, int64_t prefix, int64_t window, int64_t sinks)
+                             int64_t max_q, int64_t max_own, int64_t prefix, int64_t window, int64_t sinks, bool tree)
 {
+    const int mask = mask_of(prefix, max_own, window, tree);
     int64_t most = 0;
     for (const int dtype : {DT_F32, DT_BF16}) {
-        const AttnPlan p = plan_of(tokens, heads, kv_heads, head_dim, seqs, max_q, max_own, prefix, dtype == DT_F32, window, sinks);
+        const AttnPlan p = attn_plan(tokens, heads, kv_heads, head_dim, seqs, max_q, max_own, prefix, dtype == DT_F32,
+                                     mask != ATTN_CAUSAL, mask == ATTN_WINDOW ? window : 0, sinks);
         const int64_t need = p.direct ? 0 : (p.ml_off + 2 * (p.splits_prefix + p.splits_own) * tokens * heads) * 4;
         most = need > most ? need : most;
     }
@@ -162,9 +184,7 @@ int64_t attn_workspace_bytes(int64_t tokens, int64_t heads, int64_t kv_heads, in
 
 hipError_t launch_attention(const AttnArgs &a, hipStream_t stream)
 {
-    const AttnPlan p = plan_of(a.tokens, a.heads, a.c.heads, a.c.D, a.seqs, a.max_q, a.max_own, a.prefix,
-                               a.dtype == DT_F32, a.window, a.sinks);
-    return a.dtype == DT_F32 ? launch_attn<DT_F32>(a, p, stream) : launch_attn<DT_BF16>(a, p, stream);
+    return a.dtype == DT_F32 ? launch_attn<DT_F32>(a, stream) : launch_attn<DT_BF16>(a, stream);
 }
 
 } // namespace bl

@@ -393,6 +393,23 @@ struct RowSight {
     }
 };
 
+// Keys that every row of a tile sees, from its first and last rows.
+template <int MASK>
+struct TileSight {
+    int own, from; // the first 'own' own keys; ATTN_WINDOW: positions from 'from' on
+    __device__ __forceinline__ TileSight(const AttnArgs &a, const AttnJob &j, int G)
+    {
+        own = MASK == ATTN_TREE ? j.own - j.n : attn_own_limit(j.own, j.n, j.row0 / G);
+        from = MASK == ATTN_WINDOW ? window_start(a, attn_own_limit(j.own, j.n, (j.row0 + j.rows - 1) / G)) : 0;
+    }
+    // Whether they see the whole block that starts with key k0 of the prefix (pre) or of the sequence's own.
+    __device__ __forceinline__ bool whole(const AttnArgs &a, const AttnJob &j, bool pre, int k0) const
+    {
+        const int pos = pre ? k0 : j.prefix + k0;
+        return k0 + CACHE_BLOCK <= (pre ? j.prefix : own) && (pos >= from || pos + CACHE_BLOCK <= a.sinks);
+    }
+};
+
 // Workspace: o of every (part, token, head) [Dp], then (m, l) of every one.
 __device__ __forceinline__ int64_t part_index(const AttnArgs &a, int part, int64_t tok, int head)
 {
@@ -870,7 +887,7 @@ __global__ __launch_bounds__(256, DC == 4 ? 1 : 2) void k_attn_stream(const Attn
 // matrix instructions need 2048 and its vector instructions 2500.  One stream that
 // forms the next scores beside the weights, without phases, came to the same (91 us).
 // ---------------------------------------------------------------------------
-template <int DT, int DC, int NW, int MASK>
+template <int DT, int DC, int NW>
 __global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(const AttnArgs a, const AttnPlan pl)
 {
     constexpr int NS = DT == DT_F32 ? 2 : 1;
@@ -887,7 +904,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(const AttnArgs a, cons
     auto v_at = [&](int n) { return smem + 2 * KBYTES + n * VBYTES; };
     auto scales_at = [&](int n) { return reinterpret_cast<float *>(smem + 2 * (KBYTES + VBYTES) + n * 512); };
     AttnJob j;
-    if (!attn_job<MASK>(a, pl, 32 * NW, blockIdx.x + pl.wg0, j)) return;
+    if (!attn_job<ATTN_CAUSAL>(a, pl, 32 * NW, blockIdx.x + pl.wg0, j)) return;
     const int G = a.heads / a.c.heads, lane = lane_id(), wave = wave_id(), i = lane & 31, hf = lane >> 5;
     const int Dp = a.c.Dp, tid = threadIdx.x, rho = 32 * wave + i;
 
@@ -910,8 +927,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(const AttnArgs a, cons
         ksr = load_at<float>(block_scales(a.c.Ks, unit), 4 * lane);
         vsr = load_at<float>(block_scales(a.c.Vs, unit), 4 * lane);
         // (applied where the scales are written: a use here would wait for the loads)
-        const int list = j.at<MASK>(blk);
-        seen = there ? (list < j.nbp ? j.prefix - list * CACHE_BLOCK : j.own - (list - j.nbp) * CACHE_BLOCK) : 0;
+        seen = there ? (blk < j.nbp ? j.prefix - blk * CACHE_BLOCK : j.own - (blk - j.nbp) * CACHE_BLOCK) : 0;
     };
     auto fetch_v = [&](uint32_t unit) {
 #pragma unroll
@@ -922,7 +938,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(const AttnArgs a, cons
     uint32_t unit0 = 0, unit1 = 0;
     bool there0 = false, there1 = false;
     if (j.blk0 < j.blk1) { // (in flight while the queries are read)
-        table.load<MASK>(a, j, j.blk0, 1);
+        table.load<ATTN_CAUSAL>(a, j, j.blk0, 1);
         unit0 = table.at(0);
         there0 = table.there(0);
         fetch_k(j.blk0, unit0, there0);
@@ -968,8 +984,6 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(const AttnArgs a, cons
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) lim_min = min(lim_min, __shfl_xor(lim_min, x));
     lim_min = __builtin_amdgcn_readfirstlane(lim_min);
-    RowSight<MASK> sight;
-    sight.set(a, j, G, rho);
 
     float ref = 0.0f, vscale = 0.0f, grow = 1.0f;
     // Writing the fetched bytes, step by step.  V: unit (2 T + g % 2) * DPAD + d holds
@@ -1077,17 +1091,9 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(const AttnArgs a, cons
     for (int blk = j.blk0; blk < j.blk1; ++blk) {
         const int snext = sbuf == 2 ? 0 : sbuf + 1;
         // this block's list: its first key and those a row sees
-        const int list = j.at<MASK>(blk);
-        const bool pre = list < j.nbp;
-        const int k0 = (pre ? list : list - j.nbp) * CACHE_BLOCK, mine = there0 ? (pre ? j.prefix : lim) : 0;
-        bool masked = !there0 || k0 + CACHE_BLOCK > (pre ? j.prefix : lim_min);
-        uint64_t vis = 0; // (this lane's keys from bit 0 on)
-        if constexpr (MASK != ATTN_CAUSAL) {
-            vis = sight.of(a, j, there0, pre, k0);
-            masked = __any(vis != ~uint64_t(0));
-            vis >>= 4 * hf;
-        }
-        const bool any_seen = MASK == ATTN_CAUSAL ? k0 < mine : vis != 0;
+        const bool pre = blk < j.nbp;
+        const int k0 = (pre ? blk : blk - j.nbp) * CACHE_BLOCK, mine = there0 ? (pre ? j.prefix : lim) : 0;
+        const bool masked = !there0 || k0 + CACHE_BLOCK > (pre ? j.prefix : lim_min);
         // ---- P(blk) ----
         __builtin_amdgcn_s_setprio(2); // (its products go before the other wave's vector instructions)
         pk = reinterpret_cast<const h8 *>(k_at(kbuf));
@@ -1128,7 +1134,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(const AttnArgs a, cons
         if (blk + 1 < j.blk1) fetch_v(unit1);
         if (blk + 2 < j.blk1) {
             const unsigned x = blk + 2 - j.blk0;
-            if (x % 64 == 0) table.load<MASK>(a, j, blk + 2, 1);
+            if (x % 64 == 0) table.load<ATTN_CAUSAL>(a, j, blk + 2, 1);
             unit1 = table.at(x % 64);
             there1 = table.there(x % 64);
             fetch_k(blk + 2, unit1, there1);
@@ -1151,9 +1157,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(const AttnArgs a, cons
 #pragma unroll
                     for (int r = 0; r < 16; ++r) {
                         const int key = k0 + 32 * t + 8 * (r / 4) + 4 * hf + r % 4;
-                        const bool see =
-                            MASK == ATTN_CAUSAL ? key < mine : (vis >> (32 * t + 8 * (r / 4) + r % 4) & 1) != 0;
-                        s[t][r] = see ? s[t][r] : neg_inf();
+                        s[t][r] = key < mine ? s[t][r] : neg_inf();
                     }
             }
             // two keys a step; scales of a quad of keys, 8 x + 4 hf .., are read two quads ahead
@@ -1191,7 +1195,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(const AttnArgs a, cons
                 for (int e = 0; e < 32; ++e)
                     small = score(e / 8, e % 8) > neg_inf() ? fminf(small, static_cast<float>(p[e / 8][0][e % 8])) : small;
             }
-            if (grown != 1.0f || __any(calls_for_general(!set && any_seen, big, sum, small < WR::LEAST))) {
+            if (grown != 1.0f || __any(calls_for_general(!set && k0 < mine, big, sum, small < WR::LEAST))) {
                 // the general form: the references brought to the block's, small weights in rounds
                 int at = hf; // (the scales are read again, not kept)
                 asm volatile("" : "+v"(at));
@@ -1333,38 +1337,29 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(const AttnArgs a, cons
 
 // ---- host -------------------------------------------------------------------
 template <int DT, int MASK>
-hipError_t launch_attn_piece(const AttnArgs &a, AttnPlan pl, int rows, int waves, int64_t first, int64_t wgs, hipStream_t st)
+hipError_t launch_attn_stream(const AttnArgs &a, AttnPlan pl, int waves, int64_t first, int64_t wgs, hipStream_t st)
 {
     pl.wg0 = static_cast<int>(first);
     const int dc = a.c.Dp <= 64 ? 1 : a.c.Dp <= 128 ? 2 : 4;
     const dim3 grid(static_cast<unsigned>(wgs)), block(64 * waves);
     const size_t lds = (waves * 16 * (64 * dc + 2) + 16) * sizeof(float);
 #define BL_STREAM(DC) hipLaunchKernelGGL((k_attn_stream<DT, DC, MASK>), grid, block, lds, st, a, pl)
-#define BL_TILE(DC, NW) hipLaunchKernelGGL((k_attn_tile<DT, DC, NW, MASK>), grid, block, 0, st, a, pl)
-    if (rows == 16) {
-        if (dc == 1) BL_STREAM(1);
-        else if (dc == 2) BL_STREAM(2);
-        else BL_STREAM(4);
-    } else if (dc == 1) {
-        BL_TILE(1, 4);
-    } else if constexpr (DT == DT_BF16) {
-        if (rows == 128) BL_TILE(2, 4);
-        else BL_TILE(2, 8);
-    }
+    if (dc == 1) BL_STREAM(1);
+    else if (dc == 2) BL_STREAM(2);
+    else BL_STREAM(4);
 #undef BL_STREAM
-#undef BL_TILE
     return hipGetLastError();
 }
 
-// The launches of a plan's parts.
-template <int DT, int MASK>
-hipError_t launch_attn_parts(const AttnArgs &a, const AttnPlan &pl, hipStream_t st)
+// The launches of a plan's parts, piece by piece: piece(rows, waves, first workgroup, workgroups).
+template <class F>
+hipError_t launch_attn_parts(const AttnPlan &pl, const F &piece)
 {
     AttnLaunch l[2];
     const int n = attn_launches(pl, l);
     for (int x = 0; x < n; ++x) {
         const hipError_t e = attn_pieces(l[x].wgs, hipSuccess, [&](int64_t at, int64_t wgs) {
-            return launch_attn_piece<DT, MASK>(a, pl, l[x].rows, l[x].waves, l[x].first + at, wgs, st);
+            return piece(l[x].rows, l[x].waves, l[x].first + at, wgs);
         });
         if (e != hipSuccess) return e;
     }

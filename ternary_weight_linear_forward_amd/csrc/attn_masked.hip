@@ -1,16 +1,675 @@
-// attn_masked.hip -- the kernels of attn_core.h for rows that do not see a
+// attn_masked.hip -- attention over the int8 cache for rows that do not see a
 // sequence's first keys: a sliding window with a few first tokens, a tree of drafts.
+// Few rows take k_attn_stream (attn_core.h), many k_attn_rows.
 #include "attn_core.h"
 
+#include <utility>
+
 namespace bl {
+
+// ---------------------------------------------------------------------------
+// Many rows: k_attn_rows.  A workgroup of four waves takes 128 RT rows (a wave RT
+// tiles of 32) and a chunk of keys, in halves of 32 keys of a block.  S^T = K Q^T in
+// 32 x 32 tiles leaves a lane (row = lane % 32, hf = lane / 32) keys 8 x + 4 hf + {0..3},
+// the operand order of O^T += V^T P^T: weights never leave their lane.
+//
+// A step is one half of a block.  Its products belong to the halves around it (values
+// of the half before, scores of the half after), its vector instructions are the
+// weights of its own, so that both have no need of each other and go out in turns: two
+// weights behind every operand.  One barrier a step; K lies in LDS by halves, V by
+// blocks, two of each.
+//
+// The first product is bf16 for bf16 queries, which takes the queries as they are and
+// the bytes exactly, and binary16 in two terms for fp32 queries (brought into its range
+// by a power of two per row).  Weights are w = 2^(x - M) V_scale, M a reference in base 2
+// that a row gets with its first keys (the first 32 of which it sees some) and keeps, so
+// that sums are never brought to another one:
+//  - fp32 queries: three bf16 terms, 24 bits, in binary32's range; M is the largest x.
+//  - bf16 queries: one binary16 term, 11 bits.  M brings the largest of the first weights
+//    to 2^FIRST_TOP: later ones may be 2^14 times as large; those that are 2^16 times
+//    smaller lose bits, all below 2^-27 of it are lost.
+// A row whose later scores pass what that leaves (its sum passes 2^60, or a weight
+// binary16: then its sums are not finite) asks for more: its workgroup finds every row's
+// largest weight first and starts again.
+// ---------------------------------------------------------------------------
+typedef __bf16 b8 __attribute__((ext_vector_type(8)));
+constexpr float ROWS_SUM_MAX = 0x1p60f;
+// log2 of what a row's reference makes of the largest of its first weights (one binary16
+// term), and of all of them (a second pass)
+constexpr float FIRST_TOP = 2.0f, LAST_TOP = 13.0f;
+
+// Eight int8 (two words) to bf16, exactly, by way of binary32.
+__device__ __forceinline__ u4 bytes_to_b8(uint32_t a, uint32_t b)
+{
+    u4 r;
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+        const uint32_t w = h < 2 ? a : b;
+        const float lo = static_cast<float>(static_cast<int8_t>(w >> (16 * (h % 2))));
+        const float hi = static_cast<float>(static_cast<int8_t>(w >> (16 * (h % 2) + 8)));
+        r[h] = __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
+    }
+    return r;
+}
+
+// Two weights as operands of the second product: one binary16 term, or three bf16 ones,
+// the last rounded to nearest, those before cut (what is cut off is exact in binary32).
+template <int DT, int NT>
+__device__ __forceinline__ void weight_terms(float w0, float w1, uint32_t (&p)[NT])
+{
+    if constexpr (DT == DT_BF16) {
+        const h2 r = {static_cast<_Float16>(w0), static_cast<_Float16>(w1)};
+        p[0] = __builtin_bit_cast(uint32_t, r);
+    } else {
+        typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+        for (int z = 0; z < NT; ++z) {
+            if (z == NT - 1) {
+                const b2 r = {static_cast<__bf16>(w0), static_cast<__bf16>(w1)};
+                p[z] = __builtin_bit_cast(uint32_t, r);
+            } else {
+                p[z] = __builtin_amdgcn_perm(__float_as_uint(w1), __float_as_uint(w0), 0x07060302u);
+                w0 -= __uint_as_float(__float_as_uint(w0) & 0xffff0000u);
+                w1 -= __uint_as_float(__float_as_uint(w1) & 0xffff0000u);
+            }
+        }
+    }
+}
+
+// Operand of the first product: bytes of K, and the queries.
+template <int DT>
+__device__ __forceinline__ u4 key_operand(uint32_t a, uint32_t b)
+{
+    if constexpr (DT == DT_BF16) return bytes_to_b8(a, b);
+    else return __builtin_bit_cast(u4, bytes_to_h8(a, b));
+}
+template <int DT>
+__device__ __forceinline__ f16v score_product(u4 k, u4 q, f16v s)
+{
+    if constexpr (DT == DT_BF16)
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(b8, k), __builtin_bit_cast(b8, q), s, 0, 0, 0);
+    else return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8, k), __builtin_bit_cast(h8, q), s, 0, 0, 0);
+}
+
+// The second product's: bytes of V, and the weights.
+template <int DT>
+__device__ __forceinline__ u4 value_operand(uint32_t a, uint32_t b)
+{
+    if constexpr (DT == DT_BF16) return __builtin_bit_cast(u4, bytes_to_h8(a, b));
+    else return bytes_to_b8(a, b);
+}
+template <int DT>
+__device__ __forceinline__ f16v value_product(u4 v, u4 p, f16v o)
+{
+    if constexpr (DT == DT_BF16)
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8, v), __builtin_bit_cast(h8, p), o, 0, 0, 0);
+    else return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(b8, v), __builtin_bit_cast(b8, p), o, 0, 0, 0);
+}
+
+// A value that the matrix instructions alone use, in accumulation registers; one that
+// vector instructions use, in theirs (and formed here, not where it is used).
+template <class T>
+__device__ __forceinline__ void to_matrix(T &v)
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+    asm volatile("" : "+a"(v));
+#endif
+}
+template <class T>
+__device__ __forceinline__ void to_vector(T &v)
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+    asm volatile("" : "+v"(v));
+#endif
+}
+
+// f(0), f(1), .. f(N - 1) as constants.
+template <class F, int... I>
+__device__ __forceinline__ void in_turn(const F &f, std::integer_sequence<int, I...>)
+{
+    (f(std::integral_constant<int, I>()), ...);
+}
+template <int N, class F>
+__device__ __forceinline__ void in_turn(const F &f)
+{
+    in_turn(f, std::make_integer_sequence<int, N>());
+}
+
+// Waves of a SIMD: two where their registers (256 a lane) hold sums, scores, queries and weights.
+constexpr int rows_waves(int dt, int dc, int rt) { return dt == DT_BF16 && dc * rt <= 2 ? 2 : 1; }
+
+template <int DT, int DC, int RT, int MASK>
+__global__ __launch_bounds__(256, rows_waves(DT, DC, RT)) void k_attn_rows(const AttnArgs a, const AttnPlan pl)
+{
+    constexpr int NS = DT == DT_F32 ? 2 : 1, NT = DT == DT_F32 ? 3 : 1; // terms of queries and of weights
+    constexpr int DPAD = 64 * DC, KSTEPS = DPAD / 16, DT32 = DPAD / 32;
+    // 16-byte units of half a block of K, and of a block of V, of a thread
+    constexpr int KU = DC < 2 ? 1 : DC / 2, VU = DC;
+    // K in LDS: 16-byte unit of 8 columns c8 of a key at ((c8 / 2 + KSTEPS (c8 % 2)) KROW + key), as in k_attn_tile
+    constexpr int KROW = 33, KBYTES = 2 * KSTEPS * KROW * 16, VBYTES = 64 * DPAD * 2;
+    // two blocks of K (four halves), of V and of scales
+    __shared__ __attribute__((aligned(16))) uint8_t smem[4 * KBYTES + 2 * VBYTES + 2 * 512];
+    auto k_at = [&](int n, int half) { return smem + (2 * (n & 1) + half) * KBYTES; };
+    auto v_at = [&](int n) { return smem + 4 * KBYTES + (n & 1) * VBYTES; };
+    auto scales_at = [&](int n) { return reinterpret_cast<float *>(smem + 4 * KBYTES + 2 * VBYTES + (n & 1) * 512); };
+    AttnJob j;
+    if (!attn_job<MASK>(a, pl, 128 * RT, blockIdx.x + pl.wg0, j)) return;
+    const int G = a.heads / a.c.heads, lane = lane_id(), wave = wave_id(), i = lane & 31, hf = lane >> 5;
+    const int Dp = a.c.Dp, tid = threadIdx.x, nblk = j.blk1 - j.blk0;
+
+    // this thread's bytes of a half of K and of a block of V; columns past Dp read the row's start (the queries
+    // hold zeros there), V's rows past Dp its first rows (their sums are not stored)
+    const bool k_mine = DC >= 2 || tid < 128; // (half a block of K is 128 units of 64 columns)
+    u4 kreg[2][KU] = {};
+    uint2 vreg[2][VU] = {}; // (a block's row of V has 8 bytes of either half in 16)
+    uint32_t koff[KU], voff[VU];
+#pragma unroll
+    for (int u = 0; u < KU; ++u) {
+        const int id = tid + 256 * u, col = 16 * (id % (4 * DC));
+        koff[u] = (k_mine ? id / (4 * DC) : 0) * Dp + (col < Dp ? col : 0);
+    }
+#pragma unroll
+    for (int u = 0; u < VU; ++u) {
+        const int id = tid + 256 * u;
+        voff[u] = (id / 4 < Dp ? id : id % 4) * 16;
+    }
+    float ksr = 0.0f, vsr = 0.0f;
+    auto fetch_k = [&](int half, int u, uint32_t unit) {
+        kreg[half][u] = load_at<u4>(block_bytes(a.c.K, unit, Dp) + 32 * half * Dp, koff[u]);
+    };
+    auto fetch_v = [&](int half, int u, uint32_t unit) {
+        vreg[half][u] = load_at<uint2>(block_bytes(a.c.V, unit, Dp) + 8 * half, voff[u]);
+    };
+    auto fetch_scales = [&](uint32_t unit) {
+        ksr = load_at<float>(block_scales(a.c.Ks, unit), 4 * lane);
+        vsr = load_at<float>(block_scales(a.c.Vs, unit), 4 * lane);
+    };
+    BlockTable table;
+    uint32_t unit1 = 0, unit2 = 0, unit3 = 0; // places of the next three blocks (of some block, past the last)
+    bool there0 = false, there1 = false, there2 = false, there3 = false;
+    // the place of block n, which follows the ones before
+    auto look_up = [&](int n, uint32_t &unit, bool &there) {
+        there = false;
+        if (n >= nblk) return;
+        if (n % 64 == 0) table.load<MASK>(a, j, j.blk0 + n, 1);
+        unit = table.at(n % 64);
+        there = table.there(n % 64);
+    };
+    // block 0, and the first half of block 1's keys
+    u4 kfirst[KU] = {};
+    auto first_loads = [&]() {
+        uint32_t unit0 = 0;
+        look_up(0, unit0, there0);
+        unit1 = unit0;
+        look_up(1, unit1, there1);
+        unit2 = unit1;
+        look_up(2, unit2, there2);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int u = 0; u < KU; ++u) fetch_k(h, u, unit0);
+#pragma unroll
+            for (int u = 0; u < VU; ++u) fetch_v(h, u, unit0);
+        }
+        fetch_scales(unit0);
+#pragma unroll
+        for (int u = 0; u < KU; ++u) kfirst[u] = load_at<u4>(block_bytes(a.c.K, unit1, Dp), koff[u]);
+    };
+    if (nblk > 0) first_loads(); // (in flight while the queries are read)
+
+    // Queries: operands, and a row's factor from scores to base 2 (fp32: of its own power of two).
+    u4 q[RT][KSTEPS][NS];
+    float c[RT];
+    RowSight<MASK> sight[RT];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+        const int rho = 32 * (RT * wave + t) + i, rr = j.row0 + (rho < j.rows ? rho : 0);
+        const int64_t off = (j.tok0 + static_cast<int64_t>(rr / G)) * a.ldq_t + (j.kvh * G + rr % G) * a.ldq_h;
+        sight[t].set(a, j, G, rho);
+        float v[KSTEPS][8];
+        load_queries<DT>(a, off, [&](int n) { return 16 * n + 8 * hf; }, v);
+        if constexpr (DT == DT_BF16) {
+            c[t] = row_factor(a.scale, 0);
+            const uint32_t sign = a.scale < 0.0f ? 0x80008000u : 0u, keep = a.scale == 0.0f ? 0u : ~0u;
+#pragma unroll
+            for (int k = 0; k < KSTEPS; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    q[t][k][0][e] = (__builtin_amdgcn_perm(__float_as_uint(v[k][2 * e + 1]), __float_as_uint(v[k][2 * e]),
+                                                           0x07060302u) ^ sign) & keep;
+        } else {
+            float top = 0.0f;
+#pragma unroll
+            for (int k = 0; k < KSTEPS; ++k) top = fmaxf(top, max_abs8(v[k]));
+            top = max_across32(top);
+            const int e2 = row_exponent(top < __builtin_inff() ? top : 0.0f);
+#pragma unroll
+            for (int k = 0; k < KSTEPS; ++k) {
+                h8 terms[NS];
+                query_terms<NS>(v[k], e2, a.scale, terms);
+#pragma unroll
+                for (int z = 0; z < NS; ++z) q[t][k][z] = __builtin_bit_cast(u4, terms[z]);
+            }
+            c[t] = row_factor(a.scale, e2);
+        }
+    }
+
+    // (the queries are operands only: in accumulation registers they leave the others to the vector instructions)
+    if constexpr (rows_waves(DT, DC, RT) == 1) {
+#pragma unroll
+        for (int t = 0; t < RT; ++t)
+#pragma unroll
+            for (int k = 0; k < KSTEPS; ++k)
+#pragma unroll
+                for (int z = 0; z < NS; ++z) to_matrix(q[t][k][z]);
+    }
+    auto stage_k = [&](const u4 &from, int u, int part, uint8_t *to) {
+        const int id = tid + 256 * u, key = id / (4 * DC), cu = id % (4 * DC);
+        if (k_mine)
+            reinterpret_cast<u4 *>(to)[(cu + KSTEPS * part) * KROW + key] = key_operand<DT>(from[2 * part], from[2 * part + 1]);
+    };
+    // V: unit (2 T + g % 2) * DPAD + d holds quads g and g + 2 of 16-key tile T; a half is two tiles.
+    auto stage_v = [&](int half, int u, uint8_t *to) {
+        const int id = tid + 256 * u, d = id / 4, g = id % 4;
+        uint2 *pv = reinterpret_cast<uint2 *>(to);
+        const u4 x = value_operand<DT>(vreg[half][u].x, vreg[half][u].y);
+        pv[((4 * half + (g & 1)) * DPAD + d) * 2 + (g >> 1)] = make_uint2(x[0], x[1]);
+        pv[((4 * half + 2 + (g & 1)) * DPAD + d) * 2 + (g >> 1)] = make_uint2(x[2], x[3]);
+    };
+    // (a hidden score is -inf: never times 0.  A V_scale that is not finite counts as the largest number: its key's
+    // weight overflows where a row sees it and is 0 where it is hidden)
+    auto stage_scales = [&](float *to) {
+        if (wave == 0) {
+            to[lane] = fmaxf(DT == DT_BF16 ? ksr * c[0] : ksr, 1.17549435e-38f);
+            to[64 + lane] = fminf(vsr, 3.402823466e38f);
+        }
+    };
+
+    f16v o[RT][DT32], s[2][RT]; // sums; scores of the two halves
+    u4 p[2][RT][2][NT];         // weights of the two halves, by 16-key tile
+    float M[RT], l[RT];
+    bool set[RT], settled = false; // a row's reference, all of the wave's
+    uint64_t vis[RT];              // keys of the block the row sees
+    bool hidden = false;           // the rows do not all see all of it
+    // K_scales (V_scales) of keys 8 x + 4 hf .. of a half
+    auto key_scales = [&](int n, int half, int x) { return reinterpret_cast<const f4 *>(scales_at(n))[8 * half + 2 * x + hf]; };
+    auto value_scales = [&](int n, int half, int x) {
+        return reinterpret_cast<const f4 *>(scales_at(n))[16 + 8 * half + 2 * x + hf];
+    };
+    // Which keys of block n the rows see.  A block that every row of the tile sees whole is told from the tile's bounds
+    // alone.
+    const TileSight<MASK> tile(a, j, G);
+    auto look = [&](int n, bool there) {
+        const int list = j.at<MASK>(j.blk0 + n);
+        const bool pre = list < j.nbp;
+        const int k0 = (pre ? list : list - j.nbp) * CACHE_BLOCK;
+        hidden = !there || !tile.whole(a, j, pre, k0);
+#pragma unroll
+        for (int t = 0; t < RT; ++t) vis[t] = hidden ? sight[t].of(a, j, there, pre, k0) : ~uint64_t(0);
+    };
+    // The scores of a half that a row does not see.
+    auto hide = [&](int half, f16v &sc, int t) {
+        const uint32_t mine = static_cast<uint32_t>(vis[t] >> (32 * half)) >> (4 * hf);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) sc[r] = mine >> (8 * (r / 4) + r % 4) & 1 ? sc[r] : neg_inf();
+    };
+    // The largest exponent x of a half's scores, and of x + log2 V_scale, that of the weights.
+    auto meet = [&](int n, int half, const f16v &sc, int t, float &top, float &most) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const f4 kq = key_scales(n, half, x), vq = value_scales(n, half, x);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float y = sc[4 * x + e], z = (DT == DT_BF16 ? y : y * c[t]) * kq[e];
+                top = fmaxf(top, z);
+                if constexpr (DT == DT_BF16) most = fmaxf(most, z + __builtin_log2f(vq[e])); // (-inf for a zero scale)
+            }
+        }
+    };
+    // The reference of a row that has none.  The largest weight comes to 2^room where it is binary16; sums of p stay in
+    // range where values are very small.  bf16 terms need no more than that of p.
+    auto first_reference = [&](int t, float top, float most, float room) {
+        top = max_across32(top);
+        float m = top;
+        if constexpr (DT == DT_BF16) {
+            most = max_across32(most);
+            m = most > neg_inf() ? fmaxf(most - room, top - 40.0f) : top;
+        }
+        const bool now = !set[t] && top > neg_inf();
+        M[t] = now ? m : M[t];
+        set[t] = set[t] || now;
+    };
+    // Before a half's weights: scores a row does not see, and the reference of a row whose first keys these are (its
+    // sums are still zero).
+    auto prepare = [&](auto half_c, int n) {
+        constexpr int H = decltype(half_c)::value;
+        if (hidden) {
+#pragma unroll
+            for (int t = 0; t < RT; ++t) hide(H, s[H][t], t);
+        }
+        if (settled) return;
+        bool unset = false;
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+            float top = neg_inf(), most = neg_inf();
+            meet(n, H, s[H][t], t, top, most);
+            first_reference(t, top, most, FIRST_TOP);
+            unset |= !set[t];
+        }
+        settled = !__any(unset);
+    };
+
+    // Sums stay in accumulation registers and scores in the others; without a word the compiler carries them to and fro
+    // (64 moves a step).
+    auto place = [&](int half) {
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+            to_vector(s[half][t]);
+            if constexpr (rows_waves(DT, DC, RT) == 1) {
+#pragma unroll
+                for (int d = 0; d < DT32; ++d) to_matrix(o[t][d]);
+            }
+        }
+    };
+
+    // One block: for each half its weights, beside the products of the halves around it.  What a block stages is read
+    // after its barrier: keys from the second half of the next block to the first of the one after, values up to the
+    // first half of the next.  A register is loaded again as soon as it is staged, a block ahead of its use.
+    constexpr int OPS = 4 * DC, PAIRS = 8 * RT, AHEAD = rows_waves(DT, DC, RT) == 2 ? 2 : 3; // operands of either product; pairs of weights
+    constexpr int PER = RT * (NT + NS), PRODUCTS = OPS * PER, PARTS = 3 * PAIRS, STAGE = 4 * KU + 2 * VU + 1;
+    u4 rk[AHEAD], rv[AHEAD];
+    f4 kq[2], vq[2];
+    auto read_ops = [&](int n, int y) { // operand y % OPS of half y / OPS
+        if (y >= 2 * OPS) return;
+        const int half = y / OPS, x = y % OPS;
+        const u4 *pv = reinterpret_cast<const u4 *>(v_at(half == 0 ? n - 1 : n));
+        const u4 *pk = reinterpret_cast<const u4 *>(half == 0 ? k_at(n, 1) : k_at(n + 1, 0));
+        rv[y % AHEAD] = pv[(2 * (x / DT32 + 2 * (1 - half)) + hf) * DPAD + 32 * (x % DT32) + i];
+        rk[y % AHEAD] = pk[(x + KSTEPS * hf) * KROW + i];
+    };
+    auto read_scales = [&](int n, int x) { // quad x % 4 of half x / 4
+        if (x >= 8) return;
+        kq[x % 2] = key_scales(n, x / 4, x % 4);
+        vq[x % 2] = value_scales(n, x / 4, x % 4);
+    };
+    auto stage = [&](int n, int x) {
+        if (x < 4 * KU) { // second half of the next block's keys, first of the one after
+            const int half = x < 2 * KU ? 1 : 0, u = x / 2 % KU, part = x % 2;
+            stage_k(kreg[half][u], u, part, half ? k_at(n + 1, 1) : k_at(n + 2, 0));
+            if (part == 1) fetch_k(half, u, half ? unit2 : unit3);
+        } else if (x < 4 * KU + 2 * VU) { // second half of this block's values, first of the next
+            const int half = x < 4 * KU + VU ? 1 : 0, u = (x - 4 * KU) % VU;
+            stage_v(half, u, half ? v_at(n) : v_at(n + 1));
+            fetch_v(half, u, half ? unit1 : unit2);
+        } else {
+            stage_scales(scales_at(n + 1));
+            fetch_scales(unit2);
+        }
+    };
+    auto half_block = [&](auto half_c, int n) {
+        constexpr int H = decltype(half_c)::value;
+        if (__builtin_expect_with_probability(hidden || !settled, 0, 0.9)) prepare(half_c, n);
+        float sum[RT][2];
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+            to_vector(s[H][t]);
+            sum[t][0] = sum[t][1] = 0.0f;
+        }
+        // the weights of a pair of keys in three parts; pairs by quads of keys
+        float g[2];
+        auto weights = [&](int y) {
+            const int x = y / 3, part = y % 3, quad = x / (2 * RT), t = x / 2 % RT, e = 2 * (x % 2), r0 = 4 * quad + e;
+            if (x % (2 * RT) == 0 && part == 0) read_scales(n, 4 * H + quad + 1);
+            if (part < 2) {
+                const float v = DT == DT_BF16 ? s[H][t][r0 + part] : s[H][t][r0 + part] * c[t];
+                g[part] = __builtin_amdgcn_exp2f(__builtin_fmaf(v, kq[quad % 2][e + part], -M[t]));
+                sum[t][part] += g[part];
+                pin(sum[t][part]);
+            } else {
+                uint32_t terms[NT];
+                weight_terms<DT, NT>(g[0] * vq[quad % 2][e], g[1] * vq[quad % 2][e + 1], terms);
+#pragma unroll
+                for (int z = 0; z < NT; ++z) {
+                    to_vector(terms[z]);
+                    p[H][t][r0 / 8][z][r0 / 2 % 4] = terms[z];
+                }
+            }
+        };
+        // Product m: operand x of both products in turn, value products (32 columns of 16 keys of the half before) and
+        // score products (16 columns of the half after) one after the other, so that neither waits for its own last one.
+        static_assert(NS <= NT, "scores have no more products than values");
+        auto product = [&](int m) {
+            const int x = m / PER, y = m % PER, ring = (OPS * H + x) % AHEAD;
+            constexpr int BOTH = RT * NS;
+            const bool score = y < 2 * BOTH && y % 2 == 1; // (v s v s .., then the rest of v)
+            const int k = y < 2 * BOTH ? y / 2 : y - BOTH, t = k % RT, z = k / RT;
+            if (!score) {
+                o[t][x % DT32] = value_product<DT>(rv[ring], p[1 - H][t][x / DT32][z], o[t][x % DT32]);
+            } else if (x == 0 && z == 0) {
+                f16v zero;
+#pragma unroll
+                for (int r = 0; r < 16; ++r) zero[r] = 0.0f;
+                s[1 - H][t] = score_product<DT>(rk[ring], q[t][x][z], zero);
+            } else {
+                s[1 - H][t] = score_product<DT>(rk[ring], q[t][x][z], s[1 - H][t]);
+            }
+        };
+        // A wave issues in order: a second product right behind the first waits for it, and the vector instructions
+        // behind both wait too.  So every product has its share of them right after it.
+        __builtin_amdgcn_sched_barrier(0);
+        weights(0);
+        in_turn<PRODUCTS>([&](auto m_c) __attribute__((always_inline)) {
+            constexpr int m = decltype(m_c)::value, all = H * PRODUCTS + m;
+            __builtin_amdgcn_sched_barrier(0);
+            product(m);
+            if constexpr (m % PER == PER - 1) read_ops(n, OPS * H + m / PER + AHEAD);
+            in_turn<(m + 1) * PARTS / PRODUCTS - m * PARTS / PRODUCTS>([&](auto y) __attribute__((always_inline)) {
+                constexpr int part = m * PARTS / PRODUCTS + decltype(y)::value + 1;
+                if constexpr (part < PARTS) weights(part);
+            });
+            in_turn<(all + 1) * STAGE / (2 * PRODUCTS) - all * STAGE / (2 * PRODUCTS)>([&](auto y) __attribute__((always_inline)) {
+                stage(n, all * STAGE / (2 * PRODUCTS) + decltype(y)::value);
+            });
+        });
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int t = 0; t < RT; ++t) l[t] += sum[t][0] + sum[t][1];
+        place(1 - H);
+    };
+
+    // Every row's reference from all of its keys: for a second pass, where one has outgrown its first ones'.
+    auto all_references = [&]() {
+        float tops[RT], mosts[RT];
+#pragma unroll
+        for (int t = 0; t < RT; ++t) tops[t] = mosts[t] = neg_inf();
+        for (int n = 0; n < nblk; ++n) {
+            look_up(n, unit1, there1);
+            look(n, there1);
+#pragma unroll
+            for (int u = 0; u < KU; ++u) {
+                fetch_k(0, u, unit1);
+                fetch_k(1, u, unit1);
+            }
+            fetch_scales(unit1);
+            __syncthreads();
+#pragma unroll
+            for (int x = 0; x < 4 * KU; ++x) stage_k(kreg[x / 2 / KU][x / 2 % KU], x / 2 % KU, x % 2, k_at(0, x / 2 / KU));
+            stage_scales(scales_at(0));
+            __syncthreads();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const u4 *pk = reinterpret_cast<const u4 *>(k_at(0, h));
+#pragma unroll
+                for (int t = 0; t < RT; ++t) {
+                    f16v sc;
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) sc[r] = 0.0f;
+#pragma unroll
+                    for (int x = 0; x < KSTEPS; ++x)
+#pragma unroll
+                        for (int z = 0; z < NS; ++z) sc = score_product<DT>(pk[(x + KSTEPS * hf) * KROW + i], q[t][x][z], sc);
+                    hide(h, sc, t);
+                    meet(0, h, sc, t, tops[t], mosts[t]);
+                }
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < RT; ++t) first_reference(t, tops[t], mosts[t], LAST_TOP);
+        __syncthreads();
+        if (nblk > 0) first_loads();
+    };
+
+    for (int pass = 0;; ++pass) {
+        settled = false;
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+            M[t] = l[t] = 0.0f;
+            set[t] = false;
+            vis[t] = 0;
+        }
+        if (pass > 0) all_references();
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+#pragma unroll
+            for (int d = 0; d < DT32; ++d)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) o[t][d][r] = 0.0f;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) s[h][t][r] = 0.0f;
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int z = 0; z < NT; ++z) p[0][t][x][z] = p[1][t][x][z] = u4{0, 0, 0, 0};
+        }
+        if (nblk > 0) {
+#pragma unroll
+            for (int x = 0; x < 4 * KU; ++x) stage_k(kreg[x / 2 / KU][x / 2 % KU], x / 2 % KU, x % 2, k_at(0, x / 2 / KU));
+#pragma unroll
+            for (int x = 0; x < 2 * KU; ++x) stage_k(kfirst[x / 2], x / 2, x % 2, k_at(1, 0));
+#pragma unroll
+            for (int u = 0; u < VU; ++u) stage_v(0, u, v_at(0));
+            stage_scales(scales_at(0));
+            // (the first half adds zero weights of a block that is not there: its V must be finite)
+            for (int x = tid; x < VBYTES / 32; x += 256) reinterpret_cast<u4 *>(v_at(1) + VBYTES / 2)[x] = u4{0, 0, 0, 0};
+#pragma unroll
+            for (int u = 0; u < KU; ++u) {
+                fetch_k(1, u, unit1);
+                fetch_k(0, u, unit2);
+            }
+#pragma unroll
+            for (int u = 0; u < VU; ++u) fetch_v(0, u, unit1); // (vreg[1] holds block 0's second half)
+            fetch_scales(unit1);
+            __syncthreads();
+            // scores of the first half
+            const u4 *pk = reinterpret_cast<const u4 *>(k_at(0, 0));
+#pragma unroll
+            for (int x = 0; x < OPS; ++x) {
+                const u4 k = pk[(x + KSTEPS * hf) * KROW + i];
+#pragma unroll
+                for (int t = 0; t < RT; ++t)
+#pragma unroll
+                    for (int z = 0; z < NS; ++z) s[0][t] = score_product<DT>(k, q[t][x][z], s[0][t]);
+            }
+            __syncthreads();
+        }
+        place(0);
+        for (int n = 0; n < nblk; ++n) {
+#pragma unroll
+            for (int x = 0; x < AHEAD; ++x) read_ops(n, x);
+            read_scales(n, 0);
+            look(n, there0);
+            unit3 = unit2;
+            look_up(n + 3, unit3, there3);
+            half_block(std::integral_constant<int, 0>(), n);
+            half_block(std::integral_constant<int, 1>(), n);
+            there0 = there1;
+            there1 = there2;
+            there2 = there3;
+            unit1 = unit2;
+            unit2 = unit3;
+            __syncthreads();
+        }
+        if (nblk > 0) { // values of the last half
+            const u4 *pv = reinterpret_cast<const u4 *>(v_at(nblk - 1));
+#pragma unroll
+            for (int x = 0; x < OPS; ++x) {
+                const u4 v = pv[(2 * (x / DT32 + 2) + hf) * DPAD + 32 * (x % DT32) + i];
+#pragma unroll
+                for (int t = 0; t < RT; ++t)
+#pragma unroll
+                    for (int z = 0; z < NT; ++z) o[t][x % DT32] = value_product<DT>(v, p[1][t][x / DT32][z], o[t][x % DT32]);
+            }
+        }
+        bool outgrown = false;
+#pragma unroll
+        for (int t = 0; t < RT; ++t) outgrown |= !(l[t] <= ROWS_SUM_MAX) | !(fabsf(o[t][0][0]) < __builtin_inff());
+        if (!__syncthreads_or(outgrown) || pass > 0) break;
+    }
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+        const float sum = sum_across32(l[t]);
+        const int rho = 32 * (RT * wave + t) + i;
+        if (rho >= j.rows) continue;
+        const int rr = j.row0 + rho, head = j.kvh * G + rr % G;
+        const int64_t tok = j.tok0 + rr / G, at = part_index(a, j.part, tok, head);
+        f4 *po = reinterpret_cast<f4 *>(a.ws) + at * (Dp / 4);
+        const float f = !pl.direct ? 1.0f : (sum > 0.0f ? 1.0f / sum : 0.0f);
+#pragma unroll
+        for (int d = 0; d < DT32; ++d)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const int col = 32 * d + 8 * x + 4 * hf;
+                const f4 v = f4{o[t][d][4 * x], o[t][d][4 * x + 1], o[t][d][4 * x + 2], o[t][d][4 * x + 3]} * f;
+                if (pl.direct) store_result<DT>(a, tok, head, col, v);
+                else if (col < Dp) po[col / 4] = v;
+            }
+        if (hf == 0) {
+            if (!pl.direct) reinterpret_cast<float2 *>(a.ws + pl.ml_off)[at] = make_float2(set[t] ? M[t] : neg_inf(), sum);
+            else if (a.lse) a.lse[tok * a.heads + head] = lse_of(M[t], sum);
+        }
+    }
+}
+
+namespace {
+
+template <int DT, int MASK>
+hipError_t launch_piece(const AttnArgs &a, AttnPlan pl, int rows, int waves, int64_t first, int64_t wgs, hipStream_t st)
+{
+    if (rows == 16) return launch_attn_stream<DT, MASK>(a, pl, waves, first, wgs, st);
+    pl.wg0 = static_cast<int>(first);
+    const int dc = a.c.Dp <= 64 ? 1 : a.c.Dp <= 128 ? 2 : 4;
+    const dim3 grid(static_cast<unsigned>(wgs));
+#define BL_ROWS(DC, RT) hipLaunchKernelGGL((k_attn_rows<DT, DC, RT, MASK>), grid, dim3(256), 0, st, a, pl)
+    if (rows == 256) {
+        if constexpr (DT == DT_F32) BL_ROWS(1, 2);
+    } else if (dc == 1) {
+        BL_ROWS(1, 1);
+    } else if (dc == 2) {
+        BL_ROWS(2, 1);
+    } else {
+        BL_ROWS(4, 1);
+    }
+#undef BL_ROWS
+    return hipGetLastError();
+}
+
+template <int DT, int MASK>
+hipError_t launch_masked(const AttnArgs &a, const AttnPlan &pl, hipStream_t st)
+{
+    return launch_attn_parts(pl, [&](int rows, int waves, int64_t first, int64_t wgs) {
+        return launch_piece<DT, MASK>(a, pl, rows, waves, first, wgs, st);
+    });
+}
+
+} // namespace
 
 hipError_t launch_attn_masked(const AttnArgs &a, const AttnPlan &pl, int mask, hipStream_t st)
 {
     if (a.dtype == DT_F32)
-        return mask == ATTN_TREE ? launch_attn_parts<DT_F32, ATTN_TREE>(a, pl, st)
-                                 : launch_attn_parts<DT_F32, ATTN_WINDOW>(a, pl, st);
-    return mask == ATTN_TREE ? launch_attn_parts<DT_BF16, ATTN_TREE>(a, pl, st)
-                             : launch_attn_parts<DT_BF16, ATTN_WINDOW>(a, pl, st);
+        return mask == ATTN_TREE ? launch_masked<DT_F32, ATTN_TREE>(a, pl, st) : launch_masked<DT_F32, ATTN_WINDOW>(a, pl, st);
+    return mask == ATTN_TREE ? launch_masked<DT_BF16, ATTN_TREE>(a, pl, st) : launch_masked<DT_BF16, ATTN_WINDOW>(a, pl, st);
 }
 
 } // namespace bl

@@ -46,6 +46,16 @@ inline int tile_rows(int64_t rows, int64_t head_dim, bool f32)
     return rows <= 128 || head_dim <= 64 ? 128 : 256;
 }
 
+// The same for k_attn_rows, whose four waves take a tile of 32 rows each, or two (fp32, head_dim up to 64).  With the
+// registers of fp32 queries, or of head_dim past 128, a wave is alone on its SIMD; otherwise two workgroups share a CU,
+// which beat one of eight waves that convert the keys once (bf16, 4 x 200 rows of 8 on up to 9000 keys: 262 us, 280).
+inline int masked_rows(int64_t rows, int64_t head_dim, bool f32)
+{
+    if (rows <= kStreamRows) return 16;
+    return rows > 128 && f32 && head_dim <= 64 ? 256 : 128;
+}
+inline bool masked_alone(int dc, bool f32) { return f32 || dc == 4; }
+
 // How 'wgs' workgroups' passes over 'blocks' key blocks are split: blocks of a
 // part, parts, waves of a workgroup.
 struct AttnCut {
@@ -61,7 +71,7 @@ struct AttnCut {
 // 2^20 workgroups are a thousand rounds of the card, which no split makes shorter: no
 // more parts than that asks for, so that workgroups are numbered in 31 bits.
 inline AttnCut choose_cut(int64_t wgs, int64_t blocks, int rows, int64_t head_dim, int waves, int64_t others,
-                          int64_t part, bool joined)
+                          int64_t part, bool joined, bool masked = false, bool f32 = false)
 {
     AttnCut best{0, 0, waves ? waves : 4};
     if (blocks == 0) return best;
@@ -70,8 +80,9 @@ inline AttnCut choose_cut(int64_t wgs, int64_t blocks, int rows, int64_t head_di
     const int64_t most = std::max<int64_t>(1, std::min<int64_t>(64, (int64_t(1) << 20) / wgs));
     int64_t least = -1;
     for (int w = 1; w <= 8; w *= 2) {
-        if (stream ? w > 4 || (waves && w != waves) : w != rows / 32) continue;
-        const bool alone = stream ? dc == 4 : rows == 256; // one wave a SIMD, one workgroup a CU; or two
+        if (stream ? w > 4 || (waves && w != waves) : w != (masked ? 4 : rows / 32)) continue;
+        // one wave a SIMD, one workgroup a CU; or two
+        const bool alone = stream ? dc == 4 : masked ? masked_alone(dc, f32) : rows == 256;
         const int64_t slots = stream ? 256 * (4 / w) * (alone ? 1 : 2) : 256 * (alone ? 1 : 2);
         for (int64_t s = 1; s <= most && (s == 1 || div_up(blocks, s) >= (stream ? w : 2)); ++s) {
             const int64_t c = div_up(blocks, s), n = div_up(blocks, c);
@@ -102,12 +113,12 @@ inline int64_t attn_window_blocks(int64_t prefix, int64_t max_own, int64_t queri
     return std::min(nbp + nbo, head + div_up(window + queries - 1, ATTN_BLOCK) + 2);
 }
 
-// window > 0: with a sliding window and 'sinks' first tokens.  A sequence's own
+// masked: with k_attn_rows in k_attn_tile's place.  window > 0: with a sliding window and 'sinks' first tokens.  A sequence's own
 // workgroups then go over what they see of the prefix (its keys lie in at most a window,
 // and in another place for every sequence).
 inline AttnPlan attn_plan(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t seqs,
-                          int64_t max_q, int64_t max_own, int64_t prefix, bool f32, int64_t window = 0,
-                          int64_t sinks = 0)
+                          int64_t max_q, int64_t max_own, int64_t prefix, bool f32, bool masked = false,
+                          int64_t window = 0, int64_t sinks = 0)
 {
     AttnPlan p;
     const int64_t G = heads / kv_heads, dp = div_up(head_dim, 16) * 16;
@@ -115,8 +126,8 @@ inline AttnPlan attn_plan(int64_t tokens, int64_t heads, int64_t kv_heads, int64
     // (max_q is a bound, which a captured call keeps from its largest batch: a sequence has no more
     // query tokens than the call, so its tiles are never larger than the prefix's)
     max_q = std::min(max_q, tokens);
-    p.rows_prefix = tile_rows(tokens * G, head_dim, f32);
-    p.rows_own = tile_rows(max_q * G, head_dim, f32);
+    p.rows_prefix = masked ? masked_rows(tokens * G, head_dim, f32) : tile_rows(tokens * G, head_dim, f32);
+    p.rows_own = masked ? masked_rows(max_q * G, head_dim, f32) : tile_rows(max_q * G, head_dim, f32);
     p.tiles_own = static_cast<int>(div_up(max_q * G, p.rows_own));
     // one pass over prefix and own keys where a sequence fills row tiles of its own anyway (4 x 400 query
     // tokens x 8 rows on 2100 keys: 207 us, with a pass of its own for the prefix 222 + 25), or the prefix is
@@ -134,7 +145,7 @@ inline AttnPlan attn_plan(int64_t tokens, int64_t heads, int64_t kv_heads, int64
     AttnCut cut{0, 0, 4};
     if (tp > 0)
         cut = choose_cut(tp * kv_heads, nbp, p.rows_prefix, head_dim, 0,
-                         p.together && nbo > 0 ? busy : 0, part, true);
+                         p.together && nbo > 0 ? busy : 0, part, true, masked, f32);
     p.chunk_prefix = cut.chunk;
     p.splits_prefix = cut.splits;
     p.waves_prefix = cut.waves;
@@ -143,7 +154,7 @@ inline AttnPlan attn_plan(int64_t tokens, int64_t heads, int64_t kv_heads, int64
         window > 0 ? attn_window_blocks(prefix, max_own, std::min(max_q, (p.rows_own + G - 2) / G + 1), window, sinks)
                    : (p.joint ? nbp : 0) + nbo;
     cut = choose_cut(busy, blocks_own, p.rows_own, head_dim,
-                     p.together ? p.waves_prefix : 0, p.together ? p.wgs_prefix : 0, part, tp > 0);
+                     p.together ? p.waves_prefix : 0, p.together ? p.wgs_prefix : 0, part, tp > 0, masked, f32);
     p.chunk_own = cut.chunk;
     p.splits_own = cut.splits;
     p.waves_own = cut.waves;

@@ -251,7 +251,8 @@ struct AttnArgs {
 // a tree over the last.
 enum { ATTN_CAUSAL = 0, ATTN_WINDOW = 1, ATTN_TREE = 2 };
 int64_t attn_workspace_bytes(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim, int64_t seqs,
-                             int64_t max_q, int64_t max_own, int64_t prefix, int64_t window = 0, int64_t sinks = 0);
+                             int64_t max_q, int64_t max_own, int64_t prefix, int64_t window = 0, int64_t sinks = 0,
+                             bool tree = false);
 hipError_t launch_attention(const AttnArgs &a, hipStream_t stream);
 
 // Names (as profilers print them, without the argument list) of the kernel a

@@ -12,7 +12,7 @@ SHIM = """
 #include "attn_plan.h"
 extern "C" void cut(const int64_t *x, int64_t *out)
 {
-    const bl::AttnPlan p = bl::attn_plan(x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7], x[8] != 0, x[9], x[10]);
+    const bl::AttnPlan p = bl::attn_plan(x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7], x[8] != 0, true, x[9], x[10]);
     const int64_t v[] = {p.rows_own, p.tiles_own, p.chunk_own, p.splits_own, p.wgs_prefix, p.wgs_own, p.joint, p.direct,
                          p.waves_own};
     for (int k = 0; k < 9; ++k) out[k] = v[k];
@@ -86,7 +86,8 @@ def test_parts_cover_the_blocks(lib, heads, kvh):
                     what = (heads, kvh, D, f32, seqs, max_q, own, prefix, window, sinks, list(out))
                     assert wgs_prefix == 0 and joint == (prefix > 0) and direct == (splits == 1), what
                     assert wgs == seqs * tiles * kvh * splits and tiles == up(max_q * G, rows), what
-                    assert rows == 16 and waves in (1, 2, 4) or waves == rows // 32, what
+                    assert (rows == 16 and waves in (1, 2, 4)) or (rows in (128, 256) and waves == 4), what
+                    assert rows < 256 or (f32 and D <= 64), what
                     for tile in {0, tiles // 2, tiles - 1}:
                         first, last = tile * rows // G, (min((tile + 1) * rows, max_q * G) - 1) // G
                         ends = [prefix + max(0, min(own, own - max_q + i + 1)) for i in (first, last)]

@@ -5,7 +5,14 @@ The bound is that of the causal form (test_gpu_attention.py), which takes the ke
 that a row sees, whichever they are: with u = 2^-24 and A = scale * sum |q_d k_d|, a
 score is off by at most e = (D + 16) u A + 2^-21 A + 8 u S, S <= A + max; a weight by
 2 e, sums over n keys by (n + 16) u, the weights' rounding to 11 bits (bf16) or 22
-(fp32), and one rounding of the output."""
+(fp32), and one rounding of the output.
+
+With bf16 queries and many rows a weight w = p V_scale is one binary16 number in units
+that bring the largest of a row's first ones to 2^2 (or the largest of all to 2^13), so
+that it is off by 2^-11 of itself or by half of binary16's least step, 2^-25 of those
+units: at most 2^-27 of the row's largest w.  A value is w times a byte of at most 128,
+and o their sum over the n keys: another n 128 2^-27 max(p V_scale), which shows only in
+columns where the keys with large weights hold zeros."""
 import numpy as np
 import pytest
 
@@ -35,6 +42,12 @@ def tree_sight(P, own, n, bits):
     return see
 
 
+def value_scales(st, which, n):
+    t = np.arange(n)
+    p = np.array(st.lists[which], np.int64)[t // st.page] if n else t
+    return st.vs[p, :, t % st.page].astype(np.float64)
+
+
 def reference(st, q, nq, sight, scale, dtype):
     """(o, bound, lse, lse bound) in binary64; sight(b): [n, keys]."""
     heads, D = q.shape[1:]
@@ -59,6 +72,9 @@ def reference(st, q, nq, sight, scale, dtype):
             rel = 2 * e + (seen + 16) * U + (2.0 ** -11 if dtype == "bf16" else 2.0 ** -21)
             o[at + rows, h] = p @ vv
             bound[at + rows, h] = rel[:, None] * (p @ np.abs(vv)) + (2.0 ** -8 if dtype == "bf16" else U) * np.abs(p @ vv)
+            if dtype == "bf16":
+                vs = np.concatenate([value_scales(st, 0, st.prefix), value_scales(st, 1 + b, st.own[b])])[:, h // G]
+                bound[at + rows, h] += (seen * 2.0 ** -20 * (p * np.where(m, vs, 0.0)).max(1))[:, None]
             lse[at + rows, h] = top + np.log(total)
             lbound[at + rows, h] = 2 * e + (seen + 16) * U + 4 * U * np.abs(lse[at + rows, h])
         at += n
@@ -298,7 +314,7 @@ def test_graph_and_stream(which):
     out = torch.empty_like(q)
     sizes = (2 * n, heads, 2, 128, 2, n, 700, 100)
     nws = bl.bitlinear_attention_window_workspace_bytes(*sizes, 300, 4) if which == "window" else \
-        bl.bitlinear_attention_workspace_bytes(*sizes)
+        bl.bitlinear_attention_tree_workspace_bytes(*sizes)
     ws = torch.empty(max(16, nws), dtype=torch.uint8, device="cuda")
     kw = dict(prefix_pages=pp, prefix_len=100, max_q=n, ws=ws)
     kw.update(dict(window=300, sinks=4) if which == "window" else dict(tree=mask))

@@ -117,12 +117,13 @@ def test_workspaces():
         bad = list(args)
         bad[i] = v
         assert bl.bitlinear_attention_window_workspace_bytes(*bad, 30, 4) == -1, (i, v)
+        assert bl.bitlinear_attention_tree_workspace_bytes(*bad) == -1, (i, v)
     # a window over everything is the plain call's plan
     assert bl.bitlinear_attention_window_workspace_bytes(*args, 170, 4) == bl.bitlinear_attention_workspace_bytes(*args)
     # a long cache with a short window is not split as a long one
     long = (1, 8, 1, 128, 1, 1, 1 << 20, 0)
     assert bl.bitlinear_attention_window_workspace_bytes(*long, 64, 4) < bl.bitlinear_attention_workspace_bytes(*long)
-    need = bl.bitlinear_attention_workspace_bytes(1, 8, 2, 128, 1, 1, 100000, 0)
+    need = bl.bitlinear_attention_tree_workspace_bytes(1, 8, 2, 128, 1, 1, 100000, 0)
     assert need > 0
     one = dict(tokens=1, seqs=1, max_q=1, max_own=100000, ld_pages=2000, prefix_len=0, prefix_pages=None)
     big = cache(pages=4000)
