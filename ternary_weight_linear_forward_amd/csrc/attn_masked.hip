@@ -22,21 +22,20 @@ namespace bl {
 // The first product is bf16 for bf16 queries, which takes the queries as they are and
 // the bytes exactly, and binary16 in two terms for fp32 queries (brought into its range
 // by a power of two per row).  Weights are w = 2^(x - M) V_scale, M a reference in base 2
-// that a row gets with its first keys (the first 32 of which it sees some) and keeps, so
-// that sums are never brought to another one:
+// that a row gets with its first keys (the first 32 of which it sees some) and keeps until
+// its weights outgrow it, so that few steps touch its sums:
 //  - fp32 queries: three bf16 terms, 24 bits, in binary32's range; M is the largest x.
-//  - bf16 queries: one binary16 term, 11 bits.  M brings the largest of the first weights
-//    to 2^FIRST_TOP: later ones may be 2^14 times as large; those that are 2^16 times
-//    smaller lose bits, all below 2^-27 of it are lost.
-// A row whose later scores pass what that leaves (its sum passes 2^60, or a weight
-// binary16: then its sums are not finite) asks for more: its workgroup finds every row's
-// largest weight first and starts again.
+//  - bf16 queries: one binary16 term, 11 bits.  M brings the largest weight so far to
+//    2^FIRST_TOP: those that are 2^16 times smaller lose bits, all below 2^-27 of it are lost.
+// A half's weights have outgrown M when their sum (times the block's largest V_scale for
+// binary16) passes a bound that no weight of it can pass alone.  They are not in the sums
+// yet: the row gets a new M, its sums are brought to it and the half's weights are formed
+// again (raise).
 // ---------------------------------------------------------------------------
 typedef __bf16 b8 __attribute__((ext_vector_type(8)));
-constexpr float ROWS_SUM_MAX = 0x1p60f;
-// log2 of what a row's reference makes of the largest of its first weights (one binary16
-// term), and of all of them (a second pass)
-constexpr float FIRST_TOP = 2.0f, LAST_TOP = 13.0f;
+// log2 of what a row's reference makes of the largest weight (one binary16 term); bounds of a half's sum of weights of
+// one lane: with V_scale (binary16 ends at 2^16), and without
+constexpr float FIRST_TOP = 2.0f, ROWS_WEIGHT_MAX = 0x1p15f, ROWS_SUM_MAX = 0x1p60f;
 
 // Eight int8 (two words) to bf16, exactly, by way of binary32.
 __device__ __forceinline__ u4 bytes_to_b8(uint32_t a, uint32_t b)
@@ -123,6 +122,17 @@ __device__ __forceinline__ void to_vector(T &v)
 #endif
 }
 
+// x *= f for an x in an accumulation register, by way of one other (the compiler would find room for all of them).  Waits
+// for a product that forms x, and before one that takes it.
+__device__ __forceinline__ void scale_matrix(float &x, float f)
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+    float y;
+    asm volatile("s_nop 15\n\ts_nop 7\n\tv_accvgpr_read_b32 %1, %0\n\ts_nop 1\n\tv_mul_f32 %1, %1, %2\n\ts_nop 1\n\t"
+                 "v_accvgpr_write_b32 %0, %1\n\ts_nop 3" : "+a"(x), "=&v"(y) : "v"(f));
+#endif
+}
+
 // f(0), f(1), .. f(N - 1) as constants.
 template <class F, int... I>
 __device__ __forceinline__ void in_turn(const F &f, std::integer_sequence<int, I...>)
@@ -148,14 +158,21 @@ __global__ __launch_bounds__(256, rows_waves(DT, DC, RT)) void k_attn_rows(const
     // K in LDS: 16-byte unit of 8 columns c8 of a key at ((c8 / 2 + KSTEPS (c8 % 2)) KROW + key), as in k_attn_tile
     constexpr int KROW = 33, KBYTES = 2 * KSTEPS * KROW * 16, VBYTES = 64 * DPAD * 2;
     // two blocks of K (four halves), of V and of scales
-    __shared__ __attribute__((aligned(16))) uint8_t smem[4 * KBYTES + 2 * VBYTES + 2 * 512];
-    auto k_at = [&](int n, int half) { return smem + (2 * (n & 1) + half) * KBYTES; };
-    auto v_at = [&](int n) { return smem + 4 * KBYTES + (n & 1) * VBYTES; };
-    auto scales_at = [&](int n) { return reinterpret_cast<float *>(smem + 4 * KBYTES + 2 * VBYTES + (n & 1) * 512); };
+    __shared__ __attribute__((aligned(16))) uint8_t smem[4 * KBYTES + 2 * VBYTES + 2 * 512 + 16];
+    // bytes of half a block of keys, a block of values and one of scales (K_scales, then V_scales) in it; last, the
+    // largest V_scale of two blocks
+    auto k_at = [](int n, int half) { return (2 * (n & 1) + half) * KBYTES; };
+    auto v_at = [](int n) { return 4 * KBYTES + (n & 1) * VBYTES; };
+    auto scales_at = [](int n) { return 4 * KBYTES + 2 * VBYTES + (n & 1) * 512; };
+    auto top_at = [](int n) { return 4 * KBYTES + 2 * VBYTES + 2 * 512 + (n & 1) * 4; };
+    auto lds4 = [&](uint32_t at) -> u4 & { return *reinterpret_cast<u4 *>(smem + at); };
+    auto lds2 = [&](uint32_t at) -> uint2 & { return *reinterpret_cast<uint2 *>(smem + at); };
+    auto lds1 = [&](uint32_t at) -> float & { return *reinterpret_cast<float *>(smem + at); };
+    const int tid = threadIdx.x, G = a.heads / a.c.heads, Dp = a.c.Dp;
     AttnJob j;
     if (!attn_job<MASK>(a, pl, 128 * RT, blockIdx.x + pl.wg0, j)) return;
-    const int G = a.heads / a.c.heads, lane = lane_id(), wave = wave_id(), i = lane & 31, hf = lane >> 5;
-    const int Dp = a.c.Dp, tid = threadIdx.x, nblk = j.blk1 - j.blk0;
+    const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), i = lane & 31, hf = lane >> 5;
+    const int nblk = j.blk1 - j.blk0;
 
     // this thread's bytes of a half of K and of a block of V; columns past Dp read the row's start (the queries
     // hold zeros there), V's rows past Dp its first rows (their sums are not stored)
@@ -173,6 +190,15 @@ __global__ __launch_bounds__(256, rows_waves(DT, DC, RT)) void k_attn_rows(const
         const int id = tid + 256 * u;
         voff[u] = (id / 4 < Dp ? id : id % 4) * 16;
     }
+    // this lane's place in an operand of keys, of values and among the scales, this thread's in what it stages of keys
+    // and of values; all else is a constant apart (values kept here, so that nothing they come from has to be)
+    uint32_t kl = (KSTEPS * hf * KROW + i) * 16, vl = (hf * DPAD + i) * 16, sl = 16 * hf,
+             kst = (tid % (4 * DC) * KROW + tid / (4 * DC)) * 16, vst = ((tid & 1) * DPAD + tid / 4) * 16 + (tid & 2) * 4;
+    to_vector(kl);
+    to_vector(vl);
+    to_vector(sl);
+    to_vector(kst);
+    to_vector(vst);
     float ksr = 0.0f, vsr = 0.0f;
     auto fetch_k = [&](int half, int u, uint32_t unit) {
         kreg[half][u] = load_at<u4>(block_bytes(a.c.K, unit, Dp) + 32 * half * Dp, koff[u]);
@@ -195,9 +221,9 @@ __global__ __launch_bounds__(256, rows_waves(DT, DC, RT)) void k_attn_rows(const
         unit = table.at(n % 64);
         there = table.there(n % 64);
     };
-    // block 0, and the first half of block 1's keys
+    // block 0, and the first half of block 1's keys (in flight while the queries are read)
     u4 kfirst[KU] = {};
-    auto first_loads = [&]() {
+    if (nblk > 0) {
         uint32_t unit0 = 0;
         look_up(0, unit0, there0);
         unit1 = unit0;
@@ -214,8 +240,7 @@ __global__ __launch_bounds__(256, rows_waves(DT, DC, RT)) void k_attn_rows(const
         fetch_scales(unit0);
 #pragma unroll
         for (int u = 0; u < KU; ++u) kfirst[u] = load_at<u4>(block_bytes(a.c.K, unit1, Dp), koff[u]);
-    };
-    if (nblk > 0) first_loads(); // (in flight while the queries are read)
+    }
 
     // Queries: operands, and a row's factor from scores to base 2 (fp32: of its own power of two).
     u4 q[RT][KSTEPS][NS];
@@ -263,25 +288,28 @@ __global__ __launch_bounds__(256, rows_waves(DT, DC, RT)) void k_attn_rows(const
 #pragma unroll
                 for (int z = 0; z < NS; ++z) to_matrix(q[t][k][z]);
     }
-    auto stage_k = [&](const u4 &from, int u, int part, uint8_t *to) {
-        const int id = tid + 256 * u, key = id / (4 * DC), cu = id % (4 * DC);
+    auto stage_k = [&](const u4 &from, int u, int part, int to) { // (a second unit: 256 / (4 DC) keys on)
         if (k_mine)
-            reinterpret_cast<u4 *>(to)[(cu + KSTEPS * part) * KROW + key] = key_operand<DT>(from[2 * part], from[2 * part + 1]);
+            lds4(kst + to + (KSTEPS * part * KROW + u * (64 / DC)) * 16) = key_operand<DT>(from[2 * part], from[2 * part + 1]);
     };
-    // V: unit (2 T + g % 2) * DPAD + d holds quads g and g + 2 of 16-key tile T; a half is two tiles.
-    auto stage_v = [&](int half, int u, uint8_t *to) {
-        const int id = tid + 256 * u, d = id / 4, g = id % 4;
-        uint2 *pv = reinterpret_cast<uint2 *>(to);
+    // V: unit (2 T + g % 2) * DPAD + d holds quads g and g + 2 of 16-key tile T; a half is two tiles, the next unit of a
+    // thread 64 rows on.
+    auto stage_v = [&](int half, int u, int to) {
         const u4 x = value_operand<DT>(vreg[half][u].x, vreg[half][u].y);
-        pv[((4 * half + (g & 1)) * DPAD + d) * 2 + (g >> 1)] = make_uint2(x[0], x[1]);
-        pv[((4 * half + 2 + (g & 1)) * DPAD + d) * 2 + (g >> 1)] = make_uint2(x[2], x[3]);
+        lds2(vst + to + (4 * half * DPAD + 64 * u) * 16) = make_uint2(x[0], x[1]);
+        lds2(vst + to + ((4 * half + 2) * DPAD + 64 * u) * 16) = make_uint2(x[2], x[3]);
     };
     // (a hidden score is -inf: never times 0.  A V_scale that is not finite counts as the largest number: its key's
     // weight overflows where a row sees it and is 0 where it is hidden)
-    auto stage_scales = [&](float *to) {
+    auto stage_scales = [&](int n) {
         if (wave == 0) {
-            to[lane] = fmaxf(DT == DT_BF16 ? ksr * c[0] : ksr, 1.17549435e-38f);
-            to[64 + lane] = fminf(vsr, 3.402823466e38f);
+            const float v = fminf(vsr, 3.402823466e38f);
+            lds1(4 * lane + scales_at(n)) = fmaxf(DT == DT_BF16 ? ksr * c[0] : ksr, 1.17549435e-38f);
+            lds1(4 * lane + scales_at(n) + 256) = v;
+            if constexpr (DT == DT_BF16) {
+                const float top = wave_max_nonneg(fabsf(v));
+                if (lane == 0) lds1(top_at(n)) = top;
+            }
         }
     };
 
@@ -292,9 +320,9 @@ __global__ __launch_bounds__(256, rows_waves(DT, DC, RT)) void k_attn_rows(const
     uint64_t vis[RT];              // keys of the block the row sees
     bool hidden = false;           // the rows do not all see all of it
     // K_scales (V_scales) of keys 8 x + 4 hf .. of a half
-    auto key_scales = [&](int n, int half, int x) { return reinterpret_cast<const f4 *>(scales_at(n))[8 * half + 2 * x + hf]; };
+    auto key_scales = [&](int n, int half, int x) { return __builtin_bit_cast(f4, lds4(sl + scales_at(n) + 128 * half + 32 * x)); };
     auto value_scales = [&](int n, int half, int x) {
-        return reinterpret_cast<const f4 *>(scales_at(n))[16 + 8 * half + 2 * x + hf];
+        return __builtin_bit_cast(f4, lds4(sl + scales_at(n) + 256 + 128 * half + 32 * x));
     };
     // Which keys of block n the rows see.  A block that every row of the tile sees whole is told from the tile's bounds
     // alone.
@@ -326,18 +354,16 @@ __global__ __launch_bounds__(256, rows_waves(DT, DC, RT)) void k_attn_rows(const
             }
         }
     };
-    // The reference of a row that has none.  The largest weight comes to 2^room where it is binary16; sums of p stay in
-    // range where values are very small.  bf16 terms need no more than that of p.
-    auto first_reference = [&](int t, float top, float most, float room) {
+    // The reference that a half's scores ask for.  The largest weight comes to 2^FIRST_TOP where it is binary16; sums of p
+    // stay in range where values are very small.  bf16 terms need no more than that of p.
+    auto reference = [&](int n, int half, const f16v &sc, int t, float &top) {
+        float most = neg_inf();
+        top = neg_inf();
+        meet(n, half, sc, t, top, most);
         top = max_across32(top);
-        float m = top;
-        if constexpr (DT == DT_BF16) {
-            most = max_across32(most);
-            m = most > neg_inf() ? fmaxf(most - room, top - 40.0f) : top;
-        }
-        const bool now = !set[t] && top > neg_inf();
-        M[t] = now ? m : M[t];
-        set[t] = set[t] || now;
+        if constexpr (DT != DT_BF16) return top;
+        most = max_across32(most);
+        return most > neg_inf() ? fmaxf(most - FIRST_TOP, top - 40.0f) : top;
     };
     // Before a half's weights: scores a row does not see, and the reference of a row whose first keys these are (its
     // sums are still zero).
@@ -351,9 +377,11 @@ __global__ __launch_bounds__(256, rows_waves(DT, DC, RT)) void k_attn_rows(const
         bool unset = false;
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
-            float top = neg_inf(), most = neg_inf();
-            meet(n, H, s[H][t], t, top, most);
-            first_reference(t, top, most, FIRST_TOP);
+            float top;
+            const float m = reference(n, H, s[H][t], t, top);
+            const bool now = !set[t] && top > neg_inf();
+            M[t] = now ? m : M[t];
+            set[t] = set[t] || now;
             unset |= !set[t];
         }
         settled = !__any(unset);
@@ -379,13 +407,12 @@ __global__ __launch_bounds__(256, rows_waves(DT, DC, RT)) void k_attn_rows(const
     constexpr int PER = RT * (NT + NS), PRODUCTS = OPS * PER, PARTS = 3 * PAIRS, STAGE = 4 * KU + 2 * VU + 1;
     u4 rk[AHEAD], rv[AHEAD];
     f4 kq[2], vq[2];
+    float vtop = 0.0f; // the largest V_scale of the block
     auto read_ops = [&](int n, int y) { // operand y % OPS of half y / OPS
         if (y >= 2 * OPS) return;
         const int half = y / OPS, x = y % OPS;
-        const u4 *pv = reinterpret_cast<const u4 *>(v_at(half == 0 ? n - 1 : n));
-        const u4 *pk = reinterpret_cast<const u4 *>(half == 0 ? k_at(n, 1) : k_at(n + 1, 0));
-        rv[y % AHEAD] = pv[(2 * (x / DT32 + 2 * (1 - half)) + hf) * DPAD + 32 * (x % DT32) + i];
-        rk[y % AHEAD] = pk[(x + KSTEPS * hf) * KROW + i];
+        rv[y % AHEAD] = lds4(vl + v_at(half == 0 ? n - 1 : n) + (2 * (x / DT32 + 2 * (1 - half)) * DPAD + 32 * (x % DT32)) * 16);
+        rk[y % AHEAD] = lds4(kl + (half == 0 ? k_at(n, 1) : k_at(n + 1, 0)) + x * KROW * 16);
     };
     auto read_scales = [&](int n, int x) { // quad x % 4 of half x / 4
         if (x >= 8) return;
@@ -402,8 +429,50 @@ __global__ __launch_bounds__(256, rows_waves(DT, DC, RT)) void k_attn_rows(const
             stage_v(half, u, half ? v_at(n) : v_at(n + 1));
             fetch_v(half, u, half ? unit1 : unit2);
         } else {
-            stage_scales(scales_at(n + 1));
+            stage_scales(n + 1);
             fetch_scales(unit2);
+        }
+    };
+    // A half whose weights outgrew a row's reference.
+    auto raise = [&](auto half_c, int n, float (&sum)[RT][2]) {
+        constexpr int H = decltype(half_c)::value;
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+            float top;
+            const float m = fmaxf(M[t], reference(n, H, s[H][t], t, top)), f = __builtin_amdgcn_exp2f(M[t] - m);
+            M[t] = m;
+            l[t] *= f;
+#pragma unroll
+            for (int d = 0; d < DT32; ++d)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    if constexpr (rows_waves(DT, DC, RT) == 1) {
+                        float x = o[t][d][r];
+                        scale_matrix(x, f);
+                        o[t][d][r] = x;
+                    } else {
+                        o[t][d][r] *= f;
+                    }
+                }
+            sum[t][0] = sum[t][1] = 0.0f;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const f4 ks = key_scales(n, H, x), vs = value_scales(n, H, x);
+#pragma unroll
+                for (int e = 0; e < 4; e += 2) {
+                    float g[2];
+#pragma unroll
+                    for (int z = 0; z < 2; ++z) {
+                        const float v = DT == DT_BF16 ? s[H][t][4 * x + e + z] : s[H][t][4 * x + e + z] * c[t];
+                        g[z] = __builtin_amdgcn_exp2f(__builtin_fmaf(v, ks[e + z], -m));
+                        sum[t][z] += g[z];
+                    }
+                    uint32_t terms[NT];
+                    weight_terms<DT, NT>(g[0] * vs[e], g[1] * vs[e + 1], terms);
+#pragma unroll
+                    for (int z = 0; z < NT; ++z) p[H][t][x / 2][z][2 * (x % 2) + e / 2] = terms[z];
+                }
+            }
         }
     };
     auto half_block = [&](auto half_c, int n) {
@@ -472,140 +541,107 @@ __global__ __launch_bounds__(256, rows_waves(DT, DC, RT)) void k_attn_rows(const
             });
         });
         __builtin_amdgcn_sched_barrier(0);
+        bool outgrown = false;
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+            const float all = sum[t][0] + sum[t][1];
+            outgrown |= all > ROWS_SUM_MAX || (DT == DT_BF16 && all * vtop > ROWS_WEIGHT_MAX);
+        }
+        if (__builtin_expect_with_probability(__any(outgrown), 0, 0.95)) raise(half_c, n, sum);
 #pragma unroll
         for (int t = 0; t < RT; ++t) l[t] += sum[t][0] + sum[t][1];
         place(1 - H);
     };
 
-    // Every row's reference from all of its keys: for a second pass, where one has outgrown its first ones'.
-    auto all_references = [&]() {
-        float tops[RT], mosts[RT];
 #pragma unroll
-        for (int t = 0; t < RT; ++t) tops[t] = mosts[t] = neg_inf();
-        for (int n = 0; n < nblk; ++n) {
-            look_up(n, unit1, there1);
-            look(n, there1);
+    for (int t = 0; t < RT; ++t) {
+        M[t] = l[t] = 0.0f;
+        set[t] = false;
+        vis[t] = 0;
+    }
 #pragma unroll
-            for (int u = 0; u < KU; ++u) {
-                fetch_k(0, u, unit1);
-                fetch_k(1, u, unit1);
-            }
-            fetch_scales(unit1);
-            __syncthreads();
+    for (int t = 0; t < RT; ++t) {
 #pragma unroll
-            for (int x = 0; x < 4 * KU; ++x) stage_k(kreg[x / 2 / KU][x / 2 % KU], x / 2 % KU, x % 2, k_at(0, x / 2 / KU));
-            stage_scales(scales_at(0));
-            __syncthreads();
+        for (int d = 0; d < DT32; ++d)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const u4 *pk = reinterpret_cast<const u4 *>(k_at(0, h));
+            for (int r = 0; r < 16; ++r) o[t][d][r] = 0.0f;
 #pragma unroll
-                for (int t = 0; t < RT; ++t) {
-                    f16v sc;
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) sc[r] = 0.0f;
+            for (int r = 0; r < 16; ++r) s[h][t][r] = 0.0f;
 #pragma unroll
-                    for (int x = 0; x < KSTEPS; ++x)
+        for (int x = 0; x < 2; ++x)
 #pragma unroll
-                        for (int z = 0; z < NS; ++z) sc = score_product<DT>(pk[(x + KSTEPS * hf) * KROW + i], q[t][x][z], sc);
-                    hide(h, sc, t);
-                    meet(0, h, sc, t, tops[t], mosts[t]);
-                }
-            }
+            for (int z = 0; z < NT; ++z) p[0][t][x][z] = p[1][t][x][z] = u4{0, 0, 0, 0};
+    }
+    if (nblk > 0) {
+#pragma unroll
+        for (int x = 0; x < 4 * KU; ++x) stage_k(kreg[x / 2 / KU][x / 2 % KU], x / 2 % KU, x % 2, k_at(0, x / 2 / KU));
+#pragma unroll
+        for (int x = 0; x < 2 * KU; ++x) stage_k(kfirst[x / 2], x / 2, x % 2, k_at(1, 0));
+#pragma unroll
+        for (int u = 0; u < VU; ++u) stage_v(0, u, v_at(0));
+        stage_scales(0);
+        // (the first half adds zero weights of a block that is not there: its V must be finite)
+        for (int x = tid; x < VBYTES / 32; x += 256) lds4(v_at(1) + VBYTES / 2 + 16 * x) = u4{0, 0, 0, 0};
+#pragma unroll
+        for (int u = 0; u < KU; ++u) {
+            fetch_k(1, u, unit1);
+            fetch_k(0, u, unit2);
         }
 #pragma unroll
-        for (int t = 0; t < RT; ++t) first_reference(t, tops[t], mosts[t], LAST_TOP);
+        for (int u = 0; u < VU; ++u) fetch_v(0, u, unit1); // (vreg[1] holds block 0's second half)
+        fetch_scales(unit1);
         __syncthreads();
-        if (nblk > 0) first_loads();
-    };
-
-    for (int pass = 0;; ++pass) {
-        settled = false;
+        // scores of the first half
 #pragma unroll
-        for (int t = 0; t < RT; ++t) {
-            M[t] = l[t] = 0.0f;
-            set[t] = false;
-            vis[t] = 0;
-        }
-        if (pass > 0) all_references();
+        for (int x0 = 0; x0 < OPS; x0 += 4) { // (four operands at once: their reads take longer than a product)
+            u4 k[4];
 #pragma unroll
-        for (int t = 0; t < RT; ++t) {
+            for (int x = 0; x < 4; ++x) k[x] = lds4(kl + k_at(0, 0) + (x0 + x) * KROW * 16);
 #pragma unroll
-            for (int d = 0; d < DT32; ++d)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) o[t][d][r] = 0.0f;
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) s[h][t][r] = 0.0f;
-#pragma unroll
-            for (int x = 0; x < 2; ++x)
-#pragma unroll
-                for (int z = 0; z < NT; ++z) p[0][t][x][z] = p[1][t][x][z] = u4{0, 0, 0, 0};
-        }
-        if (nblk > 0) {
-#pragma unroll
-            for (int x = 0; x < 4 * KU; ++x) stage_k(kreg[x / 2 / KU][x / 2 % KU], x / 2 % KU, x % 2, k_at(0, x / 2 / KU));
-#pragma unroll
-            for (int x = 0; x < 2 * KU; ++x) stage_k(kfirst[x / 2], x / 2, x % 2, k_at(1, 0));
-#pragma unroll
-            for (int u = 0; u < VU; ++u) stage_v(0, u, v_at(0));
-            stage_scales(scales_at(0));
-            // (the first half adds zero weights of a block that is not there: its V must be finite)
-            for (int x = tid; x < VBYTES / 32; x += 256) reinterpret_cast<u4 *>(v_at(1) + VBYTES / 2)[x] = u4{0, 0, 0, 0};
-#pragma unroll
-            for (int u = 0; u < KU; ++u) {
-                fetch_k(1, u, unit1);
-                fetch_k(0, u, unit2);
-            }
-#pragma unroll
-            for (int u = 0; u < VU; ++u) fetch_v(0, u, unit1); // (vreg[1] holds block 0's second half)
-            fetch_scales(unit1);
-            __syncthreads();
-            // scores of the first half
-            const u4 *pk = reinterpret_cast<const u4 *>(k_at(0, 0));
-#pragma unroll
-            for (int x = 0; x < OPS; ++x) {
-                const u4 k = pk[(x + KSTEPS * hf) * KROW + i];
+            for (int x = 0; x < 4; ++x)
 #pragma unroll
                 for (int t = 0; t < RT; ++t)
 #pragma unroll
-                    for (int z = 0; z < NS; ++z) s[0][t] = score_product<DT>(k, q[t][x][z], s[0][t]);
-            }
-            __syncthreads();
+                    for (int z = 0; z < NS; ++z) s[0][t] = score_product<DT>(k[x], q[t][x0 + x][z], s[0][t]);
         }
-        place(0);
-        for (int n = 0; n < nblk; ++n) {
+        __syncthreads();
+    }
+    place(0);
+    for (int n = 0; n < nblk; ++n) {
 #pragma unroll
-            for (int x = 0; x < AHEAD; ++x) read_ops(n, x);
-            read_scales(n, 0);
-            look(n, there0);
-            unit3 = unit2;
-            look_up(n + 3, unit3, there3);
-            half_block(std::integral_constant<int, 0>(), n);
-            half_block(std::integral_constant<int, 1>(), n);
-            there0 = there1;
-            there1 = there2;
-            there2 = there3;
-            unit1 = unit2;
-            unit2 = unit3;
-            __syncthreads();
-        }
-        if (nblk > 0) { // values of the last half
-            const u4 *pv = reinterpret_cast<const u4 *>(v_at(nblk - 1));
+        for (int x = 0; x < AHEAD; ++x) read_ops(n, x);
+        read_scales(n, 0);
+        if constexpr (DT == DT_BF16) vtop = lds1(top_at(n));
+        look(n, there0);
+        unit3 = unit2;
+        look_up(n + 3, unit3, there3);
+        half_block(std::integral_constant<int, 0>(), n);
+        half_block(std::integral_constant<int, 1>(), n);
+        there0 = there1;
+        there1 = there2;
+        there2 = there3;
+        unit1 = unit2;
+        unit2 = unit3;
+        __syncthreads();
+    }
+    if (nblk > 0) { // values of the last half
 #pragma unroll
-            for (int x = 0; x < OPS; ++x) {
-                const u4 v = pv[(2 * (x / DT32 + 2) + hf) * DPAD + 32 * (x % DT32) + i];
+        for (int x0 = 0; x0 < OPS; x0 += 4) {
+            u4 v[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+                v[y] = lds4(vl + v_at(nblk - 1) + (2 * ((x0 + y) / DT32 + 2) * DPAD + 32 * ((x0 + y) % DT32)) * 16);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const int x = x0 + y;
 #pragma unroll
                 for (int t = 0; t < RT; ++t)
 #pragma unroll
-                    for (int z = 0; z < NT; ++z) o[t][x % DT32] = value_product<DT>(v, p[1][t][x / DT32][z], o[t][x % DT32]);
+                    for (int z = 0; z < NT; ++z) o[t][x % DT32] = value_product<DT>(v[y], p[1][t][x / DT32][z], o[t][x % DT32]);
             }
         }
-        bool outgrown = false;
-#pragma unroll
-        for (int t = 0; t < RT; ++t) outgrown |= !(l[t] <= ROWS_SUM_MAX) | !(fabsf(o[t][0][0]) < __builtin_inff());
-        if (!__syncthreads_or(outgrown) || pass > 0) break;
     }
 #pragma unroll
     for (int t = 0; t < RT; ++t) {

@@ -8,8 +8,8 @@ score is off by at most e = (D + 16) u A + 2^-21 A + 8 u S, S <= A + max; a weig
 (fp32), and one rounding of the output.
 
 With bf16 queries and many rows a weight w = p V_scale is one binary16 number in units
-that bring the largest of a row's first ones to 2^2 (or the largest of all to 2^13), so
-that it is off by 2^-11 of itself or by half of binary16's least step, 2^-25 of those
+that bring the largest of a row's first ones to 2^2 (and, when later ones outgrow that,
+the largest so far), so that it is off by 2^-11 of itself or by half of binary16's least step, 2^-25 of those
 units: at most 2^-27 of the row's largest w.  A value is w times a byte of at most 128,
 and o their sum over the n keys: another n 128 2^-27 max(p V_scale), which shows only in
 columns where the keys with large weights hold zeros."""
@@ -235,6 +235,26 @@ def test_scores_that_move(dtype, D, n):
     bits = rng.random((n, n)) < 0.1
     o, lse = call(st, qt, [n], entry=bl.attention_tree, tree=to_dev(words([bits], n)))
     compare(o, lse, reference(st, q, [n], lambda b: tree_sight(100, own, n, bits), D ** -0.5, dtype))
+
+
+@pytest.mark.parametrize("dtype,D,n", [("bf16", 128, 60), ("bf16", 64, 200), ("bf16", 256, 40), ("f32", 128, 60),
+                                       ("f32", 64, 60), ("f32", 256, 40)])
+def test_scores_that_grow(dtype, D, n):
+    """Keys that grow from block to block, to scores of a hundred and more: every row's weights outgrow its first keys'
+    again and again, in blocks of its own.  With values of even sizes, and values that shrink as the keys grow."""
+    own = 900
+    for shrink in (False, True):
+        st = Setup(1, D, 64, 0, [own], seed=D + n)
+        for j, page in enumerate(st.lists[1]):
+            st.ks[page] *= np.float32(0.05 + 2.5 * j)
+            if shrink:
+                st.vs[page] *= np.float32(2.0 ** -j)
+        qt, q = queries(n, 8, D, 13, dtype, size=2.0)
+        o, lse = call(st, qt, [n], entry=bl.attention_window, window=700, sinks=90)
+        compare(o, lse, reference(st, q, [n], lambda b: window_sight(0, own, n, 700, 90), D ** -0.5, dtype))
+        bits = np.random.default_rng(n).random((n, n)) < 0.3
+        o, lse = call(st, qt, [n], entry=bl.attention_tree, tree=to_dev(words([bits], n)))
+        compare(o, lse, reference(st, q, [n], lambda b: tree_sight(0, own, n, bits), D ** -0.5, dtype))
 
 
 @pytest.mark.parametrize("dtype,n", [("bf16", 1), ("bf16", 80), ("f32", 1), ("f32", 80)])
