@@ -201,17 +201,16 @@ __global__ __launch_bounds__(256) void k_cache_read(const CacheView c, const Cac
     }
 }
 
-// Moves of one group (grid x) and head (grid y): every byte and scale is read before
-// the barrier and written after it.  A token's K is one run of bytes; its V is a byte
-// of each of Dp rows of 64, where neighbouring lanes take the group's moves, whose
-// tokens lie in one or two blocks as a rule.  Only a move's own bytes are written: the
-// others of a row may be another group's.  Bound: latency for a few drafts, then the
-// rows of V that single bytes are taken from.
-__global__ __launch_bounds__(256) void k_cache_move(const CacheView c, const int64_t *src, const int64_t *dst, int width)
+// Moves of one group (grid x) and head (grid y), for 8 (256 >> shift) columns (grid z) of K and V, which no other
+// workgroup touches: every byte and scale is read before the barrier and written after it, by the same thread.  A group
+// has 1 << shift lanes, one a move, at a row of V (a byte of each of Dp rows of 64: the moves' tokens lie in one or two
+// blocks as a rule, so that neighbouring lanes meet the same line), and a thread eight rows, whose loads are in flight
+// together.  Only a move's own bytes are written: the others of a row may be another group's.
+constexpr int MOVE_ROWS = 8;
+__global__ __launch_bounds__(256) void k_cache_move(const CacheView c, const int64_t *src, const int64_t *dst, int width,
+                                                    int shift)
 {
     __shared__ int64_t at_src[MAX_MOVES], at_dst[MAX_MOVES]; // rows of the head's K; at_dst -1: no move
-    __shared__ __attribute__((aligned(16))) uint8_t k[MAX_MOVES * 256], v[MAX_MOVES * 256];
-    __shared__ float ks[MAX_MOVES], vs[MAX_MOVES];
     const int64_t g0 = static_cast<int64_t>(blockIdx.x) * width;
     const int head = blockIdx.y, tid = threadIdx.x;
     if (tid < 64) { // (one wave)
@@ -219,53 +218,61 @@ __global__ __launch_bounds__(256) void k_cache_move(const CacheView c, const int
         bool ok = s >= 0 && s < c.slots && d >= 0 && d < c.slots;
         const int64_t target = ok ? d : -1;
         for (int x = 1; x < width; ++x) { // a later move to the same slot counts instead
-            const int64_t other = __shfl(target, x);
-            ok = ok && !(x > tid && other == d);
+            const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(target), x);
+            const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(target >> 32), x);
+            ok = ok && !(x > tid && static_cast<int64_t>(static_cast<uint64_t>(hi) << 32 | lo) == d);
         }
         auto row = [&](int64_t slot) {
             const int64_t page = slot / c.page_tokens;
             return cache_row0(c, page, head) + (slot - page * c.page_tokens);
         };
-        const int64_t rs = ok ? row(s) : 0, rd = ok ? row(d) : -1;
-        at_src[tid] = rs;
-        at_dst[tid] = rd;
-        if (ok) {
-            ks[tid] = c.Ks[rs];
-            vs[tid] = c.Vs[rs];
-        }
+        at_src[tid] = ok ? row(s) : 0;
+        at_dst[tid] = ok ? row(d) : -1;
     }
     __syncthreads();
-    const int units = c.Dp / 16;
-    for (int n = tid; n < width * units; n += 256) {
-        const int m = n / units, u = n % units;
-        if (at_dst[m] >= 0)
-            reinterpret_cast<uint4 *>(k)[n] = *reinterpret_cast<const uint4 *>(c.K + at_src[m] * c.Dp + 16 * u);
+    const int m = tid & ((1 << shift) - 1), per = 256 >> shift, d0 = blockIdx.z * MOVE_ROWS * per;
+    const bool mine = m < width && at_dst[m] >= 0;
+    const int64_t rs = mine ? at_src[m] : 0, rd = mine ? at_dst[m] : 0;
+    // 16 columns of K are a thread's, of the first half
+    const int col = d0 + 16 * (tid >> shift);
+    const bool k_mine = mine && 2 * tid < 256 && col < c.Dp, scales = mine && tid < width && blockIdx.z == 0;
+    const int first = d0 + (tid >> shift), last = c.Dp - 1;
+    uint4 k = make_uint4(0, 0, 0, 0);
+    int8_t v[MOVE_ROWS];
+    float ks = 0.0f, vs = 0.0f;
+    if (scales) {
+        ks = c.Ks[rs];
+        vs = c.Vs[rs];
     }
-    for (int n = tid; n < width * c.Dp; n += 256) {
-        const int d = n / width, m = n % width;
-        if (at_dst[m] >= 0) v[n] = c.V[v_at(c, at_src[m], d)];
+    if (k_mine) k = *reinterpret_cast<const uint4 *>(c.K + rs * c.Dp + col);
+    if (mine) {
+        const int8_t *V = c.V + v_at(c, rs, 0);
+#pragma unroll
+        for (int u = 0; u < MOVE_ROWS; ++u) v[u] = V[CACHE_BLOCK * min(first + u * per, last)];
     }
     __syncthreads();
-    for (int n = tid; n < width * units; n += 256) {
-        const int m = n / units, u = n % units;
-        if (at_dst[m] >= 0)
-            *reinterpret_cast<uint4 *>(c.K + at_dst[m] * c.Dp + 16 * u) = reinterpret_cast<const uint4 *>(k)[n];
+    if (scales) {
+        c.Ks[rd] = ks;
+        c.Vs[rd] = vs;
     }
-    for (int n = tid; n < width * c.Dp; n += 256) {
-        const int d = n / width, m = n % width;
-        if (at_dst[m] >= 0) c.V[v_at(c, at_dst[m], d)] = static_cast<int8_t>(v[n]);
-    }
-    if (tid < width && at_dst[tid] >= 0) {
-        c.Ks[at_dst[tid]] = ks[tid];
-        c.Vs[at_dst[tid]] = vs[tid];
+    if (k_mine) *reinterpret_cast<uint4 *>(c.K + rd * c.Dp + col) = k;
+    if (mine) {
+        int8_t *V = c.V + v_at(c, rd, 0);
+#pragma unroll
+        for (int u = 0; u < MOVE_ROWS; ++u)
+            if (first + u * per <= last) V[CACHE_BLOCK * (first + u * per)] = v[u];
     }
 }
 
 hipError_t launch_cache_move(const CacheView &c, const int64_t *src, const int64_t *dst, int64_t groups, int width,
                              hipStream_t stream)
 {
-    hipLaunchKernelGGL(k_cache_move, dim3(static_cast<unsigned>(groups), static_cast<unsigned>(c.heads)), dim3(256), 0,
-                       stream, c, src, dst, width);
+    int shift = 0;
+    while (1 << shift < width) ++shift;
+    const int columns = MOVE_ROWS * (256 >> shift);
+    hipLaunchKernelGGL(k_cache_move,
+                       dim3(static_cast<unsigned>(groups), static_cast<unsigned>(c.heads), (c.Dp + columns - 1) / columns),
+                       dim3(256), 0, stream, c, src, dst, width, shift);
     return hipGetLastError();
 }
 
