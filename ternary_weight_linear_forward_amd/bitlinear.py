@@ -832,9 +832,15 @@ def cache_read(cache: KVCache, slots, dtype=None, stream=None):
 
 def _here(where: str, *tensors) -> None:
     """Refuses tensors that are not on the current device, whose kernels would follow their addresses."""
+    here = torch.cuda.current_device() if torch.cuda.is_initialized() else 0
     for t in tensors:
-        if t is not None and not (t.is_cuda and t.get_device() == torch.cuda.current_device()):
+        if t is not None and t.get_device() != here:  # (-1 for one on the host)
             raise BitlinearError(ERR_INVALID_ARG, where)
+
+
+def _vector(t, n: int | None) -> bool:
+    """Whether t is a packed int32 vector (of n numbers)."""
+    return t.dtype == torch.int32 and t.dim() == 1 and (n is None or t.numel() == n) and t.is_contiguous()
 
 
 def cache_assign(held, count, own_pages, free_pages, free_count, tokens: int, page_tokens: int, max_own: int | None = None,
@@ -855,17 +861,15 @@ def cache_assign(held, count, own_pages, free_pages, free_count, tokens: int, pa
     ldp, step = own_pages.stride()
     if max_own is None:
         max_own = cols * page_tokens
-    vectors = [(held, seqs), (count, seqs), (free_pages, free_pages.numel()), (free_count, 1)]
-    vectors += [(own_len, seqs)] if own_len is not None else []
-    vectors += [(free_left, 1)] if free_left is not None else []
     if own_pages.dtype != i32 or rows != seqs or (cols > 1 and step != 1) or (rows > 1 and ldp < cols) or \
             cols * page_tokens < max_own or tokens < 0 or \
-            any(t.dtype != i32 or t.dim() != 1 or t.numel() != n or not t.is_contiguous() for t, n in vectors):
+            not (_vector(held, seqs) and _vector(count, seqs) and _vector(free_pages, None) and _vector(free_count, 1)) or \
+            not (own_len is None or _vector(own_len, seqs)) or not (free_left is None or _vector(free_left, 1)):
         raise BitlinearError(ERR_INVALID_ARG, name)
     _here(name, held, count, own_pages, free_pages, free_count, own_len, free_left)
     # one allocation: lengths, first positions, starts, positions, list
     n = (0, 0 if own_len is not None else seqs, seqs, seqs + 1, tokens, 0 if free_left is not None else 1)
-    parts = held.new_empty(sum(n)).split(n[1:])
+    parts = held.new_empty(sum(n)).split_with_sizes(n[1:])
     own_len = parts[0] if own_len is None else own_len
     free_left = parts[4] if free_left is None else free_left
     first, q_start, positions = parts[1], parts[2], parts[3]
