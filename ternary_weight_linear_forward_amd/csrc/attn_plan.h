@@ -49,9 +49,14 @@ inline int tile_rows(int64_t rows, int64_t head_dim, bool f32)
 // The same for k_attn_rows, whose four waves take a tile of 32 rows each, or two (fp32, head_dim up to 64).  With the
 // registers of fp32 queries, or of head_dim past 128, a wave is alone on its SIMD; otherwise two workgroups share a CU,
 // which beat one of eight waves that convert the keys once (bf16, 4 x 200 rows of 8 on up to 9000 keys: 262 us, 280).
+// k_attn_stream and k_attn_rows, us, trees of 4 (16) sequences on 2000 keys: bf16, 8 kv heads of 128: 32 rows: 18, 23
+// (30, 36); 64: 21, 21 (40, 39); 96: 26, 22 (56, 40).  fp32, whose second term of queries k_attn_stream forms products of for
+// every 16 rows, 32 kv heads of 100: 32 rows: 52, 53 (159, 167); 48: 77, 54 (289, 169); 96: 137, 58 (444, 191).
+constexpr int64_t kMaskedRows = 64, kMaskedRowsF32 = 32;
+
 inline int masked_rows(int64_t rows, int64_t head_dim, bool f32)
 {
-    if (rows <= kStreamRows) return 16;
+    if (rows <= (f32 ? kMaskedRowsF32 : kMaskedRows)) return 16;
     return rows > 128 && f32 && head_dim <= 64 ? 256 : 128;
 }
 inline bool masked_alone(int dc, bool f32) { return f32 || dc == 4; }
@@ -66,7 +71,9 @@ struct AttnCut {
 // wave (of k_attn_stream, whose waves take blocks in turn) or workgroup (of
 // k_attn_tile) costs its blocks and about four more for its start and end; waves
 // that join their sums cost half a block, a part's sums on their way through memory
-// 'part', and the join itself, where there would be none (joined), four blocks.
+// 'part', and the join itself, where there would be none (joined), four blocks (with
+// a window or a tree and few rows two: a query token of 64 heads and 8 kv heads in a
+// window of 1000 keys: 13 us in parts, 17 in one; 32 heads of 100, fp32: 17, 35).
 // waves: those of k_attn_stream, 0 for any; others: workgroups of the same launch.
 // 2^20 workgroups are a thousand rounds of the card, which no split makes shorter: no
 // more parts than that asks for, so that workgroups are numbered in 31 bits.
@@ -88,7 +95,7 @@ inline AttnCut choose_cut(int64_t wgs, int64_t blocks, int rows, int64_t head_di
             const int64_t c = div_up(blocks, s), n = div_up(blocks, c);
             const int64_t cost =
                 8 * div_up(wgs * n + others, slots) * ((stream ? div_up(c, w) : c) + 4) +
-                (stream && w > 1 ? 4 : 0) + (n > 1 || joined ? n * part : 0) + (n > 1 && !joined ? 32 : 0);
+                (stream && w > 1 ? 4 : 0) + (n > 1 || joined ? n * part : 0) + (n > 1 && !joined ? (masked && stream ? 16 : 32) : 0);
             if (least < 0 || cost < least) {
                 least = cost;
                 best = AttnCut{static_cast<int>(c), static_cast<int>(n), w};
