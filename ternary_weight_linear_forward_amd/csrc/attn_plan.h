@@ -61,6 +61,9 @@ inline int masked_rows(int64_t rows, int64_t head_dim, bool f32)
 }
 inline bool masked_alone(int dc, bool f32) { return f32 || dc == 4; }
 
+// Parts of a row's keys at most.
+constexpr int64_t kMostParts = 64;
+
 // How 'wgs' workgroups' passes over 'blocks' key blocks are split: blocks of a
 // part, parts, waves of a workgroup.
 struct AttnCut {
@@ -84,7 +87,7 @@ inline AttnCut choose_cut(int64_t wgs, int64_t blocks, int rows, int64_t head_di
     if (blocks == 0) return best;
     const int dc = head_dim <= 64 ? 1 : head_dim <= 128 ? 2 : 4;
     const bool stream = rows == 16;
-    const int64_t most = std::max<int64_t>(1, std::min<int64_t>(64, (int64_t(1) << 20) / wgs));
+    const int64_t most = std::max<int64_t>(1, std::min<int64_t>(kMostParts, (int64_t(1) << 20) / wgs));
     int64_t least = -1;
     for (int w = 1; w <= 8; w *= 2) {
         if (stream ? w > 4 || (waves && w != waves) : w != (masked ? 4 : rows / 32)) continue;
@@ -119,6 +122,12 @@ inline int64_t attn_window_blocks(int64_t prefix, int64_t max_own, int64_t queri
     const int64_t head = sinks <= prefix ? div_up(sinks, ATTN_BLOCK) : nbp + div_up(sinks - prefix, ATTN_BLOCK);
     return std::min(nbp + nbo, head + div_up(window + queries - 1, ATTN_BLOCK) + 2);
 }
+
+// Blocks of a part at most, with a tree and many rows: sequences differ in length, and the longest one's workgroups
+// work alone at the end of a cut that takes all for as long as that.  8 kv heads of 128, bf16, us without and with this:
+// 16 x 25 tokens of 64 heads on up to 9000 keys of uneven lengths 163, 125, of equal ones 208, 224; 8 x 64: 167, 129,
+// and 199, 212; 4 x 200: 257, 256, and 330, 331.  (Past four rounds of the card the workgroups even themselves out.)
+constexpr int64_t kTreeBlocks = 48;
 
 // masked: with k_attn_rows in k_attn_tile's place.  window > 0: with a sliding window and 'sinks' first tokens.  A sequence's own
 // workgroups then go over what they see of the prefix (its keys lie in at most a window,
@@ -162,6 +171,13 @@ inline AttnPlan attn_plan(int64_t tokens, int64_t heads, int64_t kv_heads, int64
                    : (p.joint ? nbp : 0) + nbo;
     cut = choose_cut(busy, blocks_own, p.rows_own, head_dim,
                      p.together ? p.waves_prefix : 0, p.together ? p.wgs_prefix : 0, part, tp > 0, masked, f32);
+    if (masked && window == 0 && p.rows_own != 16 && busy <= 1024) {
+        const int64_t parts = std::min<int64_t>(div_up(blocks_own, kTreeBlocks), kMostParts);
+        if (parts > cut.splits) {
+            cut.chunk = static_cast<int>(div_up(blocks_own, parts));
+            cut.splits = static_cast<int>(div_up(blocks_own, cut.chunk));
+        }
+    }
     p.chunk_own = cut.chunk;
     p.splits_own = cut.splits;
     p.waves_own = cut.waves;
