@@ -7,6 +7,9 @@
 // each of which finds its sequence by halving.  A sequence gets its pages iff the pages
 // asked for up to it are no more than there are, so those that are granted are the first
 // of all that are asked for: page p of them is the p-th from the top of the stack.
+// Bound: latency, a chain of loads, sums over the waves and searches in LDS: 16 sequences of a token 5.1 us, 300 that
+// take and give 13000 tokens 10.4 and 4.1 us.  One workgroup: sums across several would cost a second launch, which is
+// as long as this one takes.
 #include "common.h"
 #include "launch.h"
 

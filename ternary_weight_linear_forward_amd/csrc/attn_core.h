@@ -1,7 +1,8 @@
 // attn_core.h -- the kernels of attention over the int8 cache, for a batch of
 // sequences that share a prefix: causal (attention.hip), with a sliding window, or
-// with a tree of drafted tokens (attn_masked.hip).  o = softmax(scale q k^T) v over the prefix's keys and the
-// sequence's own, in one pass with a running maximum m and sum l:
+// with a tree of drafted tokens (attn_masked.hip, whose own kernel takes many rows).
+// o = softmax(scale q k^T) v over the prefix's keys and the sequence's own, in one
+// pass with a running maximum m and sum l:
 //   m' = max(m, s),  l' = l e^(m - m') + e^(s - m'),  o' = o e^(m - m') + e^(s - m') v.
 //
 // The keys are cut into parts.  A part's rows are the (query, head) pairs that
@@ -550,6 +551,8 @@ __device__ __forceinline__ float max_abs8(const float (&v)[8])
 // sequences' own keys of up to 512, 1408 jobs of unequal length, the longest one (31
 // us for 107 MB: a wave alone takes 3 us a block).  More rows a wave (two and three
 // tiles on one conversion) need registers past 256 and came to the same.
+// With a window or a tree (MASK) the rows of a tile see different first keys and blocks
+// with gaps: 48 query tokens of 64 heads of 128 in windows of 4096 keys, 75 us for 321 MB.
 // ---------------------------------------------------------------------------
 template <int DT, int DC, int MASK>
 __global__ __launch_bounds__(256, DC == 4 ? 1 : 2) void k_attn_stream(const AttnArgs a, const AttnPlan pl)
@@ -631,8 +634,9 @@ __global__ __launch_bounds__(256, DC == 4 ? 1 : 2) void k_attn_stream(const Attn
 
     f4 o[DTILES];
     // m: the row's reference in base 2 (0 until it is set), have: its largest weight so far
-    // (what this lane saw of it), ref: the power of two of the V_scales that the row sees (a row sees
-    // what the rows before it see: where the first one's is set, all are)
+    // (what this lane saw of it), ref: the power of two of the V_scales that the row sees (causal: a row sees
+    // what the rows before it see, so that where the first one's is set, all are; with a window or a tree a
+    // row without one has not met a key, and asks for the general form when it does)
     float m = 0.0f, l = 0.0f, have = 0.0f, ref = 0.0f, vscale = 0.0f;
     bool set = false;
 #pragma unroll

@@ -206,6 +206,9 @@ __global__ __launch_bounds__(256) void k_cache_read(const CacheView c, const Cac
 // has 1 << shift lanes, one a move, at a row of V (a byte of each of Dp rows of 64: the moves' tokens lie in one or two
 // blocks as a rule, so that neighbouring lanes meet the same line), and a thread eight rows, whose loads are in flight
 // together.  Only a move's own bytes are written: the others of a row may be another group's.
+// Bound: latency for a few drafts (8 x 5 moves x 8 heads of 128: 3.8 us), then the lines of V that single bytes are
+// taken from and put into, 64 bytes for up to 13 each way (176 x 13 moves x 32 heads of 100: 28 us; by way of LDS, with a
+// division and an address a byte: 50 us).
 constexpr int MOVE_ROWS = 8;
 __global__ __launch_bounds__(256) void k_cache_move(const CacheView c, const int64_t *src, const int64_t *dst, int width,
                                                     int shift)
