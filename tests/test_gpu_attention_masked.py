@@ -364,6 +364,53 @@ def test_graph_and_stream(which):
     assert torch.equal(got, want)
 
 
+@pytest.mark.parametrize("G,n,dtype", [(8, 8, "bf16"), (8, 9, "bf16"), (4, 8, "f32"), (4, 9, "f32")])
+def test_parts_of_uneven_sequences(G, n, dtype):
+    """The most rows of a short tile and the fewest of a long one, on sequences of which some have none of the keys, some
+    none of the tokens, of a split's later parts."""
+    own, nq = [6500, 70, 0, 2100, n, 3], [n, n - 1, n, 0, n, n]
+    st = Setup(2, 64, 128, 0, own, seed=n)
+    rng = np.random.default_rng(n)
+    trees = [grown_tree(rng, k) for k in nq]
+    qt, q = queries(sum(nq), 2 * G, 64, 4, dtype)
+    o, lse = call(st, qt, nq, entry=bl.attention_tree, tree=to_dev(words(trees, n)))
+    compare(o, lse, reference(st, q, nq, lambda b: tree_sight(0, own[b], nq[b], trees[b]), 64 ** -0.5, dtype))
+    o, lse = call(st, qt, nq, entry=bl.attention_window, window=2500, sinks=65)
+    compare(o, lse, reference(st, q, nq, lambda b: window_sight(0, own[b], nq[b], 2500, 65), 64 ** -0.5, dtype))
+
+
+@pytest.mark.parametrize("n,dtype", [(3, "bf16"), (40, "bf16"), (40, "f32")])
+def test_graphs_that_share_a_workspace(n, dtype):
+    """Two captured calls with the same workspace, replayed in turn with eager calls between them."""
+    st = Setup(1, 128, 64, 0, [6500, 900], seed=n)
+    cache, table, ln = st.cache(), to_dev(st.table), to_dev(np.array(st.own, np.int32))
+    mask = to_dev(words([grown_tree(np.random.default_rng(b), n) for b in range(2)], n))
+    q, start = queries(2 * n, 8, 128, 5, dtype)[0], to_dev(np.array([0, n, 2 * n], np.int32))
+    nws = max(bl.bitlinear_attention_window_workspace_bytes(2 * n, 8, 1, 128, 2, n, 6500, 0, 4000, 9),
+              bl.bitlinear_attention_tree_workspace_bytes(2 * n, 8, 1, 128, 2, n, 6500, 0))
+    assert nws > 0
+    ws = torch.full((nws,), 255, dtype=torch.uint8, device="cuda")
+    kw = dict(q_start=start, max_q=n)
+    calls = [lambda **more: bl.attention_tree(cache, q, table, ln, 6500, mask, **kw, **more),
+             lambda **more: bl.attention_window(cache, q, table, ln, 6500, 4000, 9, **kw, **more)]
+    wants = [c() for c in calls]
+    outs = [torch.zeros_like(q) for _ in calls]
+    for c, out in zip(calls, outs):
+        c(out=out, ws=ws)
+    torch.cuda.synchronize()
+    graphs = []
+    for c, out in zip(calls, outs):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            c(out=out, ws=ws)
+    for r in range(6):
+        outs[r % 2].zero_()
+        graphs[r % 2].replay()
+        calls[1 - r % 2](ws=ws)
+        torch.cuda.synchronize()
+        assert torch.equal(outs[r % 2], wants[r % 2]), r
+
+
 def test_a_step_of_drafts():
     """The operators together, as a step of drafts uses them: places for the drafts, their keys and values, attention of
     the tree and of a layer with a window; then a path is accepted, its keys move together, the rest goes back, and the
