@@ -302,9 +302,22 @@ __device__ __forceinline__ bool attn_job(const AttnArgs &a, const AttnPlan &pl, 
     int r = wg - pl.wgs_prefix;
     j.kvh = r % a.c.heads;
     r /= a.c.heads;
-    const int s = r % pl.splits_own;
-    r /= pl.splits_own;
-    const int tile = r % pl.tiles_own, b = r / pl.tiles_own;
+    int s, tile, b;
+    if constexpr (MASK == ATTN_CAUSAL) {
+        s = r % pl.splits_own;
+        r /= pl.splits_own;
+        tile = r % pl.tiles_own;
+        b = r / pl.tiles_own;
+    } else {
+        // Workgroups go to the XCDs, and to the groups of CUs in one, by turns.  With the part as the fastest of these
+        // numbers a group got the same part of every sequence where their counts had a factor in common, and groups
+        // whose part no shorter sequence has stood idle (4 x 200 tokens of 64 heads on up to 9000 keys, parts of 36 blocks: 259 us, 199 so).  First parts, which all have,
+        // come first.
+        tile = r % pl.tiles_own;
+        r /= pl.tiles_own;
+        b = r % a.seqs;
+        s = r / a.seqs;
+    }
     int first = b * a.max_q, n = a.max_q;
     if (a.q_start) {
         first = a.q_start[b];
