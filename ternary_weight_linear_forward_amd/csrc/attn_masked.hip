@@ -31,7 +31,7 @@ namespace bl {
 // binary16) passes a bound that no weight of it can pass alone.  They are not in the sums
 // yet: the row gets a new M, its sums are brought to it and the half's weights are formed
 // again (raise).  So the time hardly depends on the scores: 4 x 200 tokens of 64 heads on up
-// to 9000 keys at 1.6, 3, 6 and 13 nats of standard deviation: 260, 266, 301, 344 us.
+// to 9000 keys at 1.6, 3, 6 and 13 nats of standard deviation: 223, 219, 234, 254 us.
 //
 // Bound: vector instructions.  A wave's block of 64 keys x 32 rows takes some 400 issue
 // slots of four cycles (112 and 32 exponentials at a quarter of the rate for the weights, 90

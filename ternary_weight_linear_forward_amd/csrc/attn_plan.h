@@ -125,8 +125,8 @@ inline int64_t attn_window_blocks(int64_t prefix, int64_t max_own, int64_t queri
 
 // Blocks of a part at most, with a tree and many rows: sequences differ in length, and the longest one's workgroups
 // work alone at the end of a cut that takes all for as long as that.  8 kv heads of 128, bf16, us without and with this:
-// 16 x 25 tokens of 64 heads on up to 9000 keys of uneven lengths 163, 125, of equal ones 208, 224; 8 x 64: 167, 129,
-// and 199, 212; 4 x 200: 257, 256, and 330, 331.  (Past four rounds of the card the workgroups even themselves out.)
+// 16 x 25 tokens of 64 heads on up to 9000 keys of uneven lengths 163, 123, of equal ones 215, 234; 8 x 64: 166, 127,
+// and 203, 214; 4 x 200: 205, 200, and 335, 345.  (Past four rounds of the card the workgroups even themselves out.)
 constexpr int64_t kTreeBlocks = 48;
 
 // masked: with k_attn_rows in k_attn_tile's place.  window > 0: with a sliding window and 'sinks' first tokens.  A sequence's own
