@@ -307,11 +307,11 @@ __global__ __launch_bounds__(256, rows_waves(DT, DC, RT)) void k_attn_rows(const
         lds2(vst + to + (4 * half * DPAD + 64 * u) * 16) = make_uint2(x[0], x[1]);
         lds2(vst + to + ((4 * half + 2) * DPAD + 64 * u) * 16) = make_uint2(x[2], x[3]);
     };
-    // (a hidden score is -inf: never times 0.  A V_scale that is not finite counts as the largest number: its key's
-    // weight is 0 where it is hidden)
+    // (a hidden score is -inf: never times 0.  A V_scale that is not finite counts as the largest number of its sign:
+    // its key's weight is 0 where it is hidden)
     auto stage_scales = [&](int n) {
         if (wave == 0) {
-            const float v = fminf(vsr, 3.402823466e38f);
+            const float v = fmaxf(fminf(vsr, 3.402823466e38f), -3.402823466e38f);
             lds1(4 * lane + scales_at(n)) = fmaxf(DT == DT_BF16 ? ksr * c[0] : ksr, 1.17549435e-38f);
             lds1(4 * lane + scales_at(n) + 256) = v;
             if constexpr (DT == DT_BF16) {
