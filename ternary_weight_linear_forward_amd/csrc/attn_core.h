@@ -1026,8 +1026,8 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(const AttnArgs a, cons
         grow = 1.0f;
         ksr = lane < seen ? ksr : 0.0f;
         vsr = lane < seen ? vsr : 0.0f;
-        // A V_scale that is not finite leaves the reference as it is and counts as the largest number: its
-        // key's weight overflows where a row sees it and is 0 where it is hidden.
+        // A V_scale that is not finite leaves the reference as it is and counts as the largest number of its
+        // sign: its key's weight overflows where a row sees it and is 0 where it is hidden.
         if (__any(vsr > ref)) {
             const float ref2 = fmaxf(pow2_above(wave_max_nonneg(vsr < __builtin_inff() ? vsr : 0.0f)), ref);
             grow = ref / ref2;
@@ -1036,7 +1036,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(const AttnArgs a, cons
         }
         if (wave == 0) {
             to[lane] = fmaxf(ksr * c, 1.17549435e-38f); // (a masked score is -inf: never times 0)
-            to[64 + lane] = fminf(vsr * vscale, 3.402823466e38f);
+            to[64 + lane] = fmaxf(fminf(vsr * vscale, 3.402823466e38f), -3.402823466e38f);
         }
     };
     constexpr int STAGE_STEPS = 4 * UNITS + 1;
