@@ -696,8 +696,10 @@ int bitlinear_attention(const bitlinear_cache_t *cache, const void *Q, int dtype
  * entries: such entries may hold anything.  Each sequence reads what it sees of the
  * prefix by itself.  Here and in bitlinear_attention_tree, calls of many query rows
  * round a weight p * V_scale to 11 bits or to 2^-27 of the row's largest, whichever is
- * more (BF16), and carry 24 bits (F32); V_scales are finite and not negative.  The other arguments, their bounds and the results are those of
- * bitlinear_attention, ws of bitlinear_attention_window_workspace_bytes bytes.
+ * more (BF16), and carry 24 bits (F32); the V_scales of keys that a query sees are then
+ * in [0, 2^96] (those of others may be anything).  The other arguments, their bounds and
+ * the results are those of bitlinear_attention, ws of
+ * bitlinear_attention_window_workspace_bytes bytes.
  */
 int64_t bitlinear_attention_window_workspace_bytes(int64_t tokens, int64_t heads, int64_t kv_heads, int64_t head_dim,
                                                    int64_t seqs, int64_t max_q, int64_t max_own, int64_t prefix_len,

@@ -27,6 +27,9 @@ namespace bl {
 //  - fp32 queries: three bf16 terms, 24 bits, in binary32's range; M is the largest x.
 //  - bf16 queries: one binary16 term, 11 bits.  M brings the largest weight so far to
 //    2^FIRST_TOP: those that are 2^16 times smaller lose bits, all below 2^-27 of it are lost.
+//    M so follows p V_scale, and is far below the scores where values are small or zero: down to
+//    LEAST_BELOW of them, where a value's share of the row is at the end of binary32's range.
+//    The sum of p is then held in units that are 2^LOW_BITS larger (low).
 // A half's weights have outgrown M when their sum (times the block's largest V_scale for
 // binary16) passes a bound that no weight of it can pass alone.  They are not in the sums
 // yet: the row gets a new M, its sums are brought to it and the half's weights are formed
@@ -44,6 +47,9 @@ typedef __bf16 b8 __attribute__((ext_vector_type(8)));
 // log2 of what a row's reference makes of the largest weight (one binary16 term); bounds of a half's sum of weights of
 // one lane: with V_scale (binary16 ends at 2^16), and without
 constexpr float FIRST_TOP = 2.0f, ROWS_WEIGHT_MAX = 0x1p15f, ROWS_SUM_MAX = 0x1p60f;
+// log2 of the largest p of a row that needs the sum's larger units, of those units, and of the largest p there may be when
+// a reference is set (16 of them and a few bits' growth stay in binary32)
+constexpr float LOW_FROM = 40.0f, LOW_BITS = 70.0f, LEAST_BELOW = 110.0f, LOW_UNIT = 0x1p-70f;
 
 // Eight int8 (two words) to bf16, exactly, by way of binary32.
 __device__ __forceinline__ u4 bytes_to_b8(uint32_t a, uint32_t b)
@@ -325,6 +331,7 @@ __global__ __launch_bounds__(256, rows_waves(DT, DC, RT)) void k_attn_rows(const
     u4 p[2][RT][2][NT];         // weights of the two halves, by 16-key tile
     float M[RT], l[RT];
     bool set[RT], settled = false; // a row's reference, all of the wave's
+    bool low[RT];                  // (bf16) l counts in units of 2^LOW_BITS
     uint64_t vis[RT];              // keys of the block the row sees
     bool hidden = false;           // the rows do not all see all of it
     // K_scales (V_scales) of keys 8 x + 4 hf .. of a half
@@ -362,8 +369,8 @@ __global__ __launch_bounds__(256, rows_waves(DT, DC, RT)) void k_attn_rows(const
             }
         }
     };
-    // The reference that a half's scores ask for.  The largest weight comes to 2^FIRST_TOP where it is binary16; sums of p
-    // stay in range where values are very small.  bf16 terms need no more than that of p.
+    // The reference that a half's scores ask for.  The largest weight comes to 2^FIRST_TOP where it is binary16; a row whose
+    // values are zero so far takes the least there is, which the first weight outgrows.  bf16 terms need no more than that of p.
     auto reference = [&](int n, int half, const f16v &sc, int t, float &top) {
         float most = neg_inf();
         top = neg_inf();
@@ -371,7 +378,7 @@ __global__ __launch_bounds__(256, rows_waves(DT, DC, RT)) void k_attn_rows(const
         top = max_across32(top);
         if constexpr (DT != DT_BF16) return top;
         most = max_across32(most);
-        return most > neg_inf() ? fmaxf(most - FIRST_TOP, top - 40.0f) : top;
+        return fmaxf(most - FIRST_TOP, top - LEAST_BELOW);
     };
     // Before a half's weights: scores a row does not see, and the reference of a row whose first keys these are (its
     // sums are still zero).
@@ -389,11 +396,14 @@ __global__ __launch_bounds__(256, rows_waves(DT, DC, RT)) void k_attn_rows(const
             const float m = reference(n, H, s[H][t], t, top);
             const bool now = !set[t] && top > neg_inf();
             M[t] = now ? m : M[t];
+            if constexpr (DT == DT_BF16) low[t] = now ? top > m + LOW_FROM : low[t];
             set[t] = set[t] || now;
             unset |= !set[t];
         }
         settled = !__any(unset);
     };
+
+    auto sum_unit = [&](int t) { return DT == DT_BF16 && low[t] ? LOW_UNIT : 1.0f; };
 
     // Sums stay in accumulation registers and scores in the others; without a word the compiler carries them to and fro
     // (64 moves a step).
@@ -448,8 +458,15 @@ __global__ __launch_bounds__(256, rows_waves(DT, DC, RT)) void k_attn_rows(const
         for (int t = 0; t < RT; ++t) {
             float top;
             const float m = fmaxf(M[t], reference(n, H, s[H][t], t, top)), f = __builtin_amdgcn_exp2f(M[t] - m);
+            if constexpr (DT == DT_BF16) {
+                // (the sum so far and this half's largest p say which units the sum takes from here on)
+                const float by = M[t] - m + (low[t] ? LOW_BITS : 0.0f);
+                low[t] = fmaxf(top - m, by + __builtin_log2f(sum_across32(l[t]))) > LOW_FROM;
+                l[t] *= __builtin_amdgcn_exp2f(by - (low[t] ? LOW_BITS : 0.0f));
+            } else {
+                l[t] *= f;
+            }
             M[t] = m;
-            l[t] *= f;
 #pragma unroll
             for (int d = 0; d < DT32; ++d)
 #pragma unroll
@@ -553,18 +570,19 @@ __global__ __launch_bounds__(256, rows_waves(DT, DC, RT)) void k_attn_rows(const
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
             const float all = sum[t][0] + sum[t][1];
-            outgrown |= all > ROWS_SUM_MAX || (DT == DT_BF16 && all * vtop > ROWS_WEIGHT_MAX);
+            if constexpr (DT == DT_BF16) outgrown |= all * sum_unit(t) > ROWS_SUM_MAX || all * vtop > ROWS_WEIGHT_MAX;
+            else outgrown |= all > ROWS_SUM_MAX;
         }
         if (__builtin_expect_with_probability(__any(outgrown), 0, 0.95)) raise(half_c, n, sum);
 #pragma unroll
-        for (int t = 0; t < RT; ++t) l[t] += sum[t][0] + sum[t][1];
+        for (int t = 0; t < RT; ++t) l[t] += (sum[t][0] + sum[t][1]) * sum_unit(t);
         place(1 - H);
     };
 
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
         M[t] = l[t] = 0.0f;
-        set[t] = false;
+        set[t] = low[t] = false;
         vis[t] = 0;
     }
 #pragma unroll
@@ -659,7 +677,8 @@ __global__ __launch_bounds__(256, rows_waves(DT, DC, RT)) void k_attn_rows(const
         const int rr = j.row0 + rho, head = j.kvh * G + rr % G;
         const int64_t tok = j.tok0 + rr / G, at = part_index(a, j.part, tok, head);
         f4 *po = reinterpret_cast<f4 *>(a.ws) + at * (Dp / 4);
-        const float f = !pl.direct ? 1.0f : (sum > 0.0f ? 1.0f / sum : 0.0f);
+        // (sums of values in the sum's units, and those units' reference)
+        const float f = sum_unit(t) * (!pl.direct ? 1.0f : (sum > 0.0f ? 1.0f / sum : 0.0f)), m = M[t] + (low[t] ? LOW_BITS : 0.0f);
 #pragma unroll
         for (int d = 0; d < DT32; ++d)
 #pragma unroll
@@ -670,8 +689,8 @@ __global__ __launch_bounds__(256, rows_waves(DT, DC, RT)) void k_attn_rows(const
                 else if (col < Dp) po[col / 4] = v;
             }
         if (hf == 0) {
-            if (!pl.direct) reinterpret_cast<float2 *>(a.ws + pl.ml_off)[at] = make_float2(set[t] ? M[t] : neg_inf(), sum);
-            else if (a.lse) a.lse[tok * a.heads + head] = lse_of(M[t], sum);
+            if (!pl.direct) reinterpret_cast<float2 *>(a.ws + pl.ml_off)[at] = make_float2(set[t] ? m : neg_inf(), sum);
+            else if (a.lse) a.lse[tok * a.heads + head] = lse_of(m, sum);
         }
     }
 }
