@@ -651,7 +651,8 @@ int bitlinear_cache_read(const bitlinear_cache_t *cache, const int64_t *slots, i
  * Scores and outputs are accumulated in binary32, softmax statistics are
  * binary32.  The prefix's keys are read once for all sequences.  A query that
  * sees no key gives o = 0 and lse = -inf.  A query row that is not finite, or a
- * key whose scales are not, reaches no other row, and no row that does not see it.
+ * key whose scales are not, reaches no other row, and no row that does not see it; a
+ * row that sees keys and holds a NaN gives o = lse = NaN.
  *   Q       [tokens x heads x head_dim], dtype F32 or BF16, head rows
  *           contiguous, strides in elements (>= 0).  BF16 rounds the softmax
  *           weights to 11 significant bits; F32 carries 22.

@@ -97,7 +97,7 @@ __global__ __launch_bounds__(256) void k_attn_join(const AttnArgs a, const AttnP
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[e] += __shfl_xor(o[e], s);
     }
-    if (lane % PER < LPR) store_result<DT>(a, tok, head, col, o * (l > 0.0f ? 1.0f / l : 0.0f));
+    if (lane % PER < LPR) store_result<DT>(a, tok, head, col, o * inverse_of(l));
     if (a.lse && lane % PER == 0) a.lse[tok * a.heads + head] = lse_of(top, l);
 }
 

@@ -454,8 +454,15 @@ __device__ __forceinline__ void store_result(const AttnArgs &a, int64_t tok, int
         }
 }
 
-// log(sum e^s) from a base-2 reference and sum.
-__device__ __forceinline__ float lse_of(float m, float l) { return l > 0.0f ? (m + log2f(l)) * ATTN_LN2 : neg_inf(); }
+// log(sum e^s) from a base-2 reference and sum; and what sums of values are multiplied with.  A row that sees no key
+// (l = 0) gives -inf and 0, one with a NaN query (l is NaN, as no score made a reference) NaN.
+__device__ __forceinline__ float lse_of(float m, float l)
+{
+    return l > 0.0f ? (m + log2f(l)) * ATTN_LN2 : l == 0.0f ? neg_inf() : l;
+}
+__device__ __forceinline__ float inverse_of(float l) { return l > 0.0f ? 1.0f / l : l; }
+// A part's reference: -inf, which the join skips, where the row has met no key.
+__device__ __forceinline__ float part_reference(float m, float l, bool set) { return set || l != l ? m : neg_inf(); }
 
 // Where 64 blocks of a job lie, lane x holding block first + step x: the number of
 // the block among all blocks of the cache (page, head and place in the page), 0 for a
@@ -836,7 +843,7 @@ __global__ __launch_bounds__(256, DC == 4 ? 1 : 2) void k_attn_stream(const Attn
     float2 *pml = reinterpret_cast<float2 *>(a.ws + pl.ml_off);
     float *ml = lds + waves * 16 * DPAD, *ll = ml + waves * 16, *sums = ll + waves * 16; // l of the rows
     l = sum_across32(sum_across16(l));
-    m = set ? m : neg_inf();
+    m = part_reference(m, l, set);
     if (g == 0) {
         ml[wave * 16 + i] = m;
         ll[wave * 16 + i] = l;
@@ -874,7 +881,7 @@ __global__ __launch_bounds__(256, DC == 4 ? 1 : 2) void k_attn_stream(const Attn
         for (int w = 0; w < waves; ++w) sum += *reinterpret_cast<const f4 *>(lds + (w * 16 + rho) * DPAD + 4 * d4);
         const int64_t tok = j.tok0 + rr / G;
         const int head = j.kvh * G + rr % G;
-        if (pl.direct) store_result<DT>(a, tok, head, 4 * d4, sum * (sums[rho] > 0.0f ? 1.0f / sums[rho] : 0.0f));
+        if (pl.direct) store_result<DT>(a, tok, head, 4 * d4, sum * inverse_of(sums[rho]));
         else po[part_index(a, j.part, tok, head) * (Dp / 4) + d4] = sum;
     }
 }
@@ -1335,7 +1342,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(const AttnArgs a, cons
         const int rr = j.row0 + rho, head = j.kvh * G + rr % G;
         const int64_t tok = j.tok0 + rr / G, at = part_index(a, j.part, tok, head);
         f4 *po = reinterpret_cast<f4 *>(a.ws) + at * (Dp / 4);
-        const float f = ref / WR::PSCALE * (!pl.direct ? 1.0f : (l > 0.0f ? 1.0f / l : 0.0f));
+        const float f = ref / WR::PSCALE * (!pl.direct ? 1.0f : inverse_of(l));
 #pragma unroll
         for (int d = 0; d < DT32; ++d)
 #pragma unroll
@@ -1346,7 +1353,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(const AttnArgs a, cons
                 else if (col < Dp) po[col / 4] = v;
             }
         if (hf == 0) {
-            if (!pl.direct) reinterpret_cast<float2 *>(a.ws + pl.ml_off)[at] = make_float2(set ? m : neg_inf(), l);
+            if (!pl.direct) reinterpret_cast<float2 *>(a.ws + pl.ml_off)[at] = make_float2(part_reference(m, l, set), l);
             else if (a.lse) a.lse[tok * a.heads + head] = lse_of(m, l);
         }
     }

@@ -398,7 +398,7 @@ __global__ __launch_bounds__(256, rows_waves(DT, DC, RT)) void k_attn_rows(const
             M[t] = now ? m : M[t];
             if constexpr (DT == DT_BF16) low[t] = now ? top > m + LOW_FROM : low[t];
             set[t] = set[t] || now;
-            unset |= !set[t];
+            unset |= !set[t] && l[t] == l[t]; // (one with a NaN query never gets any)
         }
         settled = !__any(unset);
     };
@@ -678,7 +678,7 @@ __global__ __launch_bounds__(256, rows_waves(DT, DC, RT)) void k_attn_rows(const
         const int64_t tok = j.tok0 + rr / G, at = part_index(a, j.part, tok, head);
         f4 *po = reinterpret_cast<f4 *>(a.ws) + at * (Dp / 4);
         // (sums of values in the sum's units, and those units' reference)
-        const float f = sum_unit(t) * (!pl.direct ? 1.0f : (sum > 0.0f ? 1.0f / sum : 0.0f)), m = M[t] + (low[t] ? LOW_BITS : 0.0f);
+        const float f = sum_unit(t) * (!pl.direct ? 1.0f : inverse_of(sum)), m = M[t] + (low[t] ? LOW_BITS : 0.0f);
 #pragma unroll
         for (int d = 0; d < DT32; ++d)
 #pragma unroll
@@ -689,7 +689,7 @@ __global__ __launch_bounds__(256, rows_waves(DT, DC, RT)) void k_attn_rows(const
                 else if (col < Dp) po[col / 4] = v;
             }
         if (hf == 0) {
-            if (!pl.direct) reinterpret_cast<float2 *>(a.ws + pl.ml_off)[at] = make_float2(set[t] ? m : neg_inf(), sum);
+            if (!pl.direct) reinterpret_cast<float2 *>(a.ws + pl.ml_off)[at] = make_float2(part_reference(m, sum, set[t]), sum);
             else if (a.lse) a.lse[tok * a.heads + head] = lse_of(m, sum);
         }
     }
