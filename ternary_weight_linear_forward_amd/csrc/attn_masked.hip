@@ -19,8 +19,9 @@ namespace bl {
 // weights behind every operand.  One barrier a step; K lies in LDS by halves, V by
 // blocks, two of each.
 //
-// The first product is bf16 for bf16 queries, which takes the queries as they are and
-// the bytes exactly, and binary16 in two terms for fp32 queries (brought into its range
+// The first product is bf16 for bf16 queries, which takes the queries as they are (below a
+// scale of SMALL_SCALE times 2^-64, as their products with the keys could pass binary32's range
+// where their scores do not) and the bytes exactly, and binary16 in two terms for fp32 queries (brought into its range
 // by a power of two per row).  Weights are w = 2^(x - M) V_scale, M a reference in base 2
 // that a row gets with its first keys (the first 32 of which it sees some) and keeps until
 // its weights outgrow it, so that few steps touch its sums:
@@ -44,6 +45,8 @@ namespace bl {
 // a job's start (queries, first blocks) takes 15 % of that.
 // ---------------------------------------------------------------------------
 typedef __bf16 b8 __attribute__((ext_vector_type(8)));
+constexpr float SMALL_SCALE = 0x1p-60f;
+constexpr int SMALL_SCALE_E2 = -64;
 // log2 of what a row's reference makes of the largest weight (one binary16 term); bounds of a half's sum of weights of
 // one lane: with V_scale (binary16 ends at 2^16), and without
 constexpr float FIRST_TOP = 2.0f, ROWS_WEIGHT_MAX = 0x1p15f, ROWS_SUM_MAX = 0x1p60f;
@@ -268,14 +271,16 @@ __global__ __launch_bounds__(256, rows_waves(DT, DC, RT)) void k_attn_rows(const
         float v[KSTEPS][8];
         load_queries<DT>(a, off, [&](int n) { return 16 * n + 8 * hf; }, v);
         if constexpr (DT == DT_BF16) {
-            c[t] = row_factor(a.scale, 0);
-            const uint32_t sign = a.scale < 0.0f ? 0x80008000u : 0u, keep = a.scale == 0.0f ? 0u : ~0u;
+            // (powers of two, so that the products are exact bf16 numbers)
+            const int e2 = fabsf(a.scale) < SMALL_SCALE ? SMALL_SCALE_E2 : 0;
+            const float by = a.scale == 0.0f ? 0.0f : __builtin_copysignf(e2 ? __builtin_ldexpf(1.0f, SMALL_SCALE_E2) : 1.0f, a.scale);
+            c[t] = row_factor(a.scale, e2);
 #pragma unroll
             for (int k = 0; k < KSTEPS; ++k)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    q[t][k][0][e] = (__builtin_amdgcn_perm(__float_as_uint(v[k][2 * e + 1]), __float_as_uint(v[k][2 * e]),
-                                                           0x07060302u) ^ sign) & keep;
+                    q[t][k][0][e] = __builtin_amdgcn_perm(__float_as_uint(v[k][2 * e + 1] * by), __float_as_uint(v[k][2 * e] * by),
+                                                          0x07060302u);
         } else {
             float top = 0.0f;
 #pragma unroll
