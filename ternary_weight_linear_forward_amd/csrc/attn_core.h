@@ -419,8 +419,8 @@ struct TileSight {
     // Whether they see the whole block that starts with key k0 of the prefix (pre) or of the sequence's own.
     __device__ __forceinline__ bool whole(const AttnArgs &a, const AttnJob &j, bool pre, int k0) const
     {
-        const int pos = pre ? k0 : j.prefix + k0;
-        return k0 + CACHE_BLOCK <= (pre ? j.prefix : own) && (pos >= from || pos + CACHE_BLOCK <= a.sinks);
+        const int pos = pre ? k0 : j.prefix + k0; // (at most 2^31 - 64)
+        return k0 + CACHE_BLOCK <= (pre ? j.prefix : own) && (pos >= from || pos <= a.sinks - CACHE_BLOCK);
     }
 };
 
