@@ -472,7 +472,7 @@ int bitlinear_cache_assign(int64_t seqs, int64_t page_tokens, const int32_t *hel
         for (int k = 0; k < i; ++k)
             if (overlap(out[i], out[k])) return BITLINEAR_ERR_INVALID_ARG;
         for (int k = 0; k < 3; ++k)
-            if (overlap(out[i], in[k]) && !(i == k && out[i].lo == in[k].lo)) return BITLINEAR_ERR_INVALID_ARG;
+            if (overlap(out[i], in[k]) && !(i == k && i < 2 && out[i].lo == in[k].lo)) return BITLINEAR_ERR_INVALID_ARG;
     }
     bl::AssignArgs a;
     a.held = held;
