@@ -98,6 +98,9 @@ bool window_ok(int64_t window, int64_t sinks)
     return window >= 1 && window <= (int64_t(1) << 31) && sinks >= 0 && sinks <= kMaxKeys;
 }
 
+// Words of a query token's row of a tree.
+int64_t tree_words(int64_t max_q, int64_t tokens) { return (std::min(max_q, tokens) + 63) / 64; }
+
 // Which keys a row sees beside the causal limit: a window, or a tree.
 struct Sight {
     int64_t window = 0, sinks = 0;
@@ -141,7 +144,7 @@ int attention_call(const Sight &sight, const bitlinear_cache_t *cache, const voi
                        no > 0 ? span_of(own_pages, seqs, ld_pages, no, 4) : Span{0, 0},
                        span_of(own_len, 1, seqs, seqs, 4),
                        np > 0 ? span_of(prefix_pages, 1, np, np, 4) : Span{0, 0},
-                       sight.tree ? span_of(sight.tree, tokens, sight.ld_tree, sight.ld_tree, 8) : Span{0, 0},
+                       sight.tree ? span_of(sight.tree, tokens, sight.ld_tree, tree_words(max_q, tokens), 8) : Span{0, 0},
                        cs.s[0], cs.s[1], cs.s[2], cs.s[3]};
     for (const Span &s : in)
         if (overlap(so, s) || overlap(sl, s) || overlap(sw, s)) return BITLINEAR_ERR_INVALID_ARG;
@@ -174,7 +177,6 @@ int attention_call(const Sight &sight, const bitlinear_cache_t *cache, const voi
     (void)hipGetLastError();
     return status_of(bl::launch_attention(a, as_stream(stream)));
 }
-
 
 } // namespace
 
@@ -426,7 +428,7 @@ int bitlinear_attention_tree(const bitlinear_cache_t *cache, const void *Q, int 
                              int64_t ws_bytes, void *stream)
 {
     if (!tree || !aligned_to(tree, 8) || tokens < 1 || tokens > kMaxQueries || max_q < 1 || ld_tree < 1 ||
-        ld_tree < (std::min(max_q, tokens) + 63) / 64 || !stride_ok(tokens, ld_tree))
+        ld_tree < tree_words(max_q, tokens) || !stride_ok(tokens, ld_tree))
         return BITLINEAR_ERR_INVALID_ARG;
     Sight s;
     s.tree = tree;
