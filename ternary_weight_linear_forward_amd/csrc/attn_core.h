@@ -311,8 +311,8 @@ __device__ __forceinline__ bool attn_job(const AttnArgs &a, const AttnPlan &pl, 
     } else {
         // Workgroups go to the XCDs, and to the groups of CUs in one, by turns.  With the part as the fastest of these
         // numbers a group got the same part of every sequence where their counts had a factor in common, and groups
-        // whose part no shorter sequence has stood idle (4 x 200 tokens of 64 heads on up to 9000 keys, parts of 36 blocks: 259 us, 199 so).  First parts, which all have,
-        // come first.
+        // whose part no shorter sequence has stood idle (4 x 200 tokens of 64 heads on up to 9000 keys, parts of 36
+        // blocks: 259 us, 199 so).  First parts, which all have, come first.
         tile = r % pl.tiles_own;
         r /= pl.tiles_own;
         b = r % a.seqs;
@@ -572,7 +572,7 @@ __device__ __forceinline__ float max_abs8(const float (&v)[8])
 // us for 107 MB: a wave alone takes 3 us a block).  More rows a wave (two and three
 // tiles on one conversion) need registers past 256 and came to the same.
 // With a window or a tree (MASK) the rows of a tile see different first keys and blocks
-// with gaps: 48 query tokens of 64 heads of 128 in windows of 4096 keys, 75 us for 321 MB.
+// with gaps: 48 query tokens of 64 heads of 128 in windows of 4096 keys, 74 us for 321 MB.
 // ---------------------------------------------------------------------------
 template <int DT, int DC, int MASK>
 __global__ __launch_bounds__(256, DC == 4 ? 1 : 2) void k_attn_stream(const AttnArgs a, const AttnPlan pl)

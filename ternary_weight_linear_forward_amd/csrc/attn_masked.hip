@@ -21,11 +21,12 @@ namespace bl {
 //
 // The first product is bf16 for bf16 queries, which takes the queries as they are (below a
 // scale of SMALL_SCALE times 2^-64, as their products with the keys could pass binary32's range
-// where their scores do not) and the bytes exactly, and binary16 in two terms for fp32 queries (brought into its range
-// by a power of two per row).  Weights are w = 2^(x - M) V_scale, M a reference in base 2
+// where their scores do not) and the bytes exactly, and binary16 in two terms for fp32 queries
+// (brought into its range by a power of two per row).  Weights are w = 2^(x - M) V_scale, M a reference in base 2
 // that a row gets with its first keys (the first 32 of which it sees some) and keeps until
 // its weights outgrow it, so that few steps touch its sums:
-//  - fp32 queries: three bf16 terms, 24 bits, in binary32's range; M is the largest x.
+//  - fp32 queries: three bf16 terms, 24 bits, in binary32's range; M is the largest
+//    x of those keys.
 //  - bf16 queries: one binary16 term, 11 bits.  M brings the largest weight so far to
 //    2^FIRST_TOP: those that are 2^16 times smaller lose bits, all below 2^-27 of it are lost.
 //    M so follows p V_scale, and is far below the scores where values are small or zero: down to
@@ -34,15 +35,16 @@ namespace bl {
 // A half's weights have outgrown M when their sum (times the block's largest V_scale for
 // binary16) passes a bound that no weight of it can pass alone.  They are not in the sums
 // yet: the row gets a new M, its sums are brought to it and the half's weights are formed
-// again (raise).  So the time hardly depends on the scores: 4 x 200 tokens of 64 heads on up
-// to 9000 keys at 1.6, 3, 6 and 13 nats of standard deviation: 223, 219, 234, 254 us.
+// again (raise).  So the time depends little on the scores: 4 x 200 tokens of 64 heads on up
+// to 9000 keys at 1.6, 3, 6 and 13 nats of standard deviation: 192, 199, 225, 256 us.
 //
 // Bound: vector instructions.  A wave's block of 64 keys x 32 rows takes some 400 issue
 // slots of four cycles (112 and 32 exponentials at a quarter of the rate for the weights, 90
 // to convert and stage its share of K and V, the rest addresses, LDS and scalar work) beside
-// 32 products of 33: 3200 of the 4370 cycles measured for two waves, matrix cores 41 % busy.
-// 2 x 4096 tokens x 64 heads of 128 in a window of 1024: 441 us, 48 % of the products' rate;
-// a job's start (queries, first blocks) takes 15 % of that.
+// 32 products of 33: 3200 of the 4370 cycles measured for two waves, in which matrix cores are
+// busy for 48 %.  2 x 4096 tokens x 64 heads of 128 in a window of 1024: 385 us (448 in the first
+// launches after an idle time), 55 % of a large matrix product's rate; counters over the whole
+// kernel have matrix cores 35 % busy, since a job's start (queries, first blocks) takes 15 %.
 // ---------------------------------------------------------------------------
 typedef __bf16 b8 __attribute__((ext_vector_type(8)));
 constexpr float SMALL_SCALE = 0x1p-60f;
